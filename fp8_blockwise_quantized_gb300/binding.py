@@ -31,7 +31,9 @@ EXPORTED = ["gmm_status_string", "gmm_last_cuda_error", "gmm_workspace_bytes", "
             "gmm_bf16_fwd", "tgmm_bf16", "gmm_get_device_status", "gmm_fp8_fwd_noalloc",
             "gmm_bf16_dgrad", "gmm_fp8_fwd_swiglu_quant", "gmm_selftest_wait_timeout", "gmm_fp8_fwd_tiled",
             "gmm_fp8_fwd_swiglu_quant_tiled", "gmm_quantize_rhs_w4", "gmm_fp8_w4_fwd",
-            "gmm_fp8_w4_fwd_swiglu_quant", "tgmm_bf16_tiled"]
+            "gmm_fp8_w4_fwd_swiglu_quant", "tgmm_bf16_tiled", "gmm_bf16_swiglu_fwd", "gmm_bf16_swiglu_bwd",
+            "tgmm_fp8_ckpt", "gmm_mx4_quantize_lhs", "gmm_mx4_quantize_rhs", "gmm_mx4_fwd",
+            "gmm_mx4_fwd_swiglu_quant"]
 
 
 class TileConfig(ctypes.Structure):
@@ -124,6 +126,20 @@ def load():
     lib.gmm_fp8_w4_fwd_swiglu_quant.restype = I
     lib.gmm_fp8_w4_fwd_swiglu_quant.argtypes = [P, P, P, P, P, I, I64, I64, I64, P, P, P, P, SZ, P,
                                                 ctypes.POINTER(TileConfig)]
+    lib.gmm_bf16_swiglu_fwd.restype = I
+    lib.gmm_bf16_swiglu_fwd.argtypes = [P, P, P, I, I64, I64, I64, P, P, P, P, P, SZ, P]
+    lib.gmm_bf16_swiglu_bwd.restype = I
+    lib.gmm_bf16_swiglu_bwd.argtypes = [P, P, P, P, P, P, I, I64, I64, I64, P, P, P, SZ, P]
+    lib.tgmm_fp8_ckpt.restype = I
+    lib.tgmm_fp8_ckpt.argtypes = [P, P, P, P, I, I64, I64, I64, P, P, SZ, P]
+    lib.gmm_mx4_quantize_lhs.restype = I
+    lib.gmm_mx4_quantize_lhs.argtypes = [P, I64, I64, P, P, P]
+    lib.gmm_mx4_quantize_rhs.restype = I
+    lib.gmm_mx4_quantize_rhs.argtypes = [P, I, I64, I64, P, P, P]
+    lib.gmm_mx4_fwd.restype = I
+    lib.gmm_mx4_fwd.argtypes = [P, P, P, P, P, I, I64, I64, I64, I, P, P, SZ, P]
+    lib.gmm_mx4_fwd_swiglu_quant.restype = I
+    lib.gmm_mx4_fwd_swiglu_quant.argtypes = [P, P, P, P, P, I, I64, I64, I64, P, P, P, P, SZ, P]
     _lib = lib
     return lib
 
@@ -269,6 +285,43 @@ def gmm_fp8_fwd_noalloc(xq, xs, wq, ws, group_sizes, G, M, K, N, fuse_silu_mul, 
     the metadata lives in the library's static device array (see gmm.h)."""
     return load().gmm_fp8_fwd_noalloc(_p(xq), _p(xs), _p(wq), _p(ws), _p(group_sizes), G, M, K, N,
                                       int(fuse_silu_mul), _p(out), _s(stream))
+
+
+def gmm_bf16_swiglu_fwd(x, w, group_sizes, G, M, K, N, h, gu, guq, gus, workspace, workspace_bytes,
+                        stream=None) -> int:
+    return load().gmm_bf16_swiglu_fwd(_p(x), _p(w), _p(group_sizes), G, M, K, N, _p(h), _p(gu), _p(guq), _p(gus),
+                                      _p(workspace), workspace_bytes, _s(stream))
+
+
+def gmm_bf16_swiglu_bwd(dy, w2, gu, guq, gus, group_sizes, G, M, K, N, dgu, h, workspace, workspace_bytes,
+                        stream=None) -> int:
+    return load().gmm_bf16_swiglu_bwd(_p(dy), _p(w2), _p(gu), _p(guq), _p(gus), _p(group_sizes), G, M, K, N,
+                                      _p(dgu), _p(h), _p(workspace), workspace_bytes, _s(stream))
+
+
+def tgmm_fp8_ckpt(xq, xs, dy, group_sizes, G, M, K, N, dw, workspace, workspace_bytes, stream=None) -> int:
+    return load().tgmm_fp8_ckpt(_p(xq), _p(xs), _p(dy), _p(group_sizes), G, M, K, N, _p(dw), _p(workspace),
+                                workspace_bytes, _s(stream))
+
+
+def gmm_mx4_quantize_lhs(x, M, K, xq, xs, stream=None) -> int:
+    return load().gmm_mx4_quantize_lhs(_p(x), M, K, _p(xq), _p(xs), _s(stream))
+
+
+def gmm_mx4_quantize_rhs(w, G, K, N, wq, ws, stream=None) -> int:
+    return load().gmm_mx4_quantize_rhs(_p(w), G, K, N, _p(wq), _p(ws), _s(stream))
+
+
+def gmm_mx4_fwd(xq, xs, wq, ws, group_sizes, G, M, K, N, fuse_silu_mul, out, workspace, workspace_bytes,
+                stream=None) -> int:
+    return load().gmm_mx4_fwd(_p(xq), _p(xs), _p(wq), _p(ws), _p(group_sizes), G, M, K, N, int(fuse_silu_mul),
+                              _p(out), _p(workspace), workspace_bytes, _s(stream))
+
+
+def gmm_mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, G, M, K, N, h, hq, hs, workspace, workspace_bytes,
+                             stream=None) -> int:
+    return load().gmm_mx4_fwd_swiglu_quant(_p(xq), _p(xs), _p(wq), _p(ws), _p(group_sizes), G, M, K, N, _p(h),
+                                           _p(hq), _p(hs), _p(workspace), workspace_bytes, _s(stream))
 
 
 # ---------------------------------------------------------------------------
@@ -487,3 +540,127 @@ def group_metadata(group_sizes, M, workspace=None, stream=None) -> Workspace:
     ws_ = _ws(workspace, G, M, group_sizes.device)
     _check(gmm_group_metadata(group_sizes, G, M, ws_.buf, ws_.nbytes, stream), "gmm_group_metadata")
     return ws_
+
+
+def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=None):
+    """The gated block's forward: x bf16 [M, K], w bf16 [G, K, 2N] (gate | up)
+    -> (h bf16 [M, N], kept), kept being what swiglu_bwd takes: the gate | up
+    values in bf16 [M, 2N] (keep="bf16"), or their 8-bit checkpoint (codes
+    uint8 [M, 2N], scales float32 [2N/128, M]) (keep="e4m3").
+    out: an (h, kept) pair to write into instead of new tensors."""
+    if keep not in ("bf16", "e4m3"):
+        raise ValueError(f"keep must be 'bf16' or 'e4m3', got {keep!r}")
+    M, K = x.shape
+    G, K2, Nw = w.shape
+    assert K2 == K and Nw % 2 == 0
+    N = Nw // 2
+    if out is not None:
+        h, kept = out
+    else:
+        h = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        if keep == "bf16":
+            kept = torch.empty((M, Nw), dtype=torch.bfloat16, device=x.device)
+        else:
+            kept = (torch.empty((M, Nw), dtype=torch.uint8, device=x.device),
+                    torch.empty((Nw // 128, M), dtype=torch.float32, device=x.device))
+    gu, (guq, gus) = (kept, (None, None)) if keep == "bf16" else (None, kept)
+    ws_ = _ws_for(group_sizes, workspace, G, M, x.device)
+    _check(gmm_bf16_swiglu_fwd(x, w, group_sizes, G, M, K, N, h, gu, guq, gus, ws_.buf, ws_.nbytes, stream),
+           "gmm_bf16_swiglu_fwd")
+    return h, kept
+
+
+def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=None, out=None):
+    """Its backward pass: dy bf16 [M, K] (the gradient of y = h W2), w2 bf16
+    [G, N, K], kept as swiglu_fwd returned it -> (dgu bf16 [M, 2N], the gradient
+    of gate | up; h bf16 [M, N], recomputed, or None).
+    out: a (dgu, h) pair to write into instead of new tensors."""
+    M, K = dy.shape
+    G, N, K2 = w2.shape
+    assert K2 == K
+    gu, guq, gus = (None, *kept) if isinstance(kept, (tuple, list)) else (kept, None, None)
+    assert tuple((guq if gu is None else gu).shape) == (M, 2 * N)
+    if out is not None:
+        dgu, h = out
+    else:
+        dgu = torch.empty((M, 2 * N), dtype=torch.bfloat16, device=dy.device)
+        h = torch.empty((M, N), dtype=torch.bfloat16, device=dy.device) if with_h else None
+    ws_ = _ws_for(group_sizes, workspace, G, M, dy.device)
+    _check(gmm_bf16_swiglu_bwd(dy, w2, gu, guq, gus, group_sizes, G, M, K, N, dgu, h, ws_.buf, ws_.nbytes, stream),
+           "gmm_bf16_swiglu_bwd")
+    return dgu, h
+
+
+def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
+    """tgmm from the 8-bit checkpoint of x: xq uint8 [M, K] e4m3 codes, xs
+    float32 [K/128, M] (quantize_lhs), dy bf16 [M, N] -> dw bf16 [G, K, N]."""
+    M, K = xq.shape
+    M2, N = dy.shape
+    assert M2 == M and tuple(xs.shape) == (K // 128, M)
+    if group_sizes is not None:
+        G = group_sizes.numel()
+    elif dw is not None:
+        G = dw.shape[0]
+    elif workspace is not None:
+        G = workspace.G
+    else:
+        raise ValueError("group_sizes=None reuses the metadata in `workspace`: pass that workspace")
+    if dw is None:
+        dw = torch.empty((G, K, N), dtype=torch.bfloat16, device=dy.device)
+    ws_ = _ws_for(group_sizes, workspace, G, M, dy.device)
+    _check(tgmm_fp8_ckpt(xq, xs, dy, group_sizes, G, M, K, N, dw, ws_.buf, ws_.nbytes, stream), "tgmm_fp8_ckpt")
+    return dw
+
+
+def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
+    """x bf16 [M, K] -> (xq uint8 [M, K/2] packed E2M1 codes, xs uint8 [K/128, M, 4] E8M0 scales)."""
+    M, K = x.shape
+    if out is not None:
+        xq, xs = out
+    else:
+        xq = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        xs = torch.empty((K // 128, M, 4), dtype=torch.uint8, device=x.device)
+    _check(gmm_mx4_quantize_lhs(x, M, K, xq, xs, stream), "gmm_mx4_quantize_lhs")
+    return xq, xs
+
+
+def mx4_quantize_rhs(w: torch.Tensor, stream=None):
+    """w bf16 [G, K, N] -> (wq uint8 [G, N, K/2] packed E2M1 codes, ws uint8 [G, N/128, K/128, 512] E8M0 scales)."""
+    G, K, N = w.shape
+    wq = torch.empty((G, N, K // 2), dtype=torch.uint8, device=w.device)
+    ws = torch.empty((G, N // 128, K // 128, 512), dtype=torch.uint8, device=w.device)
+    _check(gmm_mx4_quantize_rhs(w, G, K, N, wq, ws, stream), "gmm_mx4_quantize_rhs")
+    return wq, ws
+
+
+def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, stream=None):
+    """MXFP4 x MXFP4 grouped product -> bf16 [M, N] (fuse: silu(gate) * up, wq holding gate | up)."""
+    M, K2 = xq.shape
+    G, Nw, K3 = wq.shape
+    assert K3 == K2
+    N = Nw // 2 if fuse else Nw
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+    ws_ = _ws_for(group_sizes, workspace, G, M, xq.device)
+    _check(gmm_mx4_fwd(xq, xs, wq, ws, group_sizes, G, M, 2 * K2, N, fuse, out, ws_.buf, ws_.nbytes, stream),
+           "gmm_mx4_fwd")
+    return out
+
+
+def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=None, stream=None, out=None):
+    """Fused gate/up product: (h bf16 [M, N] or None, hq, hs), hq and hs being h in MXFP4.
+    out: an (h, hq, hs) triple to write into instead of new tensors."""
+    M, K2 = xq.shape
+    G, Nw, K3 = wq.shape
+    assert K3 == K2
+    N = Nw // 2
+    if out is not None:
+        h, hq, hs = out
+    else:
+        h = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device) if with_h else None
+        hq = torch.empty((M, N // 2), dtype=torch.uint8, device=xq.device)
+        hs = torch.empty((N // 128, M, 4), dtype=torch.uint8, device=xq.device)
+    ws_ = _ws_for(group_sizes, workspace, G, M, xq.device)
+    _check(gmm_mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, G, M, 2 * K2, N, h, hq, hs, ws_.buf, ws_.nbytes,
+                                    stream), "gmm_mx4_fwd_swiglu_quant")
+    return h, hq, hs

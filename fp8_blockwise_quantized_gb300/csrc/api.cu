@@ -198,6 +198,30 @@ int host_fp8_default_cta_group(int64_t, int, int, int) {
   return 1;
 }
 
+gmm_status host_device_sms(int* sms) {
+  DeviceInfo di;
+  gmm_status st = device_info(&di);
+  if (st == GMM_OK) *sms = di.sms;
+  return st;
+}
+
+gmm_status host_check_grouped(int G, int64_t M, int64_t K, int64_t N, int64_t Nw) {
+  return check_grouped(G, M, K, N, Nw);
+}
+
+gmm_status host_check_workspace(const void* workspace, size_t bytes, int G, int64_t M) {
+  return check_workspace(workspace, bytes, G, M);
+}
+
+gmm_status host_launch_metadata(const int32_t* sizes, int G, int64_t M, void* workspace, cudaStream_t s) {
+  return launch_metadata(sizes, G, M, workspace, s);
+}
+
+gmm_status host_encode_2d(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes, const void* base, uint64_t inner,
+                          uint64_t outer, uint32_t box_inner, uint32_t box_outer) {
+  return encode_2d(map, dt, elem_bytes, base, inner, outer, box_inner, box_outer);
+}
+
 gmm_status host_fp8_config(int64_t N, int fuse, const gmm_fp8_tile_config* in, int sms, gmm_fp8_tile_config* out) {
   gmm_fp8_tile_config c = in ? *in : gmm_fp8_tile_config{0, 0, 0, 0, 0, 0};
   if (c.cta_group == 0) c.cta_group = host_fp8_default_cta_group(N, fuse, c.bn, c.ctas);

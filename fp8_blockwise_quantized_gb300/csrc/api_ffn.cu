@@ -1,0 +1,247 @@
+// Host side of the feed-forward block's entry points (include/gmm.h): the
+// gated forward and backward, the weight gradient from 8-bit checkpoints and
+// the MXFP4 quantisation and products.  Nothing here allocates device memory
+// or synchronizes.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gmm.h"
+#include "common.cuh"
+#include "host.cuh"
+#include "kernels.cuh"
+
+using namespace gmm;
+
+namespace {
+
+// every pointer 16-byte aligned (NULL passes)
+template <typename... P>
+bool all_aligned(P... p) {
+  return (((reinterpret_cast<uintptr_t>(p) & 15u) == 0) && ...);
+}
+
+const Tile* tiles_of(const void* workspace, int G) {
+  return reinterpret_cast<const Tile*>(static_cast<const char*>(workspace) + tiles_offset_bytes(G));
+}
+
+// Upper bound of the row tiles: every group adds at most one that is not
+// full, and none without rows.
+long long max_tiles(int G, int64_t M) { return (M + kBM - 1) / kBM + (M < G ? M : G); }
+
+// The device, the workspace and (unless group_sizes is NULL) the metadata.
+gmm_status begin(const int32_t* group_sizes, int G, int64_t M, void* workspace, size_t workspace_bytes,
+                 cudaStream_t s, int* sms) {
+  gmm_status st = host_check_workspace(workspace, workspace_bytes, G, M);
+  if (st != GMM_OK) return st;
+  if ((st = host_device_sms(sms)) != GMM_OK) return st;
+  return group_sizes ? host_launch_metadata(group_sizes, G, M, workspace, s) : GMM_OK;
+}
+
+gmm_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? GMM_OK : host_cuda_fail(e, what); }
+
+// The kernels' unit indices are 32-bit, with the grid's claims on top.
+constexpr long long kMaxUnits = 1LL << 30;
+
+constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+constexpr CUtensorMapDataType kByte = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+
+// The kept gate | up values: bf16 (gu) or e4m3 with scales (guq, gus), one of them.
+gmm_status check_kept(int64_t M, const void* gu, const void* guq, const float* gus) {
+  if (M == 0) return GMM_OK;
+  const bool e4m3 = guq || gus;
+  if (e4m3 ? (!guq || !gus) : !gu) return GMM_ERR_NULL;
+  return gu && e4m3 ? GMM_ERR_UNSUPPORTED : GMM_OK;
+}
+
+gmm_status mx4_entry(const void* xq, const void* xs, const void* wq, const void* ws, const int32_t* group_sizes, int G,
+                     int64_t M, int64_t K, int64_t N, int fuse, void* out, void* hq, void* hs, bool quant,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const int64_t Nw = fuse ? 2 * N : N;
+  gmm_status st = host_check_grouped(G, M, K, N, Nw);
+  if (st != GMM_OK) return st;
+  if (!wq || !ws) return GMM_ERR_NULL;
+  if (M > 0 && (!xq || !xs || (quant ? (!hq || !hs) : !out))) return GMM_ERR_NULL;
+  if (!all_aligned(xq, xs, wq, ws, group_sizes, out, hq, hs)) return GMM_ERR_ALIGN;
+  if (max_tiles(G, M) * (N / 64) > kMaxUnits) return GMM_ERR_SHAPE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
+  if (M == 0) return GMM_OK;
+  const int bn = (fuse || N % 256 == 0) && max_tiles(G, M) * (Nw / 256) >= sms ? 256 : 128;
+  CUtensorMap map_a, map_b, map_out;
+  if ((st = host_encode_2d(&map_a, kByte, 1, xq, K / 2, M, 128, 128)) != GMM_OK) return st;
+  if ((st = host_encode_2d(&map_b, kByte, 1, wq, K / 2, G * Nw, 128, fuse ? bn / 2 : bn)) != GMM_OK) return st;
+  if (out) {
+    if ((st = host_encode_2d(&map_out, kBf16, 2, out, N, M, 64, 32)) != GMM_OK) return st;
+  } else {
+    map_out = map_a;  // never read
+  }
+  Mx4Args a{};
+  a.meta = static_cast<const int32_t*>(workspace);
+  a.tiles = tiles_of(workspace, G);
+  a.xs = static_cast<const uint32_t*>(xs);
+  a.ws = static_cast<const uint8_t*>(ws);
+  a.out = static_cast<uint16_t*>(out);
+  a.hq = quant ? static_cast<uint8_t*>(hq) : nullptr;
+  a.hs = quant ? static_cast<uint32_t*>(hs) : nullptr;
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.fuse = fuse;
+  a.bn = bn;
+  a.wait_limit_ns = host_wait_limit_ns();
+  const long long units = max_tiles(G, M) * (Nw / bn);
+  return launched(launch_gmm_mx4(map_a, map_b, map_out, a, static_cast<int>(units < sms ? units : sms), s),
+                  "gmm_mx4 kernel launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+gmm_status gmm_bf16_swiglu_fwd(const void* x, const void* w, const int32_t* group_sizes, int G, int64_t M, int64_t K,
+                               int64_t N, void* h, void* gu, void* guq, float* gus, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  gmm_status st = host_check_grouped(G, M, K, N, 2 * N);
+  if (st != GMM_OK) return st;
+  if (!w || (M > 0 && (!x || !h))) return GMM_ERR_NULL;
+  if ((st = check_kept(M, gu, guq, gus)) != GMM_OK) return st;
+  if (!all_aligned(x, w, group_sizes, h, gu, guq, gus)) return GMM_ERR_ALIGN;
+  const long long units = max_tiles(G, M) * (N / 128);
+  if (units > kMaxUnits) return GMM_ERR_SHAPE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
+  if (M == 0) return GMM_OK;
+  CUtensorMap map_x, map_w;
+  if ((st = host_encode_2d(&map_x, kBf16, 2, x, K, M, 64, 128)) != GMM_OK) return st;
+  if ((st = host_encode_2d(&map_w, kBf16, 2, w, 2 * N, G * K, 64, 64)) != GMM_OK) return st;
+  SwigluArgs a{};
+  a.meta = static_cast<const int32_t*>(workspace);
+  a.tiles = tiles_of(workspace, G);
+  a.h = static_cast<uint16_t*>(h);
+  a.gu = static_cast<uint16_t*>(gu);
+  a.guq = static_cast<uint8_t*>(guq);
+  a.gus = gus;
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.wait_limit_ns = host_wait_limit_ns();
+  return launched(launch_gmm_swiglu_fwd(map_x, map_w, a, static_cast<int>(units < sms ? units : sms), s),
+                  "gmm_swiglu forward launch");
+}
+
+gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, const void* guq, const float* gus,
+                               const int32_t* group_sizes, int G, int64_t M, int64_t K, int64_t N, void* dgu, void* h,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  gmm_status st = host_check_grouped(G, M, K, N, 2 * N);
+  if (st != GMM_OK) return st;
+  if (!w2 || (M > 0 && (!dy || !dgu))) return GMM_ERR_NULL;
+  if ((st = check_kept(M, gu, guq, gus)) != GMM_OK) return st;
+  if (!all_aligned(dy, w2, gu, guq, gus, group_sizes, dgu, h)) return GMM_ERR_ALIGN;
+  const int bn = swiglu_bwd_bn(static_cast<int>(N));
+  const long long units = max_tiles(G, M) * (N / bn);
+  if (units > kMaxUnits) return GMM_ERR_SHAPE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
+  if (M == 0) return GMM_OK;
+  CUtensorMap map_dy, map_w2;
+  if ((st = host_encode_2d(&map_dy, kBf16, 2, dy, K, M, 64, 128)) != GMM_OK) return st;
+  if ((st = host_encode_2d(&map_w2, kBf16, 2, w2, K, G * N, 64, bn)) != GMM_OK) return st;
+  SwigluArgs a{};
+  a.meta = static_cast<const int32_t*>(workspace);
+  a.tiles = tiles_of(workspace, G);
+  a.h = static_cast<uint16_t*>(h);
+  a.gu = static_cast<uint16_t*>(const_cast<void*>(gu));
+  a.guq = static_cast<uint8_t*>(const_cast<void*>(guq));
+  a.gus = const_cast<float*>(gus);
+  a.dgu = static_cast<uint16_t*>(dgu);
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.wait_limit_ns = host_wait_limit_ns();
+  return launched(launch_gmm_swiglu_bwd(map_dy, map_w2, a, static_cast<int>(units < sms ? units : sms), s),
+                  "gmm_swiglu backward launch");
+}
+
+gmm_status tgmm_fp8_ckpt(const void* xq, const float* xs, const void* dy, const int32_t* group_sizes, int G, int64_t M,
+                         int64_t K, int64_t N, void* dw, void* workspace, size_t workspace_bytes, void* stream) {
+  gmm_status st = host_check_grouped(G, M, K, N, N);
+  if (st != GMM_OK) return st;
+  const long long units = static_cast<long long>(G) * ((K + 255) / 256) * ((N + 255) / 256);
+  if (units > kMaxUnits) return GMM_ERR_SHAPE;
+  if (!dw || (M > 0 && (!xq || !xs || !dy))) return GMM_ERR_NULL;
+  if (!all_aligned(xq, xs, dy, group_sizes, dw)) return GMM_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
+  // With M == 0 every group is empty: the kernel only writes zeros and never
+  // reads x or dy, so the maps may describe a dummy one-row tensor.
+  CUtensorMap map_x, map_dy, map_dw;
+  if ((st = host_encode_2d(&map_x, kByte, 1, M > 0 ? xq : dw, K, M, 128, 64)) != GMM_OK) return st;
+  if ((st = host_encode_2d(&map_dy, kBf16, 2, M > 0 ? dy : dw, N, M, 64, 64)) != GMM_OK) return st;
+  if ((st = host_encode_2d(&map_dw, kBf16, 2, dw, N, G * K, 64, 32)) != GMM_OK) return st;
+  TgmmArgs a{};
+  a.meta = static_cast<const int32_t*>(workspace);
+  a.order = reinterpret_cast<const int32_t*>(static_cast<const char*>(workspace) + order_offset_bytes(G, M));
+  a.dw = static_cast<uint16_t*>(dw);
+  a.xs = xs;
+  a.G = G;
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.wait_limit_ns = host_wait_limit_ns();
+  const int max_pairs = static_cast<int>(units < sms / 2 ? units : sms / 2);
+  return launched(launch_tgmm_ckpt(map_x, map_dy, map_dw, a, max_pairs, s), "tgmm_ckpt kernel launch");
+}
+
+gmm_status gmm_mx4_quantize_lhs(const void* x, int64_t M, int64_t K, void* xq, void* xs, void* stream) {
+  if (M < 0 || M > INT32_MAX || K < 128 || K % 128 != 0 || K > (1 << 24)) return GMM_ERR_SHAPE;
+  if (M == 0) return GMM_OK;
+  if (!x || !xq || !xs) return GMM_ERR_NULL;
+  if (!all_aligned(x, xq, xs)) return GMM_ERR_ALIGN;
+  int sms = 0;
+  gmm_status st = host_device_sms(&sms);
+  if (st != GMM_OK) return st;
+  const long long steps = (M + 7) / 8 * (K / 128);  // a warp each, 8 warps per CTA
+  long long grid = (steps + 7) / 8;
+  if (grid > static_cast<long long>(sms) * 8) grid = static_cast<long long>(sms) * 8;
+  return launched(launch_pdl(mx4_quantize_lhs_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
+                             static_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), static_cast<int>(M),
+                             static_cast<int>(K / 128), static_cast<uint32_t*>(xq), static_cast<uint32_t*>(xs)),
+                  "mx4_quantize_lhs_kernel launch");
+}
+
+gmm_status gmm_mx4_quantize_rhs(const void* w, int G, int64_t K, int64_t N, void* wq, void* ws, void* stream) {
+  if (G < 1 || K < 128 || K % 128 != 0 || N < 128 || N % 128 != 0 || K > (1 << 24) || N > (1 << 24))
+    return GMM_ERR_SHAPE;
+  const int64_t grid = static_cast<int64_t>(G) * (K / 128) * (N / 128);
+  if (grid > INT32_MAX) return GMM_ERR_SHAPE;
+  if (!w || !wq || !ws) return GMM_ERR_NULL;
+  if (!all_aligned(w, wq, ws)) return GMM_ERR_ALIGN;
+  int sms = 0;
+  gmm_status st = host_device_sms(&sms);
+  if (st != GMM_OK) return st;
+  mx4_quantize_rhs_kernel<<<static_cast<unsigned>(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint16_t*>(w), static_cast<int>(K), static_cast<int>(N), static_cast<uint8_t*>(wq),
+      static_cast<uint8_t*>(ws));
+  return launched(cudaGetLastError(), "mx4_quantize_rhs_kernel launch");
+}
+
+gmm_status gmm_mx4_fwd(const void* xq, const void* xs, const void* wq, const void* ws, const int32_t* group_sizes,
+                       int G, int64_t M, int64_t K, int64_t N, int fuse_silu_mul, void* out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return mx4_entry(xq, xs, wq, ws, group_sizes, G, M, K, N, fuse_silu_mul ? 1 : 0, out, nullptr, nullptr, false,
+                   workspace, workspace_bytes, stream);
+}
+
+gmm_status gmm_mx4_fwd_swiglu_quant(const void* xq, const void* xs, const void* wq, const void* ws,
+                                    const int32_t* group_sizes, int G, int64_t M, int64_t K, int64_t N, void* h,
+                                    void* hq, void* hs, void* workspace, size_t workspace_bytes, void* stream) {
+  return mx4_entry(xq, xs, wq, ws, group_sizes, G, M, K, N, 1, h, hq, hs, true, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include <cuda.h>
+
 #include "gmm.h"
 
 namespace gmm {
@@ -35,5 +37,16 @@ gmm_status host_fp8_config(int64_t N, int fuse, const gmm_fp8_tile_config* in, i
 gmm_status host_fp8_launch(const void* xq, const float* xs, const void* wq, const float* ws, int G, int64_t M,
                            int64_t K, int64_t N, int fuse, void* out, void* hq, float* hs, void* workspace,
                            const gmm_fp8_tile_config& cfg, cudaStream_t s, int w4);
+
+// Checks and steps shared by every grouped entry point: the current device's
+// SM count (an error unless it is sm_103); the sizes (Nw: columns of the
+// weight); the workspace; the group metadata pass.
+gmm_status host_device_sms(int* sms);
+gmm_status host_check_grouped(int G, int64_t M, int64_t K, int64_t N, int64_t Nw);
+gmm_status host_check_workspace(const void* workspace, size_t bytes, int G, int64_t M);
+gmm_status host_launch_metadata(const int32_t* sizes, int G, int64_t M, void* workspace, cudaStream_t s);
+// Row-major 2-D tensor map with 128-byte swizzle.
+gmm_status host_encode_2d(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes, const void* base, uint64_t inner,
+                          uint64_t outer, uint32_t box_inner, uint32_t box_outer);
 
 }  // namespace gmm

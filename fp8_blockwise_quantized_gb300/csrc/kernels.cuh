@@ -72,6 +72,35 @@ struct TgmmArgs {
   int claim_ahead;        // CTA-pair kernel: units claimed beyond the producer (1..12)
   int max_batch;          // CTA-pair kernel: most small units per claim (1..4)
   uint64_t wait_limit_ns;
+  const float* xs;        // 8-bit checkpoint: fp32 [K/128][M] scales of x's codes
+};
+
+// The gated feed-forward block's kernels: the forward (K = columns of x) and
+// the backward (K = columns of dy, the reduction of dh = dy W2^T).
+struct SwigluArgs {
+  const int32_t* meta;    // workspace words
+  const Tile* tiles;      // workspace tile list (128-row tiles)
+  uint16_t* h;            // bf16 [M][N] (backward: may be null)
+  uint16_t* gu;           // kept gate | up, bf16 [M][2N], or null:
+  uint8_t* guq;           // e4m3 codes [M][2N] with
+  float* gus;             // fp32 [2N/128][M] scales
+  uint16_t* dgu;          // backward: gradient of gate | up, bf16 [M][2N]
+  int M, K, N;
+  uint64_t wait_limit_ns;
+};
+
+struct Mx4Args {
+  const int32_t* meta;    // workspace words
+  const Tile* tiles;      // workspace tile list (128-row tiles)
+  const uint32_t* xs;     // E8M0 scales of x, words of four blocks [K/128][M]
+  const uint8_t* ws;      // E8M0 scales of w, tiles [G][Nw/128][K/128][512]
+  uint16_t* out;          // bf16 [M][N] (may be null with hq)
+  uint8_t* hq;            // MXFP4 output: codes [M][N/2] (null: none)
+  uint32_t* hs;           // and scale words [N/128][M]
+  int M, K, N;            // N = output columns
+  int fuse;               // 1: silu(gate) * up, w has 2N columns
+  int bn;                 // weight columns per unit (128 or 256)
+  uint64_t wait_limit_ns;
 };
 
 // Host launchers: `grid` CTAs (persistent), on `stream`.  Return the launch error.
@@ -94,6 +123,25 @@ cudaError_t launch_gmm_bf16_dgrad(const CUtensorMap& map_a, const CUtensorMap& m
                                   int grid, cudaStream_t stream);
 cudaError_t launch_tgmm_bf16(const CUtensorMap& map_x, const CUtensorMap& map_dy, const CUtensorMap& map_dw,
                              const TgmmArgs& args, int grid, cudaStream_t stream);
+
+// map_x: x [M, K], box 64 x 128; map_w: w [G*K, 2N], box 64 x 64.
+cudaError_t launch_gmm_swiglu_fwd(const CUtensorMap& map_x, const CUtensorMap& map_w, const SwigluArgs& args,
+                                  int grid, cudaStream_t stream);
+// map_dy: dy [M, K], box 64 x 128; map_w2: w2 [G*N, K], box 64 x swiglu_bwd_bn(N).
+cudaError_t launch_gmm_swiglu_bwd(const CUtensorMap& map_dy, const CUtensorMap& map_w2, const SwigluArgs& args,
+                                  int grid, cudaStream_t stream);
+int swiglu_bwd_bn(int N);
+// map_x: codes [M, K] bytes, box 128 x 64; map_dy: box 64 x 64; map_dw: dw [G*K, N], box 64 x 32.
+cudaError_t launch_tgmm_ckpt(const CUtensorMap& map_x, const CUtensorMap& map_dy, const CUtensorMap& map_dw,
+                             const TgmmArgs& args, int max_pairs, cudaStream_t stream);
+
+// ---- MXFP4 --------------------------------------------------------------------
+__global__ void mx4_quantize_lhs_kernel(const uint4* x, int M, int KB, uint32_t* xq, uint32_t* xs);
+__global__ void mx4_quantize_rhs_kernel(const uint16_t* w, int K, int N, uint8_t* wq, uint8_t* ws);
+// map_a: codes [M, K/2] bytes, box 128 x 128; map_b: codes [G*Nw, K/2] bytes,
+// box 128 x bn (bn / 2 when fused); map_out: out [M, N], box 64 x 32.
+cudaError_t launch_gmm_mx4(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_out,
+                           const Mx4Args& args, int grid, cudaStream_t stream);
 
 // Tile geometry the host needs to build tensor maps and size grids.
 struct Fp8Geometry {

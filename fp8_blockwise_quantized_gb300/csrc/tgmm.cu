@@ -25,6 +25,7 @@
 // CTA-pair kernel below claims them from a counter.
 #include "common.cuh"
 #include "kernels.cuh"
+#include "pairqueue.cuh"
 #include "ptx.cuh"
 
 namespace gmm {
@@ -34,7 +35,6 @@ namespace {
 constexpr int kStages = 4;
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
-constexpr int kChunk = 64;  // rows per stage
 constexpr uint64_t kDrainLimitNs = 200000000ull;
 
 // The units of a launch are numbered group by group, the groups taken
@@ -351,7 +351,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kPairStages = 6;  // default ring slots with BN = 256 (4 or 5 selectable)
 constexpr int kPairThreads = 352;
 constexpr int kSchedWarp = 10;
-constexpr int kQueue = 16;
 constexpr int kQueueReaders = 2 * (2 + kEpiWarps);  // producer, warp 1, epilogue warps; both CTAs
 // the scheduler holds at most TgmmArgs::claim_ahead units (default 3) beyond
 // those the even CTA's producer has taken, claims only while fewer than 8
@@ -385,33 +384,6 @@ struct TgmmPairTile {
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + 1024;
   static_assert(kTailBytes <= 1024, "barrier area");
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-};
-
-// Entry i of a CTA's unit queue (every lane of the calling warp, or the one
-// thread of a single-thread role, with `warp_wide` false); the entry is freed
-// on the even CTA as soon as it has been read.
-struct UnitQueue {
-  uint64_t* full;
-  uint64_t* empty;
-  const int4* data;
-  uint32_t empty_leader;  // shared::cluster address of the even CTA's empty[0]
-  bool leader;
-  __device__ bool get(uint32_t i, int4& e, bool warp_wide, int lane, volatile int* abort_word,
-                      uint64_t lim) const {
-    const uint32_t slot = i % kQueue, ph = (i / kQueue) & 1u;
-    bool ok = mbar_wait(&full[slot], ph, abort_word, lim);
-    if (warp_wide) ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return false;
-    e = data[slot];
-    if (warp_wide) __syncwarp();
-    if (lane == 0) {
-      if (leader)
-        mbar_arrive(&empty[slot]);
-      else
-        mbar_arrive_remote(empty_leader + slot * 8u);
-    }
-    return true;
-  }
 };
 
 template <int BN, int STAGES>
@@ -481,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int num_units = valid_meta ? args.G * KPNT : 0;
   const int* offsets = args.meta + kWsOffsets;
   const uint64_t lim = args.wait_limit_ns;
-  const UnitQueue queue{qfull, qempty, qdata, mapa_shared(smem_u32(qempty), 0), leader};
+  const PairQueue queue{qfull, qempty, qdata, mapa_shared(smem_u32(qempty), 0), leader};
 
   if (warp == 0) {
     if (lane == 0) {
@@ -673,102 +645,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (lane == 0) bulk_wait_all();
   } else if (leader && lane == 0) {
     // ------------------------------------------------------------ scheduler
-    int* claimed = const_cast<int32_t*>(args.meta) + kWsClaimed;
-    const uint32_t odd_full = mapa_shared(smem_u32(qfull), 1);
-    const uint32_t odd_data = mapa_shared(smem_u32(qdata), 1);
-    uint32_t i = 0;
-    auto publish = [&](int4 v) -> bool {
-      const uint32_t slot = i % kQueue, ph = (i / kQueue) & 1u;
-      // no more than claim_ahead entries beyond the producer (bounded wait)
-      if (*taken + args.claim_ahead <= static_cast<int>(i)) {
-        const uint64_t t0 = global_timer_ns();
-        while (*taken + args.claim_ahead <= static_cast<int>(i)) {
-          if (*abort_word) return false;
-          if (global_timer_ns() - t0 > lim) {
-            *abort_word = 1;
-            return false;
-          }
-          __nanosleep(64);
-        }
-      }
-      if (!mbar_wait(&qempty[slot], ph ^ 1u, abort_word, lim)) return false;
-      qdata[slot] = v;
-      fence_proxy_async_smem();  // the bulk copy reads the entry through the async proxy
-      mbar_arrive_expect_tx_remote(odd_full + slot * 8u, 16);
-      bulk_copy_s2cluster(odd_data + slot * 16u, &qdata[slot], 16, odd_full + slot * 8u);
-      mbar_arrive(&qfull[slot]);
-      ++i;
-      return true;
-    };
-    constexpr int kMaxBatch = 4;
-    // Claim q takes unit q/2 from the large end of the size order when q is
-    // even and unit num_units-1-q/2 from the small end when q is odd, so every
-    // pair alternates long, read-heavy units with short ones whose cost is
-    // mostly the dW store (or only that, for an empty group): the loads of the
-    // one overlap the stores of the other, and the launch never runs a phase of
-    // loads only followed by a phase of stores only.
-    // With groups of about one size there is nothing to mix, and the plain
-    // order keeps each group's units together: alternate only when the
-    // largest group has more than twice the chunks of the smallest.
-    bool mix = false;
-    if (num_units > 0) {
-      const int gl = __ldg(args.order), gs = __ldg(args.order + args.G - 1);
-      const int cl = (__ldg(offsets + gl + 1) - __ldg(offsets + gl) + kChunk - 1) / kChunk;
-      const int cs = (__ldg(offsets + gs + 1) - __ldg(offsets + gs) + kChunk - 1) / kChunk;
-      mix = cl > 2 * cs;
-    }
-    auto unit_of = [&](int q) { return (mix && (q & 1)) ? num_units - 1 - (q >> 1) : (mix ? (q >> 1) : q); };
-    // Claims are paced by work: the next claim is made only once the producer
-    // is within kLeadChunks chunks of the end of what is already published, so
-    // that a claimed unit starts within a few microseconds (the units of one
-    // group, claimed one after the other, then read its rows at about the same
-    // time and find them in L2, instead of one of them waiting behind a long
-    // unit and reading them again after they were evicted).
-    constexpr int kLeadChunks = 8;
-    bool ok = true;
-    int batch = min(mix ? 2 : 1, args.max_batch);
-    int published = 0;  // chunks of the published units (1 for an empty group's)
-    while (ok) {
-      if (published - *ctaken >= kLeadChunks) {
-        const uint64_t t0 = global_timer_ns();
-        while (published - *ctaken >= kLeadChunks) {
-          if (*abort_word || global_timer_ns() - t0 > lim) break;
-          __nanosleep(64);
-        }
-        if (*abort_word || published - *ctaken >= kLeadChunks) {
-          *abort_word = 1;
-          ok = false;
-          break;
-        }
-      }
-      const int k0 = atomicAdd(claimed, batch);
-      if (k0 >= num_units) break;
-      const int cnt = min(batch, num_units - k0);
-      int u[kMaxBatch], g[kMaxBatch], r0[kMaxBatch], r1[kMaxBatch];
-#pragma unroll
-      for (int j = 0; j < kMaxBatch; ++j) u[j] = j < cnt ? unit_of(k0 + j) : 0;
-#pragma unroll
-      for (int j = 0; j < kMaxBatch; ++j) g[j] = j < cnt ? __ldg(args.order + u[j] / KPNT) : 0;
-#pragma unroll
-      for (int j = 0; j < kMaxBatch; ++j) {
-        r0[j] = j < cnt ? __ldg(offsets + g[j]) : 0;
-        r1[j] = j < cnt ? __ldg(offsets + g[j] + 1) : 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kMaxBatch; ++j) {
-        if (ok && j < cnt) {
-          ok = publish(make_int4(g[j], u[j] % KPNT, r0[j], r1[j]));
-          published += max(1, (r1[j] - r0[j] + kChunk - 1) / kChunk);
-        }
-      }
-      // the large-end units shrink as the claims go on: claim more at once
-      // when they get small (when mixing, the first claim of the batch is a
-      // large-end one whenever the batch size is even)
-      const int jf = (mix && (k0 & 1)) ? (cnt > 1 ? 1 : 0) : 0;
-      const int chunks = (r1[jf] - r0[jf] + kChunk - 1) / kChunk;
-      batch = min(chunks >= 4 ? (mix ? 2 : 1) : chunks >= 2 ? 2 : 4, args.max_batch);
-    }
-    if (ok) publish(make_int4(-1, 0, 0, 0));
+    pair_schedule(queue, taken, ctaken, const_cast<int32_t*>(args.meta) + kWsClaimed, args.order, offsets, args.G,
+                  KPNT, num_units, args.claim_ahead, args.max_batch, abort_word, lim);
   }
 
   // teardown: no CTA of the pair leaves while the other may still arrive on

@@ -86,9 +86,10 @@ size_t gmm_workspace_bytes(int G, int64_t M);
  *   int32 word[1]  1 if this call's sizes were valid, else 0
  *   int32 word[2]  S = sum(group_sizes)        (M when invalid)
  *   int32 word[3]  T = number of row tiles      (0 when invalid)
- *   int32 word[4], word[5]  set to 0: the work counters of tgmm_bf16 and of
- *                  the FP8 forward with one CTA per tile (units claimed, CTAs
- *                  finished); each such launch claims its units from them and
+ *   int32 word[4], word[5]  set to 0: the work counters of the kernels that
+ *                  claim their units (units claimed, CTAs finished: tgmm, the
+ *                  FP8 forward with one CTA per tile, gmm_bf16_swiglu_* and
+ *                  gmm_mx4_*); each such launch claims its units from them and
  *                  its last CTA sets them back to 0
  *   int32 word[6]  T2 = number of 256-row tiles (0 when invalid)
  *   int32 word[8 + g], g = 0..G  exclusive prefix sums off_g (off_G = S)
@@ -329,6 +330,100 @@ typedef struct {
 gmm_status tgmm_bf16_tiled(const void* x, const void* dy, const int32_t* group_sizes, int G, int64_t M,
                            int64_t K, int64_t N, void* dw, void* workspace, size_t workspace_bytes,
                            void* stream, const gmm_tgmm_tile_config* config);
+
+/*
+ * The gated feed-forward block for training ("MoE 优化的探索" §1: the SwiGLU
+ * expert; "GEMM Kernel 性能优化十问", Q5: the backward pass stays bf16).
+ * Forward: as gmm_bf16_fwd with fuse_silu_mul = 1, and besides h it leaves
+ * what the backward pass needs of gate a and up b, in one of two forms:
+ *   gu        bf16 [M, 2N] (a | b), or
+ *   guq, gus  8-bit checkpoint: e4m3 codes [M, 2N] in 1x128 blocks and fp32
+ *             scales [2N/128, M], by the rule of gmm_quantize_lhs applied to
+ *             the fp32 accumulators (one rounding)
+ * The other form's pointers are NULL (both given: GMM_ERR_UNSUPPORTED).
+ *   x  bf16 [M, K];  w  bf16 [G, K, 2N] (gate columns first);  h  bf16 [M, N]
+ * Rows >= S are written as zeros (codes 0 and scale 0).
+ */
+gmm_status gmm_bf16_swiglu_fwd(const void* x, const void* w, const int32_t* group_sizes, int G, int64_t M, int64_t K,
+                               int64_t N, void* h, void* gu, void* guq, float* gus, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward pass, from the gradient dy of the block's output y = h W2: with
+ * dh[m,n] = sum_k dy[m,k] * w2[g,n,k] (fp32, never written), a and b as kept
+ * by the forward, and s(a) = 1 / (1 + exp(-a)),
+ *   dgu[m, n]     = bf16( dh * b * s(a) * (1 + a * (1 - s(a))) )   gate's gradient
+ *   dgu[m, N + n] = bf16( dh * a * s(a) )                          up's
+ *   h[m, n]       = bf16( a * s(a) * b )       recomputed, for dW2 = h^T dy
+ *   dy  bf16 [M, K];  w2  bf16 [G, N, K];  gu or guq, gus as above
+ *   dgu bf16 [M, 2N];  h  bf16 [M, N] or NULL; rows >= S are written as zeros.
+ * dx is gmm_bf16_dgrad of dgu with w; dw is tgmm_bf16 of x and dgu, or
+ * tgmm_fp8_ckpt when x was kept in 8 bits.
+ */
+gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, const void* guq, const float* gus,
+                               const int32_t* group_sizes, int G, int64_t M, int64_t K, int64_t N, void* dgu, void* h,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tgmm_bf16 with x kept as an 8-bit checkpoint, the codes and scales that the
+ * FP8 forward multiplied (gmm_quantize_lhs):
+ *   dw[g][k,n] = bf16( sum_{m in group g} bf16(xq[m,k] * xs[k/128,m]) * dy[m,n] )
+ * fp32 accumulation; dw[g] = 0 for an empty group.  Rows >= S are not used,
+ * whatever they hold.
+ *   xq  e4m3 [M, K];  xs  fp32 [K/128, M];  dy  bf16 [M, N];  dw  bf16 [G, K, N]
+ * GMM_ERR_SHAPE also when G * ceil(K/256) * ceil(N/256) output tiles exceed 2^30.
+ */
+gmm_status tgmm_fp8_ckpt(const void* xq, const float* xs, const void* dy, const int32_t* group_sizes, int G, int64_t M,
+                         int64_t K, int64_t N, void* dw, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Microscaled 4-bit (MXFP4) activations and weights ("实现差距：GMM Kernel（V1
+ * vs V2）", §4.1 names MXFP4 as the missing piece; the format is the OCP
+ * Microscaling one): blocks of 32 values along K share a power-of-two scale
+ * 2^(b - 127), b an E8M0 byte, and each value is an E2M1 code.  With E the
+ * biased exponent field of the block's largest |value|, b = max(E - 2, 0); a
+ * block that holds an infinity or NaN gets b = 255, which stands for NaN.
+ * Codes are e2m1(value / scale), nearest even, saturating at 6, two per byte
+ * (even k in the low 4 bits).
+ *   x   bf16 [M, K]
+ *   xq  codes [M, K/2] bytes
+ *   xs  scale bytes [K/128, M, 4]: block k/32 of row m at
+ *       xs[((k/128) * M + m) * 4 + k / 32 % 4]
+ */
+gmm_status gmm_mx4_quantize_lhs(const void* x, int64_t M, int64_t K, void* xq, void* xs, void* stream);
+
+/*
+ * Weights, offline:
+ *   w   bf16 [G, K, N]
+ *   wq  codes [G, N, K/2] bytes (K-major)
+ *   ws  scale bytes [G, N/128, K/128, 512]: within the 512 of (n/128, k/128),
+ *       column n, block k/32 at (n % 32) * 16 + (n % 128 / 32) * 4 + k / 32 % 4
+ */
+gmm_status gmm_mx4_quantize_rhs(const void* w, int G, int64_t K, int64_t N, void* wq, void* ws, void* stream);
+
+/*
+ * MXFP4 x MXFP4 grouped product on the block-scaled tensor core:
+ *   out[m,n] = bf16( sum_k (xq * 2^(xs-127))[m,k] * (wq * 2^(ws-127))[g,n,k] ),
+ * fp32 accumulation.  fuse_silu_mul = 1: w holds 2N columns (gate first) and
+ * out = bf16(silu(y_gate) * y_up), as for gmm_fp8_fwd.
+ *   xq, xs  as written by gmm_mx4_quantize_lhs (M rows, K columns)
+ *   wq, ws  as written by gmm_mx4_quantize_rhs (G, K, N or 2N)
+ *   out     bf16 [M, N]; rows >= S are written as zeros
+ */
+gmm_status gmm_mx4_fwd(const void* xq, const void* xs, const void* wq, const void* ws, const int32_t* group_sizes,
+                       int G, int64_t M, int64_t K, int64_t N, int fuse_silu_mul, void* out, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * The fused gate/up product with the next layer's quantisation in its
+ * epilogue: hq, hs = exactly what gmm_mx4_quantize_lhs(h) would write, h =
+ * bf16(silu(y_gate) * y_up).
+ *   h   bf16 [M, N] or NULL;  hq  codes [M, N/2];  hs  scale bytes [N/128, M, 4];
+ *   rows >= S get zeros.
+ */
+gmm_status gmm_mx4_fwd_swiglu_quant(const void* xq, const void* xs, const void* wq, const void* ws,
+                                    const int32_t* group_sizes, int G, int64_t M, int64_t K, int64_t N, void* h,
+                                    void* hq, void* hs, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * gmm_fp8_fwd without a workspace argument, for callers that cannot allocate
