@@ -154,7 +154,9 @@ def _p(t) -> int | None:
 
 def _s(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without building a Stream object
+        # (0.4 us instead of 3 us of host time a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

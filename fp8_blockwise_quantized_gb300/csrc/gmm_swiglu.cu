@@ -19,9 +19,12 @@
 //   warps 4-11  epilogue: one thread per row and column half
 // Rows of a tile past its group's end belong to the next group: they are
 // multiplied with the wrong weight and never stored.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "rowbox.cuh"
 #include "unitqueue.cuh"
 
 namespace gmm {
@@ -34,17 +37,22 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kQueueReaders = 2 + kEpiWarps;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
+// Register split: 168 per thread at launch; the epilogue warpgroups hold a
+// 32-column piece of four tensors and the next one's inputs.
+constexpr uint32_t kControlRegs = 72, kEpiRegs = 216;
+static_assert(128 * kControlRegs + 256 * kEpiRegs <= kThreads * 168, "register split exceeds the launch budget");
 
 template <int BN>
 struct SwigluTile {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStages = BN == 256 ? 4 : 5;
   static constexpr int kABytes = kBM * 64 * 2;
   static constexpr int kBBytes = 64 * BN * 2;
   static constexpr int kBoxBytes = 64 * 64 * 2;  // one 64 x 64 box of the natural-layout weight
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kTmemCols = 2 * BN;
+  static constexpr int kStagingBytes = kEpiWarps * 4096;
   static constexpr int kBarBytes = 512;
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kBarBytes;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static_assert(8 * (2 * kStages + 5 + ClaimQueue::kBarriers) + 16 + 16 * kClaimSlots <= kBarBytes, "barrier area");
 };
@@ -53,12 +61,7 @@ struct SwigluTile {
 // of fp32; exp(-v) = inf gives 0)
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
-
-__device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& p, float* v) {
   const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -68,7 +71,7 @@ __device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8]) {
 }
 
 // 8 e4m3 codes -> their values times `scale`
-__device__ __forceinline__ void unpack8_e4m3(const uint2& p, float scale, float (&v)[8]) {
+__device__ __forceinline__ void unpack8_e4m3(const uint2& p, float scale, float* v) {
   const uint32_t w[2] = {p.x, p.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -88,41 +91,58 @@ __device__ __forceinline__ void zero_span(void* p, long long bytes, int tid) {
     q[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Row `row` of the forward's outputs, 64 columns of h and one 128-column half
-// (gate or up) of the kept values, from the accumulators at TMEM address `t`
-// (gate in columns [0, 128), up in [128, 256)).
+// The epilogues of one warp: `rows` (1..32) rows from `row0` on, this lane's row
+// in tensor memory at `t`; `stage` is the warp's 4 KB of shared memory.
+using Box64 = RowBox<64>;  // 32 rows x 32 bf16, or 64 codes
+using Box32 = RowBox<32>;  // 32 rows x 32 codes
+
+__device__ __forceinline__ void put32(uint8_t* box, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    Box64::put(box, lane, j,
+               make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                          pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
+}
+
+// Forward: 64 columns of h and of the bf16 gate | up (half 0 the first 64 of
+// the unit's 128, half 1 the rest), or all 128 codes of gate (half 0) or up.
+// The accumulators hold gate in columns [0, 128), up in [128, 256).
 template <bool E4M3>
-__device__ __forceinline__ void fwd_row(const SwigluArgs& args, uint32_t t, int half, long long row, bool valid, int n0) {
-  const long long N = args.N;
+__device__ __forceinline__ void fwd_rows(const SwigluArgs& args, uint8_t* stage, uint32_t t, int half, int lane,
+                                         long long row0, int rows, int n0) {
+  const long long N = args.N, ldh = 2 * N, ldg = 4 * N;
+  uint8_t* box0 = stage;
+  uint8_t* box1 = stage + Box64::kBytes;
 #pragma unroll 1
   for (int cc = 0; cc < 2; ++cc) {
     uint32_t ra[32], rb[32];
     tmem_ld_32x32(t + half * 64 + 32 * cc, ra);
     tmem_ld_32x32(t + 128 + half * 64 + 32 * cc, rb);
     tmem_ld_wait();
-    if (valid) {
-      const int col = n0 + half * 64 + 32 * cc;
-      uint4* ph = reinterpret_cast<uint4*>(args.h + row * N + col);
+    const int col = n0 + half * 64 + 32 * cc;
+    float v[32];
+    if (!E4M3) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float a[8], b[8], v[8];
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ra[i]);
+      put32(box0, lane, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          a[i] = __uint_as_float(ra[8 * j + i]);
-          b[i] = __uint_as_float(rb[8 * j + i]);
-          v[i] = silu_f32(a[i]) * b[i];
-        }
-        ph[j] = pack8(v);
-        if (!E4M3) {
-          reinterpret_cast<uint4*>(args.gu + row * 2 * N + col)[j] = pack8(a);
-          reinterpret_cast<uint4*>(args.gu + row * 2 * N + N + col)[j] = pack8(b);
-        }
-      }
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(rb[i]);
+      put32(box1, lane, v);
+      __syncwarp();
+      uint8_t* g = reinterpret_cast<uint8_t*>(args.gu + row0 * 2 * N + col);
+      Box64::store(box0, g, ldg, rows, lane);
+      Box64::store(box1, g + 2 * N, ldg, rows, lane);
+      __syncwarp();
     }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = silu_f32(__uint_as_float(ra[i])) * __uint_as_float(rb[i]);
+    put32(box0, lane, v);
+    __syncwarp();
+    Box64::store(box0, reinterpret_cast<uint8_t*>(args.h + row0 * N + col), ldh, rows, lane);
+    __syncwarp();
   }
   if (E4M3) {
-    // half 0 keeps the gate block, half 1 the up block: absmax, then codes
-    // (rounded once, from the fp32 sums)
+    // absmax of the row's block, then its codes (rounded once, from the fp32 sums)
     const uint32_t tb = t + half * 128;
     float amax = 0.0f;
 #pragma unroll 1
@@ -136,74 +156,107 @@ __device__ __forceinline__ void fwd_row(const SwigluArgs& args, uint32_t t, int 
     float s, inv;
     e4m3_block_scale(amax, s, inv);
     const long long block = half * (N / 128) + n0 / 128;
-    if (valid) args.gus[block * args.M + row] = s;
-    uint4* pq = reinterpret_cast<uint4*>(args.guq + row * 2 * N + block * 128);
+    if (lane < rows) args.gus[block * args.M + row0 + lane] = s;
+    uint8_t* g = args.guq + row0 * 2 * N + block * 128;
 #pragma unroll 1
     for (int cc = 0; cc < 4; ++cc) {
       uint32_t r[32];
       tmem_ld_32x32(tb + 32 * cc, r);
       tmem_ld_wait();
-      if (valid) {
+      // 64 codes fill a box
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t q[4];
+      for (int j = 0; j < 2; ++j) {
+        uint32_t q[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int c = 16 * j + 4 * k;
-            q[k] = e4m3x2(__fmul_rn(__uint_as_float(r[c]), inv), __fmul_rn(__uint_as_float(r[c + 1]), inv)) |
-                   (e4m3x2(__fmul_rn(__uint_as_float(r[c + 2]), inv), __fmul_rn(__uint_as_float(r[c + 3]), inv))
-                    << 16);
-          }
-          pq[2 * cc + j] = make_uint4(q[0], q[1], q[2], q[3]);
+        for (int k = 0; k < 4; ++k) {
+          const int c = 16 * j + 4 * k;
+          q[k] = e4m3x2(__fmul_rn(__uint_as_float(r[c]), inv), __fmul_rn(__uint_as_float(r[c + 1]), inv)) |
+                 (e4m3x2(__fmul_rn(__uint_as_float(r[c + 2]), inv), __fmul_rn(__uint_as_float(r[c + 3]), inv)) << 16);
         }
+        Box64::put(box0, lane, 2 * (cc & 1) + j, make_uint4(q[0], q[1], q[2], q[3]));
+      }
+      if (cc & 1) {
+        __syncwarp();
+        Box64::store(box0, g + 32 * (cc - 1), 2 * N, rows, lane);
+        __syncwarp();
       }
     }
   }
 }
 
-// Row `row` of the backward's outputs, BN/2 columns from column `col0`, from
-// dh at TMEM address `t`.
-template <int BN, bool E4M3>
-__device__ __forceinline__ void bwd_row(const SwigluArgs& args, uint32_t t, long long row, bool valid, int col0) {
-  const long long N = args.N;
-  float sa = 0.0f, sb = 0.0f;
-  if (E4M3 && valid) {
-    sa = args.gus[static_cast<long long>(col0 / 128) * args.M + row];
-    sb = args.gus[static_cast<long long>(N / 128 + col0 / 128) * args.M + row];
+// Backward: 32 columns at a time of the kept gate and up.
+template <bool E4M3>
+struct Kept32 {
+  using Box = std::conditional_t<E4M3, Box32, Box64>;
+  uint4 a[Box::kSweeps], b[Box::kSweeps];
+  __device__ __forceinline__ void fetch(const SwigluArgs& args, long long row0, int rows, int col, int lane) {
+    const long long N = args.N;
+    constexpr int kElem = E4M3 ? 1 : 2;
+    const uint8_t* g = (E4M3 ? args.guq : reinterpret_cast<const uint8_t*>(args.gu)) + (row0 * 2 * N + col) * kElem;
+    Box::fetch(a, g, 2 * N * kElem, rows, lane);
+    Box::fetch(b, g + N * kElem, 2 * N * kElem, rows, lane);
   }
+};
+
+// Backward: COLS columns from `col0` on, dh at tensor memory address `t`;
+// `next` holds the first 32 columns of the kept values.
+template <int COLS, bool E4M3>
+__device__ __forceinline__ void bwd_rows(const SwigluArgs& args, uint8_t* stage, uint32_t t, int lane, long long row0,
+                                         int rows, int col0, Kept32<E4M3>& next, float sa, float sb) {
+  using Box = typename Kept32<E4M3>::Box;
+  const long long N = args.N, ldh = 2 * N, ldg = 4 * N;
+  uint8_t* box0 = stage;
+  uint8_t* box1 = stage + Box64::kBytes;
 #pragma unroll 1
-  for (int cc = 0; cc < BN / 64; ++cc) {
+  for (int cc = 0; cc < COLS / 32; ++cc) {
     const int col = col0 + 32 * cc;
+    Box::put_sweeps(box0, next.a, lane);
+    Box::put_sweeps(box1, next.b, lane);
+    __syncwarp();
+    float a[32], b[32];
+    if (E4M3) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint4 ca = Box32::get(box0, lane, j), cb = Box32::get(box1, lane, j);
+        unpack8_e4m3(make_uint2(ca.x, ca.y), sa, a + 16 * j);
+        unpack8_e4m3(make_uint2(ca.z, ca.w), sa, a + 16 * j + 8);
+        unpack8_e4m3(make_uint2(cb.x, cb.y), sb, b + 16 * j);
+        unpack8_e4m3(make_uint2(cb.z, cb.w), sb, b + 16 * j + 8);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        unpack8(Box64::get(box0, lane, j), a + 8 * j);
+        unpack8(Box64::get(box1, lane, j), b + 8 * j);
+      }
+    }
+    __syncwarp();
+    if (cc + 1 < COLS / 32) next.fetch(args, row0, rows, col + 32, lane);
     uint32_t r[32];
     tmem_ld_32x32(t + 32 * cc, r);
     tmem_ld_wait();
-    if (valid) {
+    float da[32];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float a[8], b[8], da[8], db[8], hv[8];
-        if (E4M3) {
-          const uint8_t* p = args.guq + row * 2 * N + col + 8 * j;
-          unpack8_e4m3(*reinterpret_cast<const uint2*>(p), sa, a);
-          unpack8_e4m3(*reinterpret_cast<const uint2*>(p + N), sb, b);
-        } else {
-          const uint16_t* p = args.gu + row * 2 * N + col + 8 * j;
-          unpack8(*reinterpret_cast<const uint4*>(p), a);
-          unpack8(*reinterpret_cast<const uint4*>(p + N), b);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float dh = __uint_as_float(r[8 * j + i]);
-          const float sg = logistic(a[i]);
-          const float act = a[i] * sg;
-          hv[i] = act * b[i];
-          db[i] = dh * act;
-          da[i] = dh * b[i] * sg * (1.0f + a[i] * (1.0f - sg));
-        }
-        uint16_t* o = args.dgu + row * 2 * N + col + 8 * j;
-        *reinterpret_cast<uint4*>(o) = pack8(da);
-        *reinterpret_cast<uint4*>(o + N) = pack8(db);
-        if (args.h) *reinterpret_cast<uint4*>(args.h + row * N + col + 8 * j) = pack8(hv);
-      }
+    for (int i = 0; i < 32; ++i) {
+      const float dh = __uint_as_float(r[i]);
+      const float sg = logistic(a[i]);
+      const float act = a[i] * sg;
+      da[i] = dh * b[i] * sg * (1.0f + a[i] * (1.0f - sg));
+      a[i] = dh * act;    // up's gradient
+      b[i] = act * b[i];  // h
+    }
+    put32(box0, lane, da);
+    put32(box1, lane, a);
+    __syncwarp();
+    uint8_t* g = reinterpret_cast<uint8_t*>(args.dgu + row0 * 2 * N + col);
+    Box64::store(box0, g, ldg, rows, lane);
+    Box64::store(box1, g + 2 * N, ldg, rows, lane);
+    __syncwarp();
+    if (args.h) {
+      put32(box0, lane, b);
+      __syncwarp();
+      Box64::store(box0, reinterpret_cast<uint8_t*>(args.h + row0 * N + col), ldh, rows, lane);
+      __syncwarp();
     }
   }
 }
@@ -221,7 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kOutCols = FWD ? 128 : BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * C::kStageBytes);
+  uint8_t* staging = ring + kStages * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::kStagingBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
@@ -266,31 +320,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int KS = args.K / 64;
   const uint64_t lim = args.wait_limit_ns;
 
+  if (warp < kEpiWarp0) regs_dec<kControlRegs>();
   if (warp == 0) {
     if (lane == 0) {
+      // one K step's boxes
+      const auto boxes = [&](const int4& u, int ks, auto&& box) {
+        const int n0 = u.w * kOutCols;
+        box(&map_a, 0, ks * 64, u.y);
+        if (FWD) {
+          const int wrow = u.x * args.K + ks * 64;  // row of the [G*K, 2N] weight view
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            box(&map_b, C::kABytes + j * C::kBoxBytes, (j >> 1) * args.N + n0 + 64 * (j & 1), wrow);
+        } else {
+          box(&map_b, C::kABytes, ks * 64, u.x * args.N + n0);
+        }
+      };
+      RingPos<kStages> r;
       uint32_t c = 0;
       bool ok = true;
       int4 e;
       for (uint32_t i = 0; ok && queue.get(i, e, false, 0, abort_word, lim) && e.x >= 0; ++i) {
-        const int n0 = e.w * kOutCols;
         for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t s = c % kStages, ph = (c / kStages) & 1u;
-          if (!mbar_wait(&empty[s], ph ^ 1u, abort_word, lim)) {
+          if (!mbar_wait(&empty[r.slot], r.phase ^ 1u, abort_word, lim)) {
             ok = false;
             break;
           }
-          uint8_t* a_dst = ring + s * C::kStageBytes;
-          uint8_t* b_dst = a_dst + C::kABytes;
-          mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-          tma_load_2d(a_dst, &map_a, &full[s], ks * 64, e.y);
-          if (FWD) {
-            const int wrow = e.x * args.K + ks * 64;  // row of the [G*K, 2N] weight view
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tma_load_2d(b_dst + j * C::kBoxBytes, &map_b, &full[s], (j >> 1) * args.N + n0 + 64 * (j & 1), wrow);
-          } else {
-            tma_load_2d(b_dst, &map_b, &full[s], ks * 64, e.x * args.N + n0);
-          }
+          uint8_t* dst = ring + r.slot * C::kStageBytes;
+          uint64_t* bar = &full[r.slot];
+          mbar_arrive_expect_tx(bar, C::kStageBytes);
+          boxes(e, ks, [&](const CUtensorMap* map, int at, int x, int y) { tma_load_2d(dst + at, map, bar, x, y); });
+          r.advance();
           ++c;
         }
       }
@@ -304,38 +364,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
+    // The tensor core's queue is short: whatever this thread does between two
+    // steps' products beyond some 200 cycles is time without products, so the
+    // loop keeps running positions and descriptor words instead of deriving them.
     if (lane == 0) {
       constexpr uint32_t idesc = make_idesc(1u /*bf16*/, false, FWD, kBM, BN);
-      uint32_t c = 0, t = 0;
-      bool ok = true;
+      const uint32_t a_lo0 = desc_lo_sw128(smem_u32(ring), 16);
+      const uint32_t b_lo0 = desc_lo_sw128(smem_u32(ring) + C::kABytes, FWD ? C::kBoxBytes : 16);
+      constexpr uint32_t kBStep = (FWD ? 2048 : 32) >> 4;
+      RingPos<kStages> r;
+      RingPos<2> acc;
+      bool ok = true, any = false, next_ready = false;
       int4 e;
       for (uint32_t i = 0; ok && queue.get(i, e, false, 0, abort_word, lim) && e.x >= 0; ++i) {
-        const uint32_t b = t & 1u, tph = (t >> 1) & 1u;
-        if (!mbar_wait(&tempty[b], tph ^ 1u, abort_word, lim)) break;
-        const uint32_t d = tbase + b * BN;
+        if (!mbar_wait(&tempty[acc.slot], acc.phase ^ 1u, abort_word, lim)) break;
+        tc_fence_after();
+        const uint32_t d = tbase + acc.slot * BN;
         for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t s = c % kStages, ph = (c / kStages) & 1u;
-          if (!mbar_wait(&full[s], ph, abort_word, lim)) {
+          if (!next_ready && !mbar_wait(&full[r.slot], r.phase, abort_word, lim)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t a_addr = smem_u32(ring + s * C::kStageBytes);
-          const uint32_t b_addr = a_addr + C::kABytes;
+          const uint32_t a_lo = a_lo0 + r.slot * (C::kStageBytes >> 4);
+          const uint32_t b_lo = b_lo0 + r.slot * (C::kStageBytes >> 4);
+          uint64_t* freed = &empty[r.slot];
+          r.advance();
+          next_ready = mbar_test(&full[r.slot], r.phase);  // answered while the products are issued
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint64_t bdesc = FWD ? smem_desc_sw128(b_addr + 2048 * j, C::kBoxBytes, 1024)
-                                       : smem_desc_sw128(b_addr + 32 * j, 16, 1024);
-            mma_bf16(d, smem_desc_sw128(a_addr + 32 * j, 16, 1024), bdesc, idesc, (ks > 0 || j > 0) ? 1u : 0u);
-          }
-          mma_commit(&empty[s]);
-          ++c;
+          for (uint32_t j = 0; j < 4; ++j)
+            mma_bf16(d, desc_sw128(a_lo + 2 * j), desc_sw128(b_lo + kBStep * j), idesc, (ks > 0 || j > 0) ? 1u : 0u);
+          mma_commit(freed);
+          any = true;
         }
         if (!ok) break;
-        mma_commit(&tfull[b]);
-        ++t;
+        mma_commit(&tfull[acc.slot]);
+        acc.advance();
       }
-      if (c > 0) {
+      if (any) {
         volatile int no_abort = 0;
         mma_commit(drain);
         mbar_wait(drain, 0, &no_abort, kDrainLimitNs);
@@ -346,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       queue.schedule(args.tiles, const_cast<int32_t*>(args.meta) + kWsClaimed, num_units,
                      static_cast<uint32_t>(per_tile), abort_word, lim);
   } else if (warp >= kEpiWarp0) {
+    regs_inc<kEpiRegs>();
     const int half = (warp - kEpiWarp0) >> 2;
     const int quad = warp & 3;  // TMEM lane quadrant this warp may access
     const int tid = static_cast<int>(threadIdx.x) - 32 * kEpiWarp0;
@@ -365,23 +431,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         zero_span(args.gu + S * 2 * N, rest * N * 4, tid);
       }
     }
-    uint32_t t = 0;
+    uint8_t* stage = staging + (warp - kEpiWarp0) * 4096;
+    RingPos<2> acc;
     int4 e;
     for (uint32_t i = 0; queue.get(i, e, true, lane, abort_word, lim) && e.x >= 0; ++i) {
-      const int row = e.y + quad * 32 + lane;
-      const bool valid = row < e.z;
-      const uint32_t b = t & 1u, tph = (t >> 1) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[b], tph, abort_word, lim))) break;
+      const long long row0 = e.y + quad * 32;
+      const int rows = min(32, e.z - static_cast<int>(row0));  // of this warp; may be <= 0
+      const int col0 = e.w * kOutCols + (FWD ? 0 : half * (BN / 2));
+      Kept32<E4M3> kept;
+      float sa = 0.0f, sb = 0.0f;
+      if (!FWD) {  // read while the products run
+        kept.fetch(args, row0, rows, col0, lane);
+        if (E4M3 && lane < rows) {
+          sa = args.gus[(col0 / 128) * static_cast<long long>(args.M) + row0 + lane];
+          sb = args.gus[(N / 128 + col0 / 128) * args.M + row0 + lane];
+        }
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc.slot], acc.phase, abort_word, lim))) break;
       tc_fence_after();
-      const uint32_t tb = t_lane + b * BN;
-      if (FWD)
-        fwd_row<E4M3>(args, tb, half, valid ? row : 0, valid, e.w * 128);
-      else
-        bwd_row<BN, E4M3>(args, tb + half * (BN / 2), valid ? row : 0, valid, e.w * BN + half * (BN / 2));
+      const uint32_t tb = t_lane + acc.slot * BN;
+      if (rows > 0) {
+        if (FWD)
+          fwd_rows<E4M3>(args, stage, tb, half, lane, row0, rows, col0);
+        else
+          bwd_rows<BN / 2, E4M3>(args, stage, tb + half * (BN / 2), lane, row0, rows, col0, kept, sa, sb);
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[b]);
-      ++t;
+      if (lane == 0) mbar_arrive(&tempty[acc.slot]);
+      acc.advance();
     }
   }
 
@@ -398,8 +476,8 @@ template <int BN, bool FWD, bool E4M3>
 cudaError_t launch(const CUtensorMap& map_a, const CUtensorMap& map_b, const SwigluArgs& args, int grid,
                    cudaStream_t stream) {
   constexpr int smem = SwigluTile<BN>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(gmm_swiglu_kernel<BN, FWD, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(gmm_swiglu_kernel<BN, FWD, E4M3>, smem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(gmm_swiglu_kernel<BN, FWD, E4M3>, dim3(grid), dim3(kThreads), smem, stream, map_a, map_b, args);
 }

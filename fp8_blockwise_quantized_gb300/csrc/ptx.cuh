@@ -65,6 +65,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
   return ok != 0;
 }
 
+// Whether that phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for the phase of `bar` with the given parity to complete, for at most
 // `limit_ns` nanoseconds.  Every 64 polls the shared abort word is checked, so
 // that when one role of the CTA gives up, the others stop waiting too.
@@ -158,6 +171,14 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
 
 // x is the innermost coordinate (elements); it must be a multiple of
 // 16 bytes / element size, which every caller guarantees by construction.
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
                                             int32_t y) {
   asm volatile(
@@ -172,20 +193,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
 // landed (.noinc: the barrier's expected count already includes it).
 __device__ __forceinline__ void cp_async_4(void* sdst, const void* gsrc) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sdst)), "l"(gsrc) : "memory");
-}
-// 8- and 16-byte ones (addresses aligned to their size)
-__device__ __forceinline__ void cp_async_8(void* sdst, const void* gsrc) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(sdst)), "l"(gsrc) : "memory");
-}
-__device__ __forceinline__ void cp_async_16(void* sdst, const void* gsrc) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(sdst)), "l"(gsrc) : "memory");
-}
-// this thread's cp.async copies so far form a group; wait until at most N
-// groups are still in flight
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait_group() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -293,13 +300,6 @@ __device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t a_desc, uint64
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
       : "memory");
 }
-// Copy of 32 rows x 16 bytes from shared memory to the 32 lanes x 4 columns at
-// `d_tmem`, repeated in the tensor memory's four lane quarters.  Runs in order
-// with the MMAs that the same thread issues after it.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t d_tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d_tmem), "l"(desc) : "memory");
-}
-
 // The mbarrier gets one arrival once every tcgen05 operation this thread has
 // issued so far has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -363,6 +363,18 @@ __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// 32 lanes x 16 columns of 32-bit: thread i of the warp writes row (lane base +
+// i), columns [col, col + 16).
+__device__ __forceinline__ void tmem_st_32x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Re-split the register file between warpgroups (all warps of a warpgroup
 // execute the same instruction).  The launch gives every thread the same
 // count; the decreasing warpgroups must free at least what the increasing
@@ -400,12 +412,24 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
-// Shared-memory descriptor of contiguous 16-byte rows without swizzle: 8-row
-// groups 128 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
-         (static_cast<uint64_t>(1) << 46);
+// The same in two words: the low one (start address and LBO), to which a step
+// of 16 bytes adds 1, and the constant high one for 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint32_t desc_lo_sw128(uint32_t saddr, uint32_t lbo) {
+  return (saddr >> 4) | ((lbo >> 4) << 16);
 }
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t lo) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+// A position in a ring of N slots and the parity of its phase.
+template <int N>
+struct RingPos {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == N) slot = 0, phase ^= 1u;
+  }
+};
 
 // Instruction descriptor for kind::f16 / kind::f8f6f4 with an fp32 accumulator.
 //   bits 4-5: D format (1 = f32); bits 7-9 / 10-12: A / B format

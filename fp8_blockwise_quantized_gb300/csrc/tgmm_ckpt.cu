@@ -12,13 +12,14 @@
 //
 // A cluster of two CTAs on the two SMs of a pair owns the tile (g, 256 rows of
 // K, 256 columns of N) and walks the group's rows in chunks of 64; each CTA
-// holds 128 k columns and 128 n columns (512 threads):
+// holds 128 k columns and 128 n columns (608 threads):
 //   warp 0       TMA: the chunk's codes (64 x 128 bytes) and dy (two 64 x 64
 //                boxes) into a ring of kRing slots
-//   warps 12-15  expand the codes to bf16 (MN-major 128-byte swizzled boxes)
-//                into one of kOper operand buffers; rows past the group's end
-//                become zeros there, and in dy, whatever the rows of the next
-//                group hold
+//   warps 11-18  expand the codes to bf16 (MN-major 128-byte swizzled boxes)
+//                into one of kOper operand buffers, two groups of four warps
+//                taking every other chunk; rows past the group's end become
+//                zeros there, and in dy, whatever the rows of the next group
+//                hold
 //   warp 1       even CTA: one M=256 tcgen05.mma (cta_group::2) per 16 rows
 //                over both CTAs' shared memory
 //   warps 2-9    epilogue: 128 k rows x 256 columns per CTA, as bf16 boxes
@@ -35,16 +36,17 @@ namespace gmm {
 namespace {
 
 constexpr int BN = 256;
-constexpr int kThreads = 512;
+constexpr int kThreads = 608;
 constexpr int kEpiWarps = 8;
 constexpr int kSchedWarp = 10;
-constexpr int kExpandWarp0 = 12;
-constexpr int kExpandWarps = 4;
-constexpr int kRing = 6;
-constexpr int kOper = 3;
+constexpr int kExpandWarp0 = 11;
+constexpr int kExpandWarps = 4;  // per group
+constexpr int kGroups = 2;
+constexpr int kRing = 5;
+constexpr int kOper = 4;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
 // producer, epilogue and expanding warps of both CTAs, and the MMA issuer
-constexpr int kReaders = 2 * (1 + kEpiWarps + kExpandWarps) + 1;
+constexpr int kReaders = 2 * (1 + kEpiWarps + kGroups * kExpandWarps) + 1;
 
 constexpr int kBoxBytes = kChunk * 128;      // 64 rows x 128 bytes
 constexpr int kSlotBytes = 3 * kBoxBytes;    // codes, two boxes of dy
@@ -271,7 +273,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= kExpandWarp0) {
     // thread: row `row` of the chunk, 64 of its 128 codes (half `hb`)
     const int et = static_cast<int>(threadIdx.x) - 32 * kExpandWarp0;
-    const int row = et >> 1, hb = et & 1;
+    const uint32_t group = static_cast<uint32_t>(et) / (32 * kExpandWarps);
+    const int row = et % (32 * kExpandWarps) >> 1, hb = et & 1;
     const uint32_t ready0 = mapa_shared(smem_u32(ready), 0);
     uint32_t c = 0;
     bool ok = true;
@@ -280,10 +283,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int k0 = (e.y / NT) * 256 + static_cast<int>(rank) * 128;
       const float* xs = args.xs + static_cast<long long>(k0 / 128) * args.M;
       const bool inside = k0 < args.K;
-      float next = inside && e.z + row < e.w ? __ldg(xs + e.z + row) : 0.0f;
-      for (int r = e.z; r < e.w; r += kChunk) {
+      // this group's chunks of the unit; a chunk's scale is loaded one ahead
+      const int mine = (c % kGroups == group ? 0 : kChunk) + row;
+      float next = inside && e.z + mine < e.w ? __ldg(xs + e.z + mine) : 0.0f;
+      for (int r = e.z; r < e.w; r += kChunk, ++c) {
+        if (c % kGroups != group) continue;
         const float scale = next;
-        next = inside && r + kChunk + row < e.w ? __ldg(xs + r + kChunk + row) : 0.0f;
+        const int ahead = r + kGroups * kChunk + row;
+        next = inside && ahead < e.w ? __ldg(xs + ahead) : 0.0f;
         const int live = e.w - r;
         const uint32_t s = c % kRing, j = c % kOper;
         bool got = mbar_wait(&full[s], (c / kRing) & 1u, abort_word, lim);
@@ -324,7 +331,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();  // the tensor core reads what was written here
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(ready0 + j * 8u);
-        ++c;
       }
     }
   }
@@ -354,18 +360,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_tgmm_ckpt(const CUtensorMap& map_x, const CUtensorMap& map_dy, const CUtensorMap& map_dw,
                              const TgmmArgs& args, int max_pairs, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(tgmm_ckpt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> resident[64];
+  cudaError_t e = allow_smem(tgmm_ckpt_kernel, kSmemBytes, done);
+  int dev = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // as many pairs as can be resident at once (one CTA per SM)
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * max_pairs, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  int clusters = 0;
-  e = cudaOccupancyMaxActiveClusters(&clusters, tgmm_ckpt_kernel, &cfg);
-  if (e != cudaSuccess) return e;
-  if (clusters < 1) return cudaErrorInvalidConfiguration;
+  // as many pairs as can be resident at once (one CTA per SM), asked once per device
+  int clusters = resident[dev & 63].load(std::memory_order_relaxed);
+  if (clusters == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 1024, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    e = cudaOccupancyMaxActiveClusters(&clusters, tgmm_ckpt_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    resident[dev & 63].store(clusters, std::memory_order_relaxed);
+  }
   const int pairs = clusters < max_pairs ? clusters : max_pairs;
   return launch_pdl(tgmm_ckpt_kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, stream, map_x, map_dy, map_dw,
                     args);

@@ -10,7 +10,7 @@
 
 namespace gmm {
 
-constexpr int kClaimSlots = 4;  // entries of a CTA's unit queue
+constexpr int kClaimSlots = 2;  // entries of a CTA's unit queue
 
 // The queue of one CTA.  An entry is {g, row0, row1, column block}; g < 0:
 // no more units.  READERS roles (warps, or single threads) take the entries
@@ -36,28 +36,40 @@ struct ClaimQueue {
     if (lane == 0) mbar_arrive(&empty[slot]);
     return true;
   }
+  // Entry i, for a look ahead, if it is there already; it stays in the queue.
+  __device__ bool peek(uint32_t i, int4& e) const {
+    if (!mbar_test(&full[i % kClaimSlots], (i / kClaimSlots) & 1u)) return false;
+    e = data[i % kClaimSlots];
+    return e.x >= 0;
+  }
   // Scheduler (one thread): the CTA's first unit is its block index, the next
-  // ones are claimed from the workspace counter, one claim in flight while the
-  // current unit is published (a CTA that runs slower takes fewer units).
+  // ones are claimed from the workspace counter (a CTA that runs slower takes
+  // fewer units), two claims and the next unit's tile in flight while a unit
+  // is published: one claim at a time takes about 1 us a unit.
   // Unit u is row tile u / per_tile, column block u % per_tile.
   __device__ void schedule(const Tile* tiles, int* claimed, uint32_t num_units, uint32_t per_tile,
                            volatile int* abort_word, uint64_t lim) const {
-    uint32_t u = blockIdx.x;
+    const auto tile = [&](uint32_t u) {
+      return u < num_units ? __ldg(reinterpret_cast<const int4*>(tiles + u / per_tile)) : make_int4(-1, 0, 0, 0);
+    };
+    const auto claim = [&]() { return gridDim.x + static_cast<uint32_t>(atomicAdd(claimed, 1)); };
+    uint32_t u = blockIdx.x, u1 = num_units, u2 = num_units;
+    if (u < num_units) {
+      u1 = claim();
+      u2 = claim();
+    }
+    int4 t = tile(u);
     for (uint32_t i = 0;; ++i) {
-      const bool live = u < num_units;
-      uint32_t next = 0;
-      if (live) next = gridDim.x + static_cast<uint32_t>(atomicAdd(claimed, 1));
-      int4 ent = make_int4(-1, 0, 0, 0);
-      if (live) {
-        const int4 t = __ldg(reinterpret_cast<const int4*>(tiles + u / per_tile));
-        ent = make_int4(t.x, t.y, t.z, static_cast<int>(u % per_tile));
-      }
       const uint32_t slot = i % kClaimSlots, ph = (i / kClaimSlots) & 1u;
       if (!mbar_wait(&empty[slot], ph ^ 1u, abort_word, lim)) return;
-      data[slot] = ent;
+      t.w = static_cast<int>(u % per_tile);
+      data[slot] = t;
       mbar_arrive(&full[slot]);
-      if (!live) return;
-      u = next;
+      if (u >= num_units) return;
+      u = u1;
+      u1 = u2;
+      if (u2 < num_units) u2 = claim();
+      t = tile(u);
     }
   }
 };
