@@ -339,7 +339,7 @@ class Workspace:
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
 
     def fits(self, G: int, M: int) -> bool:
-        return gmm_workspace_bytes(G, M) <= self.nbytes
+        return (G == self.G and M == self.M) or gmm_workspace_bytes(G, M) <= self.nbytes
 
     def status(self, stream=None) -> int:
         return gmm_get_device_status(self.buf, stream)
@@ -544,6 +544,15 @@ def group_metadata(group_sizes, M, workspace=None, stream=None) -> Workspace:
     return ws_
 
 
+def _new2(a, b, dtype, device):
+    """torch.empty((a, b)) by way of empty_strided, which takes half the host time."""
+    return torch.empty_strided((a, b), (b, 1), dtype=dtype, device=device)
+
+
+def _new3(a, b, c, dtype, device):
+    return torch.empty_strided((a, b, c), (b * c, c, 1), dtype=dtype, device=device)
+
+
 def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=None):
     """The gated block's forward: x bf16 [M, K], w bf16 [G, K, 2N] (gate | up)
     -> (h bf16 [M, N], kept), kept being what swiglu_bwd takes: the gate | up
@@ -559,12 +568,11 @@ def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=
     if out is not None:
         h, kept = out
     else:
-        h = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        h = _new2(M, N, torch.bfloat16, x.device)
         if keep == "bf16":
-            kept = torch.empty((M, Nw), dtype=torch.bfloat16, device=x.device)
+            kept = _new2(M, Nw, torch.bfloat16, x.device)
         else:
-            kept = (torch.empty((M, Nw), dtype=torch.uint8, device=x.device),
-                    torch.empty((Nw // 128, M), dtype=torch.float32, device=x.device))
+            kept = (_new2(M, Nw, torch.uint8, x.device), _new2(Nw // 128, M, torch.float32, x.device))
     gu, (guq, gus) = (kept, (None, None)) if keep == "bf16" else (None, kept)
     ws_ = _ws_for(group_sizes, workspace, G, M, x.device)
     _check(gmm_bf16_swiglu_fwd(x, w, group_sizes, G, M, K, N, h, gu, guq, gus, ws_.buf, ws_.nbytes, stream),
@@ -585,8 +593,8 @@ def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=No
     if out is not None:
         dgu, h = out
     else:
-        dgu = torch.empty((M, 2 * N), dtype=torch.bfloat16, device=dy.device)
-        h = torch.empty((M, N), dtype=torch.bfloat16, device=dy.device) if with_h else None
+        dgu = _new2(M, 2 * N, torch.bfloat16, dy.device)
+        h = _new2(M, N, torch.bfloat16, dy.device) if with_h else None
     ws_ = _ws_for(group_sizes, workspace, G, M, dy.device)
     _check(gmm_bf16_swiglu_bwd(dy, w2, gu, guq, gus, group_sizes, G, M, K, N, dgu, h, ws_.buf, ws_.nbytes, stream),
            "gmm_bf16_swiglu_bwd")
@@ -608,7 +616,7 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     else:
         raise ValueError("group_sizes=None reuses the metadata in `workspace`: pass that workspace")
     if dw is None:
-        dw = torch.empty((G, K, N), dtype=torch.bfloat16, device=dy.device)
+        dw = _new3(G, K, N, torch.bfloat16, dy.device)
     ws_ = _ws_for(group_sizes, workspace, G, M, dy.device)
     _check(tgmm_fp8_ckpt(xq, xs, dy, group_sizes, G, M, K, N, dw, ws_.buf, ws_.nbytes, stream), "tgmm_fp8_ckpt")
     return dw
@@ -620,8 +628,8 @@ def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
     if out is not None:
         xq, xs = out
     else:
-        xq = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-        xs = torch.empty((K // 128, M, 4), dtype=torch.uint8, device=x.device)
+        xq = _new2(M, K // 2, torch.uint8, x.device)
+        xs = _new3(K // 128, M, 4, torch.uint8, x.device)
     _check(gmm_mx4_quantize_lhs(x, M, K, xq, xs, stream), "gmm_mx4_quantize_lhs")
     return xq, xs
 
@@ -629,7 +637,7 @@ def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
 def mx4_quantize_rhs(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq uint8 [G, N, K/2] packed E2M1 codes, ws uint8 [G, N/128, K/128, 512] E8M0 scales)."""
     G, K, N = w.shape
-    wq = torch.empty((G, N, K // 2), dtype=torch.uint8, device=w.device)
+    wq = _new3(G, N, K // 2, torch.uint8, w.device)
     ws = torch.empty((G, N // 128, K // 128, 512), dtype=torch.uint8, device=w.device)
     _check(gmm_mx4_quantize_rhs(w, G, K, N, wq, ws, stream), "gmm_mx4_quantize_rhs")
     return wq, ws
@@ -642,7 +650,7 @@ def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, s
     assert K3 == K2
     N = Nw // 2 if fuse else Nw
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        out = _new2(M, N, torch.bfloat16, xq.device)
     ws_ = _ws_for(group_sizes, workspace, G, M, xq.device)
     _check(gmm_mx4_fwd(xq, xs, wq, ws, group_sizes, G, M, 2 * K2, N, fuse, out, ws_.buf, ws_.nbytes, stream),
            "gmm_mx4_fwd")
@@ -659,9 +667,9 @@ def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
     if out is not None:
         h, hq, hs = out
     else:
-        h = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device) if with_h else None
-        hq = torch.empty((M, N // 2), dtype=torch.uint8, device=xq.device)
-        hs = torch.empty((N // 128, M, 4), dtype=torch.uint8, device=xq.device)
+        h = _new2(M, N, torch.bfloat16, xq.device) if with_h else None
+        hq = _new2(M, N // 2, torch.uint8, xq.device)
+        hs = _new3(N // 128, M, 4, torch.uint8, xq.device)
     ws_ = _ws_for(group_sizes, workspace, G, M, xq.device)
     _check(gmm_mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, G, M, 2 * K2, N, h, hq, hs, ws_.buf, ws_.nbytes,
                                     stream), "gmm_mx4_fwd_swiglu_quant")

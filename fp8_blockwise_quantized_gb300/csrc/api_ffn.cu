@@ -69,7 +69,11 @@ gmm_status mx4_entry(const void* xq, const void* xs, const void* wq, const void*
   int sms = 0;
   if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
   if (M == 0) return GMM_OK;
-  const int bn = (fuse || N % 256 == 0) && max_tiles(G, M) * (Nw / 256) >= sms ? 256 : 128;
+  // 128-column units while one per SM covers the call: latency (8 row tiles, K
+  // 2048, N 2 x 512: 8.4 us, 9.2 with 256; 128 units of K 512: 6.3 and 6.5).
+  // Beyond that 256: half the reads of x (256 units of 128 columns: 11.4 to
+  // 15.0 us, 128 of 256: 9.9 to 11.8).
+  const int bn = (fuse || N % 256 == 0) && max_tiles(G, M) * (Nw / 128) > sms ? 256 : 128;
   CUtensorMap map_a, map_b, map_out;
   if ((st = host_encode_2d(&map_a, kByte, 1, xq, K / 2, M, 128, 128)) != GMM_OK) return st;
   if ((st = host_encode_2d(&map_b, kByte, 1, wq, K / 2, G * Nw, 128, fuse ? bn / 2 : bn)) != GMM_OK) return st;
@@ -109,7 +113,7 @@ gmm_status gmm_bf16_swiglu_fwd(const void* x, const void* w, const int32_t* grou
   if (!w || (M > 0 && (!x || !h))) return GMM_ERR_NULL;
   if ((st = check_kept(M, gu, guq, gus)) != GMM_OK) return st;
   if (!all_aligned(x, w, group_sizes, h, gu, guq, gus)) return GMM_ERR_ALIGN;
-  const long long units = max_tiles(G, M) * (N / 128);
+  const long long units = max_tiles(G, M) * (N / 64);  // narrow ones
   if (units > kMaxUnits) return GMM_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = 0;
@@ -141,8 +145,7 @@ gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, c
   if (!w2 || (M > 0 && (!dy || !dgu))) return GMM_ERR_NULL;
   if ((st = check_kept(M, gu, guq, gus)) != GMM_OK) return st;
   if (!all_aligned(dy, w2, gu, guq, gus, group_sizes, dgu, h)) return GMM_ERR_ALIGN;
-  const int bn = swiglu_bwd_bn(static_cast<int>(N));
-  const long long units = max_tiles(G, M) * (N / bn);
+  const long long units = max_tiles(G, M) * (N / 128);  // narrow ones
   if (units > kMaxUnits) return GMM_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = 0;
@@ -150,7 +153,7 @@ gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, c
   if (M == 0) return GMM_OK;
   CUtensorMap map_dy, map_w2;
   if ((st = host_encode_2d(&map_dy, kBf16, 2, dy, K, M, 64, 128)) != GMM_OK) return st;
-  if ((st = host_encode_2d(&map_w2, kBf16, 2, w2, K, G * N, 64, bn)) != GMM_OK) return st;
+  if ((st = host_encode_2d(&map_w2, kBf16, 2, w2, K, G * N, 64, 128)) != GMM_OK) return st;
   SwigluArgs a{};
   a.meta = static_cast<const int32_t*>(workspace);
   a.tiles = tiles_of(workspace, G);
@@ -207,11 +210,15 @@ gmm_status gmm_mx4_quantize_lhs(const void* x, int64_t M, int64_t K, void* xq, v
   gmm_status st = host_device_sms(&sms);
   if (st != GMM_OK) return st;
   const long long steps = (M + 7) / 8 * (K / 128);  // a warp each, 8 warps per CTA
+  if (steps >= (1LL << 31)) return GMM_ERR_SHAPE;   // 4 TB of x
   long long grid = (steps + 7) / 8;
-  if (grid > static_cast<long long>(sms) * 8) grid = static_cast<long long>(sms) * 8;
+  // many short CTAs: 65536 x 2048 takes 59.8 us with 32 per SM, 63.4 with 16,
+  // 67.0 with 8 and 64.5 with one step per warp
+  if (grid > static_cast<long long>(sms) * 32) grid = static_cast<long long>(sms) * 32;
   return launched(launch_pdl(mx4_quantize_lhs_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
                              static_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), static_cast<int>(M),
-                             static_cast<int>(K / 128), static_cast<uint32_t*>(xq), static_cast<uint32_t*>(xs)),
+                             static_cast<uint32_t>(K / 128), static_cast<uint32_t>(steps), static_cast<uint32_t*>(xq),
+                             static_cast<uint32_t*>(xs)),
                   "mx4_quantize_lhs_kernel launch");
 }
 

@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();  // inputs and metadata come from earlier kernels
 
-  const int per_tile = args.N / kOutCols;
-  const uint32_t num_units = static_cast<uint32_t>(args.meta[kWsNumTiles]) * static_cast<uint32_t>(per_tile);
+  const uint32_t per_tile = args.N / kOutCols;
+  const uint32_t num_units = static_cast<uint32_t>(args.meta[kWsNumTiles]) * per_tile;
   const int KB = args.K / 128, KS = (KB + 1) / 2;
   const int Nw = FUSE ? 2 * args.N : args.N;
   const uint64_t lim = args.wait_limit_ns;
@@ -246,8 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kEpiWarp0) {
     if (warp == 2 && lane == 0)  // warp 3 has no role
-      queue.schedule(args.tiles, const_cast<int32_t*>(args.meta) + kWsClaimed, num_units,
-                     static_cast<uint32_t>(per_tile), abort_word, lim);
+      queue.schedule(
+          args.tiles, const_cast<int32_t*>(args.meta) + kWsClaimed, num_units,
+          [&](uint32_t u) { return make_uint2(u / per_tile, u % per_tile); }, abort_word, lim);
   } else if (warp >= kScaleWarp0) {
     regs_dec<kScaleRegs>();
     const uint32_t t_scale = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kScaleCol0;
@@ -408,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t m2 = 0;
 #pragma unroll
           for (int j = 0; j < 16; ++j) m2 = absmax2(m2, v[16 * q + j]);
-          const uint32_t byte = mx4_scale_byte(max(m2 & 0xffffu, m2 >> 16));
-          const float inv = mx4_inverse(byte);
+          const uint32_t byte = mx4_scale_byte(absmax2(m2, m2 >> 16) & 0xffffu);
+          const uint32_t inv = mx4_inverse2(byte);
           uint32_t c4[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {

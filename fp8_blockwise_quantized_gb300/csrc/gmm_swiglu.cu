@@ -11,10 +11,10 @@
 //
 // Both are one grouped GEMM on the tensor core with the activation in its
 // epilogue (384 threads, one persistent CTA per SM):
-//   warp 0      TMA: per 64-wide K step the 128 rows of x (or dy) and BN
+//   warp 0      TMA: per 64-wide K step the 128 rows of x (or dy) and the unit's
 //               columns of the weight into a ring of shared-memory slots
-//   warp 1      TMEM, tcgen05.mma kind::f16 M=128 N=BN K=16, two accumulators,
-//               so that one unit's epilogue overlaps the next unit's products
+//   warp 1      TMEM, tcgen05.mma kind::f16 M=128 K=16, two accumulators, so that
+//               one unit's epilogue overlaps the next unit's products
 //   warp 2      claims the CTA's units and queues them for the other roles
 //   warps 4-11  epilogue: one thread per row and column half
 // Rows of a tile past its group's end belong to the next group: they are
@@ -42,19 +42,53 @@ constexpr uint64_t kDrainLimitNs = 200000000ull;
 constexpr uint32_t kControlRegs = 72, kEpiRegs = 216;
 static_assert(128 * kControlRegs + 256 * kEpiRegs <= kThreads * 168, "register split exceeds the launch budget");
 
-template <int BN>
-struct SwigluTile {
-  static constexpr int kStages = BN == 256 ? 4 : 5;
-  static constexpr int kABytes = kBM * 64 * 2;
-  static constexpr int kBBytes = 64 * BN * 2;
-  static constexpr int kBoxBytes = 64 * 64 * 2;  // one 64 x 64 box of the natural-layout weight
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kTmemCols = 2 * BN;
-  static constexpr int kStagingBytes = kEpiWarps * 4096;
-  static constexpr int kBarBytes = 512;
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kBarBytes;
-  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static_assert(8 * (2 * kStages + 5 + ClaimQueue::kBarriers) + 16 + 16 * kClaimSlots <= kBarBytes, "barrier area");
+constexpr int kStages = 4;
+constexpr int kABytes = kBM * 64 * 2;
+constexpr int kHalfB = 128 * 64 * 2;        // 128 weight columns of a K step
+constexpr int kBoxBytes = 64 * 64 * 2;      // one 64 x 64 box of the natural-layout weight
+constexpr int kStageBytes = kABytes + 2 * kHalfB;
+constexpr int kStagingBytes = kEpiWarps * 4096;
+constexpr int kBarBytes = 512;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kBarBytes;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+static_assert(8 * (2 * kStages + 5 + ClaimQueue::kBarriers) + 16 + 16 * kClaimSlots <= kBarBytes, "barrier area");
+
+// The work units.  A wide unit is 128 rows x 256 weight columns (forward: 128
+// gate and 128 up columns; backward: 256 columns of dh), a narrow one half of
+// that.  Units are wide, but where the last round of wide ones would leave half
+// of the CTAs or more without any, its units are cut in two: a narrow unit
+// takes a little over half a wide one's time (80 row tiles, K 2048, N 512, as
+// many as one eighth of a production layer: TAILFIGS).
+// Widths are fixed to wide for the forward's e4m3 output (a scale covers a
+// unit's 128 columns) and to narrow where N is not a multiple of 256 in the
+// backward.
+struct Units {
+  uint32_t wide;      // units [0, wide) are wide
+  uint32_t num;       // units in all
+  uint32_t per_tile;  // wide units (narrow ones when there are no wide ones) per row tile
+  bool all_narrow;
+  __device__ Units(uint32_t tiles, int N, bool fwd, bool can_wide, bool can_narrow) {
+    const uint32_t wide_cols = fwd ? 128 : 256;
+    all_narrow = !can_wide;
+    per_tile = all_narrow ? N / (wide_cols / 2) : N / wide_cols;
+    num = tiles * per_tile;
+    wide = all_narrow ? 0 : num;
+    if (!all_narrow && can_narrow) {
+      const uint32_t rest = num % gridDim.x;
+      if (2 * rest <= gridDim.x) {
+        wide = num - rest;
+        num += rest;
+      }
+    }
+  }
+  // row tile, and the first half-unit column with the width (1 narrow, 2 wide)
+  // in the low bits
+  __device__ uint2 at(uint32_t u) const {
+    if (all_narrow) return make_uint2(u / per_tile, (u % per_tile) << 2 | 1);
+    if (u < wide) return make_uint2(u / per_tile, (2 * (u % per_tile)) << 2 | 2);
+    const uint32_t v = u - wide, w = wide + v / 2;
+    return make_uint2(w / per_tile, (2 * (w % per_tile) + (v & 1)) << 2 | 1);
+  }
 };
 
 // s(v) = 1 / (1 + exp(-v)) with the hardware exponential and divide (a few ulp
@@ -104,22 +138,22 @@ __device__ __forceinline__ void put32(uint8_t* box, int lane, const float (&v)[3
                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
 }
 
-// Forward: 64 columns of h and of the bf16 gate | up (half 0 the first 64 of
-// the unit's 128, half 1 the rest), or all 128 codes of gate (half 0) or up.
-// The accumulators hold gate in columns [0, 128), up in [128, 256).
+// Forward: half of the unit's `cols` (64 or 128) columns of h and of the bf16
+// gate | up, or all 128 codes of gate (half 0) or up (half 1).  The accumulators
+// hold gate in columns [0, cols), up in [cols, 2 cols).
 template <bool E4M3>
 __device__ __forceinline__ void fwd_rows(const SwigluArgs& args, uint8_t* stage, uint32_t t, int half, int lane,
-                                         long long row0, int rows, int n0) {
+                                         long long row0, int rows, int n0, int cols) {
   const long long N = args.N, ldh = 2 * N, ldg = 4 * N;
   uint8_t* box0 = stage;
   uint8_t* box1 = stage + Box64::kBytes;
 #pragma unroll 1
-  for (int cc = 0; cc < 2; ++cc) {
+  for (int c0 = half * cols / 2; c0 < (half + 1) * cols / 2; c0 += 32) {
     uint32_t ra[32], rb[32];
-    tmem_ld_32x32(t + half * 64 + 32 * cc, ra);
-    tmem_ld_32x32(t + 128 + half * 64 + 32 * cc, rb);
+    tmem_ld_32x32(t + c0, ra);
+    tmem_ld_32x32(t + cols + c0, rb);
     tmem_ld_wait();
-    const int col = n0 + half * 64 + 32 * cc;
+    const int col = n0 + c0;
     float v[32];
     if (!E4M3) {
 #pragma unroll
@@ -198,17 +232,18 @@ struct Kept32 {
   }
 };
 
-// Backward: COLS columns from `col0` on, dh at tensor memory address `t`;
+// Backward: `cols` columns from `col0` on, dh at tensor memory address `t`;
 // `next` holds the first 32 columns of the kept values.
-template <int COLS, bool E4M3>
+template <bool E4M3>
 __device__ __forceinline__ void bwd_rows(const SwigluArgs& args, uint8_t* stage, uint32_t t, int lane, long long row0,
-                                         int rows, int col0, Kept32<E4M3>& next, float sa, float sb) {
+                                         int rows, int col0, int cols, Kept32<E4M3>& next, float sa,
+                                         float sb) {
   using Box = typename Kept32<E4M3>::Box;
   const long long N = args.N, ldh = 2 * N, ldg = 4 * N;
   uint8_t* box0 = stage;
   uint8_t* box1 = stage + Box64::kBytes;
 #pragma unroll 1
-  for (int cc = 0; cc < COLS / 32; ++cc) {
+  for (int cc = 0; cc < cols / 32; ++cc) {
     const int col = col0 + 32 * cc;
     Box::put_sweeps(box0, next.a, lane);
     Box::put_sweeps(box1, next.b, lane);
@@ -231,7 +266,7 @@ __device__ __forceinline__ void bwd_rows(const SwigluArgs& args, uint8_t* stage,
       }
     }
     __syncwarp();
-    if (cc + 1 < COLS / 32) next.fetch(args, row0, rows, col + 32, lane);
+    if (cc + 1 < cols / 32) next.fetch(args, row0, rows, col + 32, lane);
     uint32_t r[32];
     tmem_ld_32x32(t + 32 * cc, r);
     tmem_ld_wait();
@@ -261,21 +296,16 @@ __device__ __forceinline__ void bwd_rows(const SwigluArgs& args, uint8_t* stage,
   }
 }
 
-// FWD: W natural [G*K, 2N] (MN-major), units of 128 gate + 128 up columns
-// (BN = 256).  Otherwise W2 as rows of its N output columns, K-major, units of
-// BN columns.
-template <int BN, bool FWD, bool E4M3>
+// FWD: W natural [G*K, 2N] (MN-major).  Otherwise W2 as rows of its N output
+// columns, K-major.
+template <bool FWD, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
     gmm_swiglu_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const SwigluArgs args) {
-  static_assert(!FWD || BN == 256, "a forward unit is 128 gate and 128 up columns");
-  using C = SwigluTile<BN>;
-  constexpr int kStages = C::kStages;
-  constexpr int kOutCols = FWD ? 128 : BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* staging = ring + kStages * C::kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::kStagingBytes);
+  uint8_t* staging = ring + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStagingBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
@@ -305,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_b);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -315,41 +345,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();  // inputs and metadata come from earlier kernels
 
-  const int per_tile = args.N / kOutCols;
-  const uint32_t num_units = static_cast<uint32_t>(args.meta[kWsNumTiles]) * static_cast<uint32_t>(per_tile);
+  const Units units(static_cast<uint32_t>(args.meta[kWsNumTiles]), args.N, FWD, FWD || args.N % 256 == 0,
+                    !FWD || !E4M3);
   const int KS = args.K / 64;
   const uint64_t lim = args.wait_limit_ns;
 
   if (warp < kEpiWarp0) regs_dec<kControlRegs>();
   if (warp == 0) {
     if (lane == 0) {
-      // one K step's boxes
-      const auto boxes = [&](const int4& u, int ks, auto&& box) {
-        const int n0 = u.w * kOutCols;
-        box(&map_a, 0, ks * 64, u.y);
-        if (FWD) {
-          const int wrow = u.x * args.K + ks * 64;  // row of the [G*K, 2N] weight view
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            box(&map_b, C::kABytes + j * C::kBoxBytes, (j >> 1) * args.N + n0 + 64 * (j & 1), wrow);
-        } else {
-          box(&map_b, C::kABytes, ks * 64, u.x * args.N + n0);
-        }
-      };
       RingPos<kStages> r;
       uint32_t c = 0;
       bool ok = true;
       int4 e;
       for (uint32_t i = 0; ok && queue.get(i, e, false, 0, abort_word, lim) && e.x >= 0; ++i) {
+        const int width = e.w & 3, n0 = (e.w >> 2) * (FWD ? 64 : 128);
         for (int ks = 0; ks < KS; ++ks) {
           if (!mbar_wait(&empty[r.slot], r.phase ^ 1u, abort_word, lim)) {
             ok = false;
             break;
           }
-          uint8_t* dst = ring + r.slot * C::kStageBytes;
+          uint8_t* dst = ring + r.slot * kStageBytes;
           uint64_t* bar = &full[r.slot];
-          mbar_arrive_expect_tx(bar, C::kStageBytes);
-          boxes(e, ks, [&](const CUtensorMap* map, int at, int x, int y) { tma_load_2d(dst + at, map, bar, x, y); });
+          mbar_arrive_expect_tx(bar, kABytes + width * kHalfB);
+          tma_load_2d(dst, &map_a, bar, ks * 64, e.y);
+          dst += kABytes;
+          if (FWD) {
+            // gate boxes, then up boxes, of 64 columns
+            const int wrow = e.x * args.K + ks * 64;  // row of the [G*K, 2N] weight view
+            tma_load_2d(dst, &map_b, bar, n0, wrow);
+            if (width == 2) tma_load_2d(dst + kBoxBytes, &map_b, bar, n0 + 64, wrow);
+            dst += width * kBoxBytes;
+            tma_load_2d(dst, &map_b, bar, args.N + n0, wrow);
+            if (width == 2) tma_load_2d(dst + kBoxBytes, &map_b, bar, args.N + n0 + 64, wrow);
+          } else {
+            tma_load_2d(dst, &map_b, bar, ks * 64, e.x * args.N + n0);
+            if (width == 2) tma_load_2d(dst + kHalfB, &map_b, bar, ks * 64, e.x * args.N + n0 + 128);
+          }
           r.advance();
           ++c;
         }
@@ -368,9 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // steps' products beyond some 200 cycles is time without products, so the
     // loop keeps running positions and descriptor words instead of deriving them.
     if (lane == 0) {
-      constexpr uint32_t idesc = make_idesc(1u /*bf16*/, false, FWD, kBM, BN);
+      constexpr uint32_t idesc1 = make_idesc(1u /*bf16*/, false, FWD, kBM, 128);
+      constexpr uint32_t idesc2 = make_idesc(1u /*bf16*/, false, FWD, kBM, 256);
       const uint32_t a_lo0 = desc_lo_sw128(smem_u32(ring), 16);
-      const uint32_t b_lo0 = desc_lo_sw128(smem_u32(ring) + C::kABytes, FWD ? C::kBoxBytes : 16);
+      const uint32_t b_lo0 = desc_lo_sw128(smem_u32(ring) + kABytes, FWD ? kBoxBytes : 16);
       constexpr uint32_t kBStep = (FWD ? 2048 : 32) >> 4;
       RingPos<kStages> r;
       RingPos<2> acc;
@@ -379,14 +411,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t i = 0; ok && queue.get(i, e, false, 0, abort_word, lim) && e.x >= 0; ++i) {
         if (!mbar_wait(&tempty[acc.slot], acc.phase ^ 1u, abort_word, lim)) break;
         tc_fence_after();
-        const uint32_t d = tbase + acc.slot * BN;
+        const uint32_t d = tbase + acc.slot * 256;
+        const uint32_t idesc = (e.w & 3) == 2 ? idesc2 : idesc1;
         for (int ks = 0; ks < KS; ++ks) {
           if (!next_ready && !mbar_wait(&full[r.slot], r.phase, abort_word, lim)) {
             ok = false;
             break;
           }
-          const uint32_t a_lo = a_lo0 + r.slot * (C::kStageBytes >> 4);
-          const uint32_t b_lo = b_lo0 + r.slot * (C::kStageBytes >> 4);
+          const uint32_t a_lo = a_lo0 + r.slot * (kStageBytes >> 4);
+          const uint32_t b_lo = b_lo0 + r.slot * (kStageBytes >> 4);
           uint64_t* freed = &empty[r.slot];
           r.advance();
           next_ready = mbar_test(&full[r.slot], r.phase);  // answered while the products are issued
@@ -408,8 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     if (lane == 0)
-      queue.schedule(args.tiles, const_cast<int32_t*>(args.meta) + kWsClaimed, num_units,
-                     static_cast<uint32_t>(per_tile), abort_word, lim);
+      queue.schedule(
+          args.tiles, const_cast<int32_t*>(args.meta) + kWsClaimed, units.num,
+          [&](uint32_t u) { return units.at(u); }, abort_word, lim);
   } else if (warp >= kEpiWarp0) {
     regs_inc<kEpiRegs>();
     const int half = (warp - kEpiWarp0) >> 2;
@@ -437,7 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = 0; queue.get(i, e, true, lane, abort_word, lim) && e.x >= 0; ++i) {
       const long long row0 = e.y + quad * 32;
       const int rows = min(32, e.z - static_cast<int>(row0));  // of this warp; may be <= 0
-      const int col0 = e.w * kOutCols + (FWD ? 0 : half * (BN / 2));
+      const int cols = (e.w & 3) * (FWD ? 64 : 128);  // of the unit
+      const int col0 = (e.w >> 2) * (FWD ? 64 : 128) + (FWD ? 0 : half * (cols / 2));
       Kept32<E4M3> kept;
       float sa = 0.0f, sb = 0.0f;
       if (!FWD) {  // read while the products run
@@ -449,12 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc.slot], acc.phase, abort_word, lim))) break;
       tc_fence_after();
-      const uint32_t tb = t_lane + acc.slot * BN;
+      const uint32_t tb = t_lane + acc.slot * 256;
       if (rows > 0) {
         if (FWD)
-          fwd_rows<E4M3>(args, stage, tb, half, lane, row0, rows, col0);
+          fwd_rows<E4M3>(args, stage, tb, half, lane, row0, rows, col0, cols);
         else
-          bwd_rows<BN / 2, E4M3>(args, stage, tb + half * (BN / 2), lane, row0, rows, col0, kept, sa, sb);
+          bwd_rows<E4M3>(args, stage, tb + half * (cols / 2), lane, row0, rows, col0, cols / 2, kept, sa, sb);
       }
       tc_fence_before();
       __syncwarp();
@@ -467,39 +502,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, C::kTmemCols);
+    tmem_dealloc(tbase, 512);
   }
   if (threadIdx.x == 0) finish_claims(const_cast<int32_t*>(args.meta), *abort_word != 0);
 }
 
-template <int BN, bool FWD, bool E4M3>
+template <bool FWD, bool E4M3>
 cudaError_t launch(const CUtensorMap& map_a, const CUtensorMap& map_b, const SwigluArgs& args, int grid,
                    cudaStream_t stream) {
-  constexpr int smem = SwigluTile<BN>::kSmemBytes;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(gmm_swiglu_kernel<BN, FWD, E4M3>, smem, done);
+  cudaError_t e = allow_smem(gmm_swiglu_kernel<FWD, E4M3>, kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(gmm_swiglu_kernel<BN, FWD, E4M3>, dim3(grid), dim3(kThreads), smem, stream, map_a, map_b, args);
+  return launch_pdl(gmm_swiglu_kernel<FWD, E4M3>, dim3(grid), dim3(kThreads), kSmemBytes, stream, map_a, map_b, args);
 }
 
 }  // namespace
 
 cudaError_t launch_gmm_swiglu_fwd(const CUtensorMap& map_x, const CUtensorMap& map_w, const SwigluArgs& args,
                                   int grid, cudaStream_t stream) {
-  if (args.guq) return launch<256, true, true>(map_x, map_w, args, grid, stream);
-  return launch<256, true, false>(map_x, map_w, args, grid, stream);
+  if (args.guq) return launch<true, true>(map_x, map_w, args, grid, stream);
+  return launch<true, false>(map_x, map_w, args, grid, stream);
 }
-
-int swiglu_bwd_bn(int N) { return N % 256 == 0 ? 256 : 128; }
 
 cudaError_t launch_gmm_swiglu_bwd(const CUtensorMap& map_dy, const CUtensorMap& map_w2, const SwigluArgs& args,
                                   int grid, cudaStream_t stream) {
-  if (swiglu_bwd_bn(args.N) == 256) {
-    if (args.guq) return launch<256, false, true>(map_dy, map_w2, args, grid, stream);
-    return launch<256, false, false>(map_dy, map_w2, args, grid, stream);
-  }
-  if (args.guq) return launch<128, false, true>(map_dy, map_w2, args, grid, stream);
-  return launch<128, false, false>(map_dy, map_w2, args, grid, stream);
+  if (args.guq) return launch<false, true>(map_dy, map_w2, args, grid, stream);
+  return launch<false, false>(map_dy, map_w2, args, grid, stream);
 }
 
 }  // namespace gmm

@@ -142,16 +142,16 @@ cudaError_t launch_tgmm_bf16(const CUtensorMap& map_x, const CUtensorMap& map_dy
 // map_x: x [M, K], box 64 x 128; map_w: w [G*K, 2N], box 64 x 64.
 cudaError_t launch_gmm_swiglu_fwd(const CUtensorMap& map_x, const CUtensorMap& map_w, const SwigluArgs& args,
                                   int grid, cudaStream_t stream);
-// map_dy: dy [M, K], box 64 x 128; map_w2: w2 [G*N, K], box 64 x swiglu_bwd_bn(N).
+// map_dy: dy [M, K], box 64 x 128; map_w2: w2 [G*N, K], box 64 x 128.
 cudaError_t launch_gmm_swiglu_bwd(const CUtensorMap& map_dy, const CUtensorMap& map_w2, const SwigluArgs& args,
                                   int grid, cudaStream_t stream);
-int swiglu_bwd_bn(int N);
 // map_x: codes [M, K] bytes, box 128 x 64; map_dy: box 64 x 64; map_dw: dw [G*K, N], box 64 x 32.
 cudaError_t launch_tgmm_ckpt(const CUtensorMap& map_x, const CUtensorMap& map_dy, const CUtensorMap& map_dw,
                              const TgmmArgs& args, int max_pairs, cudaStream_t stream);
 
 // ---- MXFP4 --------------------------------------------------------------------
-__global__ void mx4_quantize_lhs_kernel(const uint4* x, int M, int KB, uint32_t* xq, uint32_t* xs);
+__global__ void mx4_quantize_lhs_kernel(const uint4* x, int M, uint32_t KB, uint32_t steps, uint32_t* xq,
+                                        uint32_t* xs);
 __global__ void mx4_quantize_rhs_kernel(const uint16_t* w, int K, int N, uint8_t* wq, uint8_t* ws);
 // map_a: codes [M, K/2] bytes, box 128 x 128; map_b: codes [G*Nw, K/2] bytes,
 // box 128 x bn (bn / 2 when fused); map_out: out [M, N], box 64 x 32.

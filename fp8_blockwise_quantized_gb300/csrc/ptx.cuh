@@ -171,14 +171,6 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
 
 // x is the innermost coordinate (elements); it must be a multiple of
 // 16 bytes / element size, which every caller guarantees by construction.
-// The same box into L2 only.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y)
-               : "memory");
-}
-
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
                                             int32_t y) {
   asm volatile(

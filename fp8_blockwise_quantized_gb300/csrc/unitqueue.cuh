@@ -36,40 +36,37 @@ struct ClaimQueue {
     if (lane == 0) mbar_arrive(&empty[slot]);
     return true;
   }
-  // Entry i, for a look ahead, if it is there already; it stays in the queue.
-  __device__ bool peek(uint32_t i, int4& e) const {
-    if (!mbar_test(&full[i % kClaimSlots], (i / kClaimSlots) & 1u)) return false;
-    e = data[i % kClaimSlots];
-    return e.x >= 0;
-  }
-  // Scheduler (one thread): the CTA's first unit is its block index, the next
-  // ones are claimed from the workspace counter (a CTA that runs slower takes
-  // fewer units), two claims and the next unit's tile in flight while a unit
-  // is published: one claim at a time takes about 1 us a unit.
-  // Unit u is row tile u / per_tile, column block u % per_tile.
-  __device__ void schedule(const Tile* tiles, int* claimed, uint32_t num_units, uint32_t per_tile,
-                           volatile int* abort_word, uint64_t lim) const {
-    const auto tile = [&](uint32_t u) {
-      return u < num_units ? __ldg(reinterpret_cast<const int4*>(tiles + u / per_tile)) : make_int4(-1, 0, 0, 0);
+  // Scheduler (one thread).  unit(u) gives unit u's row tile and column block
+  // (x, y).  A CTA's first kDealt units are dealt round by round (claimed from
+  // the start, the CTAs that begin a microsecond early take the units of the
+  // others: decoding steps of 264 units ran 23 us instead of 10); the next ones
+  // are claimed from the workspace counter, so that a CTA that runs slower
+  // takes fewer.  Two claims and the next unit's tile are in flight while a
+  // unit is published: a claim and its tile take 1 us or more.
+  template <typename F>
+  __device__ void schedule(const Tile* tiles, int* claimed, uint32_t num_units, F&& unit, volatile int* abort_word,
+                           uint64_t lim) const {
+    constexpr uint32_t kDealt = 4;
+    const auto entry = [&](uint32_t u) {
+      if (u >= num_units) return make_int4(-1, 0, 0, 0);
+      const uint2 at = unit(u);
+      int4 t = __ldg(reinterpret_cast<const int4*>(tiles + at.x));
+      t.w = static_cast<int>(at.y);
+      return t;
     };
-    const auto claim = [&]() { return gridDim.x + static_cast<uint32_t>(atomicAdd(claimed, 1)); };
-    uint32_t u = blockIdx.x, u1 = num_units, u2 = num_units;
-    if (u < num_units) {
-      u1 = claim();
-      u2 = claim();
-    }
-    int4 t = tile(u);
+    uint32_t u = blockIdx.x, u1 = u + gridDim.x, u2 = u1 + gridDim.x;
+    int4 t = entry(u);
     for (uint32_t i = 0;; ++i) {
       const uint32_t slot = i % kClaimSlots, ph = (i / kClaimSlots) & 1u;
       if (!mbar_wait(&empty[slot], ph ^ 1u, abort_word, lim)) return;
-      t.w = static_cast<int>(u % per_tile);
       data[slot] = t;
       mbar_arrive(&full[slot]);
       if (u >= num_units) return;
       u = u1;
       u1 = u2;
-      if (u2 < num_units) u2 = claim();
-      t = tile(u);
+      if (u2 < num_units)
+        u2 = i + 3 < kDealt ? u2 + gridDim.x : kDealt * gridDim.x + static_cast<uint32_t>(atomicAdd(claimed, 1));
+      t = entry(u);
     }
   }
 };

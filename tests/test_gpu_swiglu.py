@@ -24,6 +24,8 @@ EDGE = [
     ([15, 16, 17, 33, 63, 64, 65], 300, 640, 256),
     ([0, 0, 0], 64, 256, 128),
     ([1000, 3, 700, 0, 0, 297], 2000, 1152, 512),
+    # more units than SMs: rounds of wide ones and a rest cut in two (43 row tiles)
+    ([2500, 31, 0, 2900], 5500, 128, 1024),
 ]
 
 
