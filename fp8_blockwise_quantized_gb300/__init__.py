@@ -14,7 +14,7 @@ from .binding import (EXPORTED, GmmError, LIB_PATH, STATUS_NAMES, Workspace, bf1
                       group_metadata, load, quantize_lhs, quantize_rhs, tgmm, tgmm_bf16,
                       gmm_quantize_rhs_w4, gmm_fp8_w4_fwd, gmm_fp8_w4_fwd_swiglu_quant, quantize_rhs_w4,
                       fp8_w4_fwd, fp8_w4_fwd_swiglu_quant, tgmm_bf16_tiled, TgmmConfig,
-                      gmm_bf16_swiglu_fwd, gmm_bf16_swiglu_bwd, tgmm_fp8_ckpt, gmm_mx4_quantize_lhs,
+                      gmm_bf16_swiglu_fwd, gmm_bf16_swiglu_bwd, tgmm_fp8_ckpt, tgmm_fp8_ckpt_scratch_bytes, gmm_mx4_quantize_lhs,
                       gmm_mx4_quantize_rhs, gmm_mx4_fwd, gmm_mx4_fwd_swiglu_quant,
                       swiglu_fwd, swiglu_bwd, tgmm_ckpt, mx4_quantize_lhs,
                       mx4_quantize_rhs, mx4_fwd, mx4_fwd_swiglu_quant)
@@ -28,7 +28,7 @@ __all__ = ["EXPORTED", "GmmError", "LIB_PATH", "STATUS_NAMES", "Workspace", "bf1
            "group_metadata", "load", "quantize_lhs", "quantize_rhs", "tgmm", "tgmm_bf16",
            "gmm_quantize_rhs_w4", "gmm_fp8_w4_fwd", "gmm_fp8_w4_fwd_swiglu_quant", "quantize_rhs_w4",
            "fp8_w4_fwd", "fp8_w4_fwd_swiglu_quant", "tgmm_bf16_tiled", "TgmmConfig",
-           "gmm_bf16_swiglu_fwd", "gmm_bf16_swiglu_bwd", "tgmm_fp8_ckpt", "gmm_mx4_quantize_lhs",
+           "gmm_bf16_swiglu_fwd", "gmm_bf16_swiglu_bwd", "tgmm_fp8_ckpt", "tgmm_fp8_ckpt_scratch_bytes", "gmm_mx4_quantize_lhs",
            "gmm_mx4_quantize_rhs", "gmm_mx4_fwd", "gmm_mx4_fwd_swiglu_quant",
            "swiglu_fwd", "swiglu_bwd", "tgmm_ckpt", "mx4_quantize_lhs",
            "mx4_quantize_rhs", "mx4_fwd", "mx4_fwd_swiglu_quant"]

@@ -32,7 +32,7 @@ EXPORTED = ["gmm_status_string", "gmm_last_cuda_error", "gmm_workspace_bytes", "
             "gmm_bf16_dgrad", "gmm_fp8_fwd_swiglu_quant", "gmm_selftest_wait_timeout", "gmm_fp8_fwd_tiled",
             "gmm_fp8_fwd_swiglu_quant_tiled", "gmm_quantize_rhs_w4", "gmm_fp8_w4_fwd",
             "gmm_fp8_w4_fwd_swiglu_quant", "tgmm_bf16_tiled", "gmm_bf16_swiglu_fwd", "gmm_bf16_swiglu_bwd",
-            "tgmm_fp8_ckpt", "gmm_mx4_quantize_lhs", "gmm_mx4_quantize_rhs", "gmm_mx4_fwd",
+            "tgmm_fp8_ckpt", "tgmm_fp8_ckpt_scratch_bytes", "gmm_mx4_quantize_lhs", "gmm_mx4_quantize_rhs", "gmm_mx4_fwd",
             "gmm_mx4_fwd_swiglu_quant"]
 
 
@@ -131,7 +131,9 @@ def load():
     lib.gmm_bf16_swiglu_bwd.restype = I
     lib.gmm_bf16_swiglu_bwd.argtypes = [P, P, P, P, P, P, I, I64, I64, I64, P, P, P, SZ, P]
     lib.tgmm_fp8_ckpt.restype = I
-    lib.tgmm_fp8_ckpt.argtypes = [P, P, P, P, I, I64, I64, I64, P, P, SZ, P]
+    lib.tgmm_fp8_ckpt.argtypes = [P, P, P, P, I, I64, I64, I64, P, P, SZ, P, SZ, P]
+    lib.tgmm_fp8_ckpt_scratch_bytes.restype = SZ
+    lib.tgmm_fp8_ckpt_scratch_bytes.argtypes = [I, I64, I64, I64]
     lib.gmm_mx4_quantize_lhs.restype = I
     lib.gmm_mx4_quantize_lhs.argtypes = [P, I64, I64, P, P, P]
     lib.gmm_mx4_quantize_rhs.restype = I
@@ -301,9 +303,14 @@ def gmm_bf16_swiglu_bwd(dy, w2, gu, guq, gus, group_sizes, G, M, K, N, dgu, h, w
                                       _p(dgu), _p(h), _p(workspace), workspace_bytes, _s(stream))
 
 
-def tgmm_fp8_ckpt(xq, xs, dy, group_sizes, G, M, K, N, dw, workspace, workspace_bytes, stream=None) -> int:
-    return load().tgmm_fp8_ckpt(_p(xq), _p(xs), _p(dy), _p(group_sizes), G, M, K, N, _p(dw), _p(workspace),
-                                workspace_bytes, _s(stream))
+def tgmm_fp8_ckpt_scratch_bytes(G: int, M: int, K: int, N: int) -> int:
+    return int(load().tgmm_fp8_ckpt_scratch_bytes(G, M, K, N))
+
+
+def tgmm_fp8_ckpt(xq, xs, dy, group_sizes, G, M, K, N, dw, scratch, scratch_bytes, workspace, workspace_bytes,
+                  stream=None) -> int:
+    return load().tgmm_fp8_ckpt(_p(xq), _p(xs), _p(dy), _p(group_sizes), G, M, K, N, _p(dw), _p(scratch),
+                                scratch_bytes, _p(workspace), workspace_bytes, _s(stream))
 
 
 def gmm_mx4_quantize_lhs(x, M, K, xq, xs, stream=None) -> int:
@@ -603,7 +610,8 @@ def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=No
 
 def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     """tgmm from the 8-bit checkpoint of x: xq uint8 [M, K] e4m3 codes, xs
-    float32 [K/128, M] (quantize_lhs), dy bf16 [M, N] -> dw bf16 [G, K, N]."""
+    float32 [K/128, M] (quantize_lhs), dy bf16 [M, N] -> dw bf16 [G, K, N].
+    The scratch that few tiles with many rows need is allocated with torch."""
     M, K = xq.shape
     M2, N = dy.shape
     assert M2 == M and tuple(xs.shape) == (K // 128, M)
@@ -618,7 +626,15 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     if dw is None:
         dw = _new3(G, K, N, torch.bfloat16, dy.device)
     ws_ = _ws_for(group_sizes, workspace, G, M, dy.device)
-    _check(tgmm_fp8_ckpt(xq, xs, dy, group_sizes, G, M, K, N, dw, ws_.buf, ws_.nbytes, stream), "tgmm_fp8_ckpt")
+    nbytes = tgmm_fp8_ckpt_scratch_bytes(G, M, K, N)
+    scratch = None
+    if nbytes:
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
+        if stream is not None:  # not the stream that the allocator thinks of
+            scratch.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                  else torch.cuda.ExternalStream(int(stream), device=dy.device))
+    _check(tgmm_fp8_ckpt(xq, xs, dy, group_sizes, G, M, K, N, dw, scratch, nbytes, ws_.buf, ws_.nbytes, stream),
+           "tgmm_fp8_ckpt")
     return dw
 
 

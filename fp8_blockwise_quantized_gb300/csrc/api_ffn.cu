@@ -170,33 +170,51 @@ gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, c
                   "gmm_swiglu backward launch");
 }
 
+size_t tgmm_fp8_ckpt_scratch_bytes(int G, int64_t M, int64_t K, int64_t N) {
+  int sms = 0;
+  if (host_check_grouped(G, M, K, N, N) != GMM_OK || host_device_sms(&sms) != GMM_OK) return 0;
+  const int splits = tgmm_ckpt_splits(G, M, K, N, sms);
+  return splits > 1 ? static_cast<size_t>(splits) * G * K * N * sizeof(float) : 0;
+}
+
 gmm_status tgmm_fp8_ckpt(const void* xq, const float* xs, const void* dy, const int32_t* group_sizes, int G, int64_t M,
-                         int64_t K, int64_t N, void* dw, void* workspace, size_t workspace_bytes, void* stream) {
+                         int64_t K, int64_t N, void* dw, void* scratch, size_t scratch_bytes, void* workspace,
+                         size_t workspace_bytes, void* stream) {
   gmm_status st = host_check_grouped(G, M, K, N, N);
   if (st != GMM_OK) return st;
-  const long long units = static_cast<long long>(G) * ((K + 255) / 256) * ((N + 255) / 256);
-  if (units > kMaxUnits) return GMM_ERR_SHAPE;
+  const long long tiles = static_cast<long long>(G) * ((K + 255) / 256) * ((N + 255) / 256);
+  if (tiles > kMaxUnits) return GMM_ERR_SHAPE;
   if (!dw || (M > 0 && (!xq || !xs || !dy))) return GMM_ERR_NULL;
-  if (!all_aligned(xq, xs, dy, group_sizes, dw)) return GMM_ERR_ALIGN;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!all_aligned(xq, xs, dy, group_sizes, dw, scratch)) return GMM_ERR_ALIGN;
+  if ((st = host_check_workspace(workspace, workspace_bytes, G, M)) != GMM_OK) return st;
   int sms = 0;
+  if ((st = host_device_sms(&sms)) != GMM_OK) return st;
+  const int splits = scratch ? tgmm_ckpt_splits(G, M, K, N, sms) : 1;
+  if (splits > 1 && scratch_bytes < static_cast<size_t>(splits) * G * K * N * sizeof(float)) return GMM_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
   // With M == 0 every group is empty: the kernel only writes zeros and never
   // reads x or dy, so the maps may describe a dummy one-row tensor.
   CUtensorMap map_x, map_dy, map_dw;
   if ((st = host_encode_2d(&map_x, kByte, 1, M > 0 ? xq : dw, K, M, 128, 64)) != GMM_OK) return st;
   if ((st = host_encode_2d(&map_dy, kBf16, 2, M > 0 ? dy : dw, N, M, 64, 64)) != GMM_OK) return st;
-  if ((st = host_encode_2d(&map_dw, kBf16, 2, dw, N, G * K, 64, 32)) != GMM_OK) return st;
+  st = splits > 1 ? host_encode_2d(&map_dw, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, scratch, N,
+                                   static_cast<uint64_t>(splits) * G * K, 32, 32)
+                  : host_encode_2d(&map_dw, kBf16, 2, dw, N, G * K, 64, 32);
+  if (st != GMM_OK) return st;
   TgmmArgs a{};
   a.meta = static_cast<const int32_t*>(workspace);
   a.order = reinterpret_cast<const int32_t*>(static_cast<const char*>(workspace) + order_offset_bytes(G, M));
   a.dw = static_cast<uint16_t*>(dw);
   a.xs = xs;
+  a.parts = static_cast<const float*>(scratch);
+  a.splits = splits;
   a.G = G;
   a.M = static_cast<int>(M);
   a.K = static_cast<int>(K);
   a.N = static_cast<int>(N);
   a.wait_limit_ns = host_wait_limit_ns();
+  const long long units = tiles * splits;
   const int max_pairs = static_cast<int>(units < sms / 2 ? units : sms / 2);
   return launched(launch_tgmm_ckpt(map_x, map_dy, map_dw, a, max_pairs, s), "tgmm_ckpt kernel launch");
 }

@@ -88,6 +88,8 @@ struct TgmmArgs {
   int max_batch;          // CTA-pair kernel: most small units per claim (1..4)
   uint64_t wait_limit_ns;
   const float* xs;        // 8-bit checkpoint: fp32 [K/128][M] scales of x's codes
+  const float* parts;     // 8-bit checkpoint, splits > 1: the parts' sums, fp32 [splits][G][K][N]
+  int splits;             // parts that each group's rows are cut into
 };
 
 // The gated feed-forward block's kernels: the forward (K = columns of x) and
@@ -145,9 +147,12 @@ cudaError_t launch_gmm_swiglu_fwd(const CUtensorMap& map_x, const CUtensorMap& m
 // map_dy: dy [M, K], box 64 x 128; map_w2: w2 [G*N, K], box 64 x 128.
 cudaError_t launch_gmm_swiglu_bwd(const CUtensorMap& map_dy, const CUtensorMap& map_w2, const SwigluArgs& args,
                                   int grid, cudaStream_t stream);
-// map_x: codes [M, K] bytes, box 128 x 64; map_dy: box 64 x 64; map_dw: dw [G*K, N], box 64 x 32.
+// map_x: codes [M, K] bytes, box 128 x 64; map_dy: box 64 x 64; map_dw: dw [G*K, N], box 64 x 32, or with
+// splits > 1 the parts [splits*G*K, N], box 32 x 32.
 cudaError_t launch_tgmm_ckpt(const CUtensorMap& map_x, const CUtensorMap& map_dy, const CUtensorMap& map_dw,
                              const TgmmArgs& args, int max_pairs, cudaStream_t stream);
+
+int tgmm_ckpt_splits(int G, int64_t M, int64_t K, int64_t N, int sms);
 
 // ---- MXFP4 --------------------------------------------------------------------
 __global__ void mx4_quantize_lhs_kernel(const uint4* x, int M, uint32_t KB, uint32_t steps, uint32_t* xq,

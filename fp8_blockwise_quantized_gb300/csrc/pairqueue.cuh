@@ -40,11 +40,14 @@ struct PairQueue {
 };
 
 // The pair's scheduler: one thread of the even CTA.  taken, ctaken: queue
-// entries and chunks that the even CTA's producer has taken.
+// entries and chunks that the even CTA's producer has taken.  With splits > 1 a
+// group's rows are cut into that many parts of whole chunks: unit u % per_group
+// counts them fastest, and its entry holds the part's rows (none where the
+// group has too few).
 __device__ __forceinline__ void pair_schedule(const PairQueue& queue, volatile int* taken, volatile int* ctaken,
                                               int* claimed, const int* order, const int* offsets, int G,
                                               int per_group, int num_units, int claim_ahead, int max_batch,
-                                              volatile int* abort_word, uint64_t lim) {
+                                              volatile int* abort_word, uint64_t lim, int splits = 1) {
   const uint32_t odd_full = mapa_shared(smem_u32(queue.full), 1);
   const uint32_t odd_data = mapa_shared(smem_u32(queue.data), 1);
   uint32_t i = 0;
@@ -124,6 +127,11 @@ __device__ __forceinline__ void pair_schedule(const PairQueue& queue, volatile i
     for (int j = 0; j < kMaxBatch; ++j) {
       r0[j] = j < cnt ? __ldg(offsets + g[j]) : 0;
       r1[j] = j < cnt ? __ldg(offsets + g[j] + 1) : 0;
+      if (splits > 1) {
+        const int part = ((r1[j] - r0[j] + kChunk - 1) / kChunk + splits - 1) / splits * kChunk;
+        r0[j] = min(r1[j], r0[j] + part * (u[j] % per_group % splits));
+        r1[j] = min(r1[j], r0[j] + part);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kMaxBatch; ++j) {

@@ -26,6 +26,11 @@
 //   warp 10      even CTA: the pair's scheduler
 // Tiles that reach past K or N (multiples of 128) load zeros and store nothing
 // there.
+//
+// Few tiles and many rows (one group of 65536 rows, K = N = 256: one tile) would
+// leave most pairs idle: then each group's rows are cut into `splits` parts whose
+// fp32 sums go to a scratch tensor, and a second kernel adds them in order (the
+// same bits every time) and rounds once.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "pairqueue.cuh"
@@ -65,6 +70,9 @@ __device__ __forceinline__ uint2 expand4(uint32_t codes, float scale) {
   return make_uint2(pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(b.x * scale, b.y * scale));
 }
 
+// SPLIT: the parts' fp32 sums to the scratch tensor [splits * G * K, N] that
+// map_dw describes (32 x 32 boxes) instead of bf16 dw (64 x 32 boxes).
+template <bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tgmm_ckpt_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy,
                      const __grid_constant__ CUtensorMap map_dw, const TgmmArgs args) {
@@ -125,7 +133,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   griddep_wait();  // inputs, metadata and the work counter come from earlier kernels
 
   const int KT = (args.K + 255) / 256, NT = (args.N + BN - 1) / BN;
-  const int num_units = args.meta[kWsValid] != 0 ? args.G * KT * NT : 0;
+  const int splits = SPLIT ? args.splits : 1;
+  const int per_group = KT * NT * splits;
+  const int num_units = args.meta[kWsValid] != 0 ? args.G * per_group : 0;
   const int* offsets = args.meta + kWsOffsets;
   const uint64_t lim = args.wait_limit_ns;
   const PairQueue queue{qfull, qempty, qdata, mapa_shared(smem_u32(qempty), 0), leader};
@@ -139,8 +149,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (uint32_t i = 0; ok && queue.get(i, e, false, 0, abort_word, lim) && e.x >= 0; ++i) {
         *taken = static_cast<int>(i) + 1;
         if (e.w <= e.z) *ctaken = ++issued;  // an empty group's unit counts as one chunk
-        const int k0 = (e.y / NT) * 256 + static_cast<int>(rank) * 128;
-        const int n0 = (e.y % NT) * BN + static_cast<int>(rank) * 128;
+        const int k0 = (e.y / splits / NT) * 256 + static_cast<int>(rank) * 128;
+        const int n0 = (e.y / splits % NT) * BN + static_cast<int>(rank) * 128;
         for (int r = e.z; r < e.w; r += kChunk) {
           const uint32_t s = c % kRing, ph = (c / kRing) & 1u;
           if (!mbar_wait(&empty[s], ph ^ 1u, abort_word, lim)) {
@@ -217,10 +227,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t t = 0;
     int4 e;
     for (uint32_t i = 0; queue.get(i, e, true, lane, abort_word, lim) && e.x >= 0; ++i) {
-      const int k0 = (e.y / NT) * 256 + static_cast<int>(rank) * 128;
-      const int n0 = (e.y % NT) * BN + half * 128;
+      const int k0 = (e.y / splits / NT) * 256 + static_cast<int>(rank) * 128;
+      const int n0 = (e.y / splits % NT) * BN + half * 128;
       const bool inside = k0 < args.K && n0 < args.N;
-      const int y = e.x * args.K + k0 + quad * 32;
+      const int y = (SPLIT ? e.y % splits * args.G + e.x : e.x) * args.K + k0 + quad * 32;
       const bool some = e.w > e.z;
       const uint32_t b = t & 1u;
       if (some) {
@@ -246,6 +256,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 64; ++j) r[j] = 0u;
         }
         if (!inside) continue;
+        if (SPLIT) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (lane == 0) bulk_wait_read_all();  // the previous store has read the box
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int c = 32 * q + 4 * j;
+              *reinterpret_cast<uint4*>(brow + ((j ^ (lane & 7)) << 4)) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&map_dw, box, n0 + 64 * pass + 32 * q, y);
+              bulk_commit();
+            }
+          }
+          continue;
+        }
         if (lane == 0) bulk_wait_read_all();  // the previous store has read the box
         __syncwarp();
 #pragma unroll
@@ -269,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kSchedWarp) {
     if (leader && lane == 0)
       pair_schedule(queue, taken, ctaken, const_cast<int32_t*>(args.meta) + kWsClaimed, args.order, offsets, args.G,
-                    KT * NT, num_units, 3, 4, abort_word, lim);
+                    per_group, num_units, 3, 4, abort_word, lim, splits);
   } else if (warp >= kExpandWarp0) {
     // thread: row `row` of the chunk, 64 of its 128 codes (half `hb`)
     const int et = static_cast<int>(threadIdx.x) - 32 * kExpandWarp0;
@@ -280,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     int4 e;
     for (uint32_t i = 0; ok && queue.get(i, e, true, lane, abort_word, lim) && e.x >= 0; ++i) {
-      const int k0 = (e.y / NT) * 256 + static_cast<int>(rank) * 128;
+      const int k0 = (e.y / splits / NT) * 256 + static_cast<int>(rank) * 128;
       const float* xs = args.xs + static_cast<long long>(k0 / 128) * args.M;
       const bool inside = k0 < args.K;
       // this group's chunks of the unit; a chunk's scale is loaded one ahead
@@ -356,13 +385,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-}  // namespace
+// dw = bf16(sum over the parts, in order), four elements a thread.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float4* __restrict__ parts, long long n4, int splits,
+                                                        uint2* __restrict__ dw) {
+  griddep_launch_dependents();
+  griddep_wait();
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n4;
+       i += static_cast<long long>(gridDim.x) * 256) {
+    float4 a = __ldg(parts + i);
+    for (int s = 1; s < splits; ++s) {
+      const float4 b = __ldg(parts + s * n4 + i);
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    dw[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+}
 
-cudaError_t launch_tgmm_ckpt(const CUtensorMap& map_x, const CUtensorMap& map_dy, const CUtensorMap& map_dw,
-                             const TgmmArgs& args, int max_pairs, cudaStream_t stream) {
+template <bool SPLIT>
+cudaError_t launch(const CUtensorMap& map_x, const CUtensorMap& map_dy, const CUtensorMap& map_dw,
+                   const TgmmArgs& args, int max_pairs, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> resident[64];
-  cudaError_t e = allow_smem(tgmm_ckpt_kernel, kSmemBytes, done);
+  auto kernel = tgmm_ckpt_kernel<SPLIT>;
+  cudaError_t e = allow_smem(kernel, kSmemBytes, done);
   int dev = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -373,14 +418,43 @@ cudaError_t launch_tgmm_ckpt(const CUtensorMap& map_x, const CUtensorMap& map_dy
     cfg.gridDim = dim3(2 * 1024, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = kSmemBytes;
-    e = cudaOccupancyMaxActiveClusters(&clusters, tgmm_ckpt_kernel, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (clusters < 1) return cudaErrorInvalidConfiguration;
     resident[dev & 63].store(clusters, std::memory_order_relaxed);
   }
   const int pairs = clusters < max_pairs ? clusters : max_pairs;
-  return launch_pdl(tgmm_ckpt_kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, stream, map_x, map_dy, map_dw,
-                    args);
+  return launch_pdl(kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, stream, map_x, map_dy, map_dw, args);
+}
+
+}  // namespace
+
+// The fewest parts that bring the busiest pair's share of the rows down by a
+// tenth or more; no more than two units per pair (the parts' sums are written
+// and read again) and at least eight chunks per part of a mean group (one group
+// of 65536 rows, K = N = 256: 73 parts, 35 us for 387; 4 groups of 4096, K 1024,
+// N 512: 2 parts, 27 us for 33; 16 groups of 1250, K 512, N 256 in 2 parts of
+// ten chunks: 18 us for 16).
+int tgmm_ckpt_splits(int G, int64_t M, int64_t K, int64_t N, int sms) {
+  const int64_t units = static_cast<int64_t>(G) * ((K + 255) / 256) * ((N + BN - 1) / BN), pairs = sms / 2;
+  int best = 1;
+  double share = static_cast<double>((units + pairs - 1) / pairs);
+  for (int s = 2; s * units <= 2 * pairs && s <= M / (8LL * kChunk * G); ++s) {
+    const double v = static_cast<double>((s * units + pairs - 1) / pairs) / s;
+    if (v < 0.9 * share) best = s, share = v;
+  }
+  return best;
+}
+
+cudaError_t launch_tgmm_ckpt(const CUtensorMap& map_x, const CUtensorMap& map_dy, const CUtensorMap& map_dw,
+                             const TgmmArgs& args, int max_pairs, cudaStream_t stream) {
+  if (args.splits <= 1) return launch<false>(map_x, map_dy, map_dw, args, max_pairs, stream);
+  cudaError_t e = launch<true>(map_x, map_dy, map_dw, args, max_pairs, stream);
+  if (e != cudaSuccess) return e;
+  const long long n4 = static_cast<long long>(args.G) * args.K * args.N / 4;
+  const long long ctas = (n4 + 255) / 256;
+  return launch_pdl(sum_parts_kernel, dim3(static_cast<unsigned>(ctas < 4096 ? ctas : 4096)), dim3(256), 0, stream,
+                    reinterpret_cast<const float4*>(args.parts), n4, args.splits, reinterpret_cast<uint2*>(args.dw));
 }
 
 }  // namespace gmm

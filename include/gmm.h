@@ -371,10 +371,18 @@ gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, c
  * fp32 accumulation; dw[g] = 0 for an empty group.  Rows >= S are not used,
  * whatever they hold.
  *   xq  e4m3 [M, K];  xs  fp32 [K/128, M];  dy  bf16 [M, N];  dw  bf16 [G, K, N]
- * GMM_ERR_SHAPE also when G * ceil(K/256) * ceil(N/256) output tiles exceed 2^30.
+ *   scratch  tgmm_fp8_ckpt_scratch_bytes(G, M, K, N) bytes, or NULL.  With few
+ *            output tiles and many rows that is not 0: the groups' rows are then
+ *            cut into parts whose fp32 sums are joined in a second, ordered pass,
+ *            so that all SMs have work.  Without scratch every tile is one
+ *            CTA pair's work.  The scratch's contents do not matter, before or after.
+ * GMM_ERR_SHAPE also when G * ceil(K/256) * ceil(N/256) output tiles exceed 2^30;
+ * GMM_ERR_WORKSPACE also when a scratch is given that is too small.
  */
+size_t tgmm_fp8_ckpt_scratch_bytes(int G, int64_t M, int64_t K, int64_t N);
 gmm_status tgmm_fp8_ckpt(const void* xq, const float* xs, const void* dy, const int32_t* group_sizes, int G, int64_t M,
-                         int64_t K, int64_t N, void* dw, void* workspace, size_t workspace_bytes, void* stream);
+                         int64_t K, int64_t N, void* dw, void* scratch, size_t scratch_bytes, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 /*
  * Microscaled 4-bit (MXFP4) activations and weights ("实现差距：GMM Kernel（V1

@@ -30,7 +30,8 @@ TAIL_V, SIZES_V = [FAKE, 1 << 20, None], [FAKE, 4, 512, 256, 256]
 FWD = (["x", "w"] + SIZES + ["h", "gu", "guq", "gus"] + TAIL, [FAKE, FAKE] + SIZES_V + [FAKE, FAKE, None, None] + TAIL_V)
 BWD = (["dy", "w2", "gu", "guq", "gus"] + SIZES + ["dgu", "h"] + TAIL,
        [FAKE, FAKE, None, FAKE, FAKE] + SIZES_V + [FAKE, FAKE] + TAIL_V)
-WGRAD = (["xq", "xs", "dy"] + SIZES + ["dw"] + TAIL, [FAKE] * 3 + SIZES_V + [FAKE] + TAIL_V)
+WGRAD = (["xq", "xs", "dy"] + SIZES + ["dw", "scratch", "sbytes"] + TAIL,
+         [FAKE] * 3 + SIZES_V + [FAKE, FAKE, 1 << 30] + TAIL_V)
 MX4 = (["xq", "xs", "wq", "ws"] + SIZES + ["fuse", "out"] + TAIL, [FAKE] * 4 + SIZES_V + [0, FAKE] + TAIL_V)
 MX4Q = (["xq", "xs", "wq", "ws"] + SIZES + ["h", "hq", "hs"] + TAIL, [FAKE] * 4 + SIZES_V + [FAKE] * 3 + TAIL_V)
 
@@ -55,7 +56,7 @@ def test_swiglu_bwd_refusals(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", COMMON + [
     (dict(xq=None), 1), (dict(xs=None), 1), (dict(dy=None), 1), (dict(dw=None), 1), (dict(xq=FAKE + 8), 3),
-    (dict(dw=FAKE + 2), 3)])
+    (dict(dw=FAKE + 2), 3), (dict(scratch=FAKE + 4), 3)])
 def test_wgrad_refusals(lib, kw, code):
     assert _call(lib.tgmm_fp8_ckpt, *WGRAD, kw) == code
 

@@ -121,6 +121,34 @@ def test_wgrad(sizes, M, K, N):
     R.check(bf16_to_np64(dw.t), ref, err, "dw")
 
 
+@pytest.mark.parametrize("sizes,M,K,N", [
+    ([5000], 5000, 128, 128), ([4097], 4100, 256, 384), ([0, 9000, 70, 1], 9100, 384, 256), ([600, 2500], 3100, 512, 256)])
+def test_wgrad_of_few_tiles_splits_the_rows(sizes, M, K, N):
+    rng = np.random.default_rng(M + K + N)
+    G = len(sizes)
+    assert gmm.tgmm_fp8_ckpt_scratch_bytes(G, M, K, N) >= 2 * 4 * G * K * N
+    xq, xs = gmm.quantize_lhs(to_dev_bf16(normal_bf16((M, K), 1.0, rng, outlier_p=0.01)))
+    dy = normal_bf16((M, N), 1.0, rng)
+    args = (xq, xs, to_dev_bf16(dy), to_dev(np.array(sizes, np.int32)))
+    dw = _guard((G, K, N), torch.bfloat16)
+    work = gmm.Workspace(G, M)
+    gmm.tgmm_ckpt(*args, dw=dw.t, workspace=work)
+    torch.cuda.synchronize()
+    assert work.status() == 0
+    dw.check("dw")
+    ref, err = R.wgrad(xq.cpu().numpy(), xs.cpu().numpy(), _f64(dy), sizes)
+    R.check(bf16_to_np64(dw.t), ref, err, "dw in parts")
+    again = gmm.tgmm_ckpt(*args, workspace=work)
+    assert torch.equal(again.view(torch.int16), dw.t.view(torch.int16))  # the parts are added in order
+    # without scratch, each tile is one pair's work
+    whole = torch.empty_like(dw.t)
+    assert gmm.tgmm_fp8_ckpt(*args, G, M, K, N, whole, None, 0, work.buf, work.nbytes) == 0
+    R.check(bf16_to_np64(whole), ref, err, "dw whole")
+    short = torch.empty(64, dtype=torch.uint8, device="cuda")
+    assert gmm.tgmm_fp8_ckpt(*args, G, M, K, N, whole, short, 64, work.buf, work.nbytes) == 8
+    assert work.status() == 0
+
+
 def test_gradients_against_differences():
     """The loss sum(dy * y), y = h W2, differentiated by central differences of
     the 64-bit forward in every coordinate of one row's gate | up values and
