@@ -178,39 +178,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (leader && lane == 0) {
       constexpr uint32_t idesc = make_idesc(1u /*bf16*/, true, true, 2 * kBM, BN);
-      uint32_t c = 0, t = 0;
-      bool ok = true;
+      const uint32_t a_lo0 = desc_lo_sw128(smem_u32(oper), kBoxBytes);
+      const uint32_t b_lo0 = desc_lo_sw128(smem_u32(ring) + kBoxBytes, kBoxBytes);
+      RingPos<kRing> r;
+      RingPos<kOper> o;
+      RingPos<2> acc;
+      bool ok = true, any = false, next_ready = false;
       int4 e;
       for (uint32_t i = 0; ok && queue.get(i, e, false, 0, abort_word, lim) && e.x >= 0; ++i) {
         if (e.w <= e.z) continue;  // empty group: the epilogues write zeros
-        const uint32_t b = t & 1u, tph = (t >> 1) & 1u;
-        if (!mbar_wait(&tempty[b], tph ^ 1u, abort_word, lim)) break;
-        const uint32_t d = tbase + b * BN;
-        for (int r = e.z; r < e.w; r += kChunk) {
-          const uint32_t j = c % kOper, ph = (c / kOper) & 1u;
-          if (!mbar_wait(&ready[j], ph, abort_word, lim)) {
+        if (!mbar_wait(&tempty[acc.slot], acc.phase ^ 1u, abort_word, lim)) break;
+        tc_fence_after();
+        const uint32_t d = tbase + acc.slot * BN;
+        uint32_t more = 0;  // the unit's first product overwrites the accumulator
+        for (int live = e.w - e.z; live > 0; live -= kChunk) {
+          if (!next_ready && !mbar_wait(&ready[o.slot], o.phase, abort_word, lim)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const int live = e.w - r;
-          const int steps = live < kChunk ? (live + 15) / 16 : 4;
-          const uint32_t a_addr = smem_u32(oper + j * kOperBytes);
-          const uint32_t b_addr = smem_u32(ring + (c % kRing) * kSlotBytes + kBoxBytes);
+          const uint32_t a_lo = a_lo0 + o.slot * (kOperBytes >> 4), b_lo = b_lo0 + r.slot * (kSlotBytes >> 4);
+          uint64_t* freed = &empty[r.slot];
+          r.advance();
+          o.advance();
+          next_ready = mbar_test(&ready[o.slot], o.phase);  // answered while the products are issued
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (q < steps)
-              mma_bf16_pair(d, smem_desc_sw128(a_addr + 2048 * q, kBoxBytes, 1024),
-                            smem_desc_sw128(b_addr + 2048 * q, kBoxBytes, 1024), idesc, (r > e.z || q > 0) ? 1u : 0u);
+            if (16 * q < live)
+              mma_bf16_pair(d, desc_sw128(a_lo + (2048 >> 4) * q), desc_sw128(b_lo + (2048 >> 4) * q), idesc,
+                            q > 0 ? 1u : more);
           }
-          mma_commit_pair(&empty[c % kRing], 0x3);
-          ++c;
+          mma_commit_pair(freed, 0x3);
+          more = 1;
         }
+        any |= more != 0;
         if (!ok) break;
-        mma_commit_pair(&tfull[b], 0x3);
-        ++t;
+        mma_commit_pair(&tfull[acc.slot], 0x3);
+        acc.advance();
       }
-      if (c > 0) {
+      if (any) {
         volatile int no_abort = 0;
         mma_commit_pair(drain, 0x1);
         mbar_wait(drain, 0, &no_abort, kDrainLimitNs);
@@ -305,7 +310,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t group = static_cast<uint32_t>(et) / (32 * kExpandWarps);
     const int row = et % (32 * kExpandWarps) >> 1, hb = et & 1;
     const uint32_t ready0 = mapa_shared(smem_u32(ready), 0);
-    uint32_t c = 0;
+    static_assert(kGroups == 2 && kOper == kRing - 1, "the positions below");
+    RingPos<kRing> s;      // the chunk's slot
+    RingPos<kOper> o;      // its operand buffer
+    // That buffer is free once the products of the chunk kOper before are done:
+    // it lay in the slot after this one (kRing - kOper on).  That slot's next
+    // phase cannot complete before this chunk's, so the parity is unambiguous.
+    uint32_t c = 0;        // chunks so far
     bool ok = true;
     int4 e;
     for (uint32_t i = 0; ok && queue.get(i, e, true, lane, abort_word, lim) && e.x >= 0; ++i) {
@@ -313,28 +324,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float* xs = args.xs + static_cast<long long>(k0 / 128) * args.M;
       const bool inside = k0 < args.K;
       // this group's chunks of the unit; a chunk's scale is loaded one ahead
-      const int mine = (c % kGroups == group ? 0 : kChunk) + row;
+      const int mine = ((c & 1) == group ? 0 : kChunk) + row;
       float next = inside && e.z + mine < e.w ? __ldg(xs + e.z + mine) : 0.0f;
-      for (int r = e.z; r < e.w; r += kChunk, ++c) {
-        if (c % kGroups != group) continue;
+      for (int r = e.z; r < e.w; r += kChunk, ++c, s.advance(), o.advance()) {
+        if ((c & 1) != group) continue;
         const float scale = next;
         const int ahead = r + kGroups * kChunk + row;
         next = inside && ahead < e.w ? __ldg(xs + ahead) : 0.0f;
         const int live = e.w - r;
-        const uint32_t s = c % kRing, j = c % kOper;
-        bool got = mbar_wait(&full[s], (c / kRing) & 1u, abort_word, lim);
-        // the operand buffer is free once the products of chunk c - kOper are
-        // done (kOper < kRing: that slot's next phase cannot complete before
-        // this chunk's)
-        if (got && c >= kOper)
-          got = mbar_wait(&empty[(c - kOper) % kRing], ((c - kOper) / kRing) & 1u, abort_word, lim);
+        bool got = mbar_wait(&full[s.slot], s.phase, abort_word, lim);
+        if (got && c >= kOper) {
+          RingPos<kRing> f = s;
+          f.advance();  // kOper chunks back: the next slot, in the phase before
+          got = mbar_wait(&empty[f.slot], f.phase ^ 1u, abort_word, lim);
+        }
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        uint8_t* slot = ring + s * kSlotBytes;
+        uint8_t* slot = ring + s.slot * kSlotBytes;
         const uint8_t* src = slot + row * 128;
-        uint8_t* dst = oper + j * kOperBytes + hb * kBoxBytes + row * 128;
+        uint8_t* dst = oper + o.slot * kOperBytes + hb * kBoxBytes + row * 128;
         const int sw = row & 7;
         if (row < live) {
           // 16 codes at a time; the halves run in opposite order so that their
@@ -359,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();  // the tensor core reads what was written here
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(ready0 + j * 8u);
+        if (lane == 0) mbar_arrive_remote(ready0 + o.slot * 8u);
       }
     }
   }
