@@ -149,9 +149,10 @@ def load():
 def _p(t) -> int | None:
     if t is None:
         return None
-    if isinstance(t, torch.Tensor):
-        return t.data_ptr() if t.numel() > 0 else None
-    return int(t)
+    try:
+        return t.data_ptr() or None  # a tensor without elements has the address 0
+    except AttributeError:
+        return int(t)
 
 
 def _s(stream) -> int | None:

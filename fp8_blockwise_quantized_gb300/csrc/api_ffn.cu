@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "host.cuh"
 #include "kernels.cuh"
+#include "metadata.cuh"
 
 using namespace gmm;
 
@@ -30,6 +31,9 @@ const Tile* tiles_of(const void* workspace, int G) {
 // full, and none without rows.
 long long max_tiles(int G, int64_t M) { return (M + kBM - 1) / kBM + (M < G ? M : G); }
 
+// Whether a kernel that can reads the sizes itself: no metadata launch.
+bool scanned(const int32_t* group_sizes, int G, int64_t M) { return group_sizes && G <= kScanGroups && M > 0; }
+
 // The device, the workspace and (unless group_sizes is NULL) the metadata.
 gmm_status begin(const int32_t* group_sizes, int G, int64_t M, void* workspace, size_t workspace_bytes,
                  cudaStream_t s, int* sms) {
@@ -40,6 +44,13 @@ gmm_status begin(const int32_t* group_sizes, int G, int64_t M, void* workspace, 
 }
 
 gmm_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? GMM_OK : host_cuda_fail(e, what); }
+
+// One CTA per unit up to one per SM, and one without a unit, if there is room,
+// for the CTA that fills the workspace when the kernel reads the sizes itself.
+int grid_of(long long units, const int32_t* sizes, int sms) {
+  if (sizes) ++units;
+  return static_cast<int>(units < sms ? units : sms);
+}
 
 // The kernels' unit indices are 32-bit, with the grid's claims on top.
 constexpr long long kMaxUnits = 1LL << 30;
@@ -67,7 +78,8 @@ gmm_status mx4_entry(const void* xq, const void* xs, const void* wq, const void*
   if (max_tiles(G, M) * (N / 64) > kMaxUnits) return GMM_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = 0;
-  if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
+  const int32_t* sizes = scanned(group_sizes, G, M) ? group_sizes : nullptr;
+  if ((st = begin(sizes ? nullptr : group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
   if (M == 0) return GMM_OK;
   // 128-column units while one per SM covers the call: latency (8 row tiles, K
   // 2048, N 2 x 512: 8.4 us, 9.2 with 256; 128 units of K 512: 6.3 and 6.5).
@@ -85,6 +97,8 @@ gmm_status mx4_entry(const void* xq, const void* xs, const void* wq, const void*
   Mx4Args a{};
   a.meta = static_cast<const int32_t*>(workspace);
   a.tiles = tiles_of(workspace, G);
+  a.sizes = sizes;
+  a.G = G;
   a.xs = static_cast<const uint32_t*>(xs);
   a.ws = static_cast<const uint8_t*>(ws);
   a.out = static_cast<uint16_t*>(out);
@@ -97,7 +111,7 @@ gmm_status mx4_entry(const void* xq, const void* xs, const void* wq, const void*
   a.bn = bn;
   a.wait_limit_ns = host_wait_limit_ns();
   const long long units = max_tiles(G, M) * (Nw / bn);
-  return launched(launch_gmm_mx4(map_a, map_b, map_out, a, static_cast<int>(units < sms ? units : sms), s),
+  return launched(launch_gmm_mx4(map_a, map_b, map_out, a, grid_of(units, sizes, sms), s),
                   "gmm_mx4 kernel launch");
 }
 
@@ -117,7 +131,8 @@ gmm_status gmm_bf16_swiglu_fwd(const void* x, const void* w, const int32_t* grou
   if (units > kMaxUnits) return GMM_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = 0;
-  if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
+  const int32_t* sizes = scanned(group_sizes, G, M) ? group_sizes : nullptr;
+  if ((st = begin(sizes ? nullptr : group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
   if (M == 0) return GMM_OK;
   CUtensorMap map_x, map_w;
   if ((st = host_encode_2d(&map_x, kBf16, 2, x, K, M, 64, 128)) != GMM_OK) return st;
@@ -125,6 +140,8 @@ gmm_status gmm_bf16_swiglu_fwd(const void* x, const void* w, const int32_t* grou
   SwigluArgs a{};
   a.meta = static_cast<const int32_t*>(workspace);
   a.tiles = tiles_of(workspace, G);
+  a.sizes = sizes;
+  a.G = G;
   a.h = static_cast<uint16_t*>(h);
   a.gu = static_cast<uint16_t*>(gu);
   a.guq = static_cast<uint8_t*>(guq);
@@ -133,7 +150,7 @@ gmm_status gmm_bf16_swiglu_fwd(const void* x, const void* w, const int32_t* grou
   a.K = static_cast<int>(K);
   a.N = static_cast<int>(N);
   a.wait_limit_ns = host_wait_limit_ns();
-  return launched(launch_gmm_swiglu_fwd(map_x, map_w, a, static_cast<int>(units < sms ? units : sms), s),
+  return launched(launch_gmm_swiglu_fwd(map_x, map_w, a, grid_of(units, sizes, sms), s),
                   "gmm_swiglu forward launch");
 }
 
@@ -149,7 +166,8 @@ gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, c
   if (units > kMaxUnits) return GMM_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = 0;
-  if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
+  const int32_t* sizes = scanned(group_sizes, G, M) ? group_sizes : nullptr;
+  if ((st = begin(sizes ? nullptr : group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
   if (M == 0) return GMM_OK;
   CUtensorMap map_dy, map_w2;
   if ((st = host_encode_2d(&map_dy, kBf16, 2, dy, K, M, 64, 128)) != GMM_OK) return st;
@@ -157,6 +175,8 @@ gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, c
   SwigluArgs a{};
   a.meta = static_cast<const int32_t*>(workspace);
   a.tiles = tiles_of(workspace, G);
+  a.sizes = sizes;
+  a.G = G;
   a.h = static_cast<uint16_t*>(h);
   a.gu = static_cast<uint16_t*>(const_cast<void*>(gu));
   a.guq = static_cast<uint8_t*>(const_cast<void*>(guq));
@@ -166,7 +186,7 @@ gmm_status gmm_bf16_swiglu_bwd(const void* dy, const void* w2, const void* gu, c
   a.K = static_cast<int>(K);
   a.N = static_cast<int>(N);
   a.wait_limit_ns = host_wait_limit_ns();
-  return launched(launch_gmm_swiglu_bwd(map_dy, map_w2, a, static_cast<int>(units < sms ? units : sms), s),
+  return launched(launch_gmm_swiglu_bwd(map_dy, map_w2, a, grid_of(units, sizes, sms), s),
                   "gmm_swiglu backward launch");
 }
 

@@ -70,6 +70,12 @@ struct Mx4Tile {
                 "barrier area");
 };
 
+// Unit u: row tile u / per_tile, column block u % per_tile.
+struct Mx4Units {
+  uint32_t num, per_tile;
+  __device__ uint2 at(uint32_t u) const { return make_uint2(u / per_tile, u % per_tile); }
+};
+
 // Instruction descriptor of kind::mxf4: E2M1 operands (bits 7-9, 10-11: 1),
 // E8M0 scales (bit 23), N >> 3 in bits 17-22, M >> 7 in bits 27-28; which pair
 // of a scale word's four bytes applies (0 or 2): B's in bits 4-5, A's in 29-30.
@@ -139,8 +145,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();  // inputs and metadata come from earlier kernels
 
-  const uint32_t per_tile = args.N / kOutCols;
-  const uint32_t num_units = static_cast<uint32_t>(args.meta[kWsNumTiles]) * per_tile;
   const int KB = args.K / 128, KS = (KB + 1) / 2;
   const int Nw = FUSE ? 2 * args.N : args.N;
   const uint64_t lim = args.wait_limit_ns;
@@ -245,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kEpiWarp0) {
-    if (warp == 2 && lane == 0)  // warp 3 has no role
-      queue.schedule(
-          args.tiles, const_cast<int32_t*>(args.meta) + kWsClaimed, num_units,
-          [&](uint32_t u) { return make_uint2(u / per_tile, u % per_tile); }, abort_word, lim);
+    if (warp == 2)  // warp 3 has no role
+      schedule_tiles(
+          queue, args, [&](uint32_t tiles) { const uint32_t n = args.N / kOutCols; return Mx4Units{tiles * n, n}; },
+          lane, abort_word, lim);
   } else if (warp >= kScaleWarp0) {
     regs_dec<kScaleRegs>();
     const uint32_t t_scale = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kScaleCol0;
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long N = args.N;
     // rows [S, M) belong to no group: zeros (zero scale bytes too, as
     // quantising zero rows gives)
-    const long long S = args.meta[kWsS], rest = args.M - S;
+    const long long S = grouped_rows(args, tid, staging), rest = args.M - S;
     if (rest > 0) {
       const long long first = tid + static_cast<long long>(blockIdx.x) * kEpiThreads;
       const long long step = static_cast<long long>(gridDim.x) * kEpiThreads;

@@ -345,8 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();  // inputs and metadata come from earlier kernels
 
-  const Units units(static_cast<uint32_t>(args.meta[kWsNumTiles]), args.N, FWD, FWD || args.N % 256 == 0,
-                    !FWD || !E4M3);
   const int KS = args.K / 64;
   const uint64_t lim = args.wait_limit_ns;
 
@@ -440,10 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 2) {
-    if (lane == 0)
-      queue.schedule(
-          args.tiles, const_cast<int32_t*>(args.meta) + kWsClaimed, units.num,
-          [&](uint32_t u) { return units.at(u); }, abort_word, lim);
+    schedule_tiles(
+        queue, args,
+        [&](uint32_t tiles) { return Units(tiles, args.N, FWD, FWD || args.N % 256 == 0, !FWD || !E4M3); }, lane,
+        abort_word, lim);
   } else if (warp >= kEpiWarp0) {
     regs_inc<kEpiRegs>();
     const int half = (warp - kEpiWarp0) >> 2;
@@ -451,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = static_cast<int>(threadIdx.x) - 32 * kEpiWarp0;
     const uint32_t t_lane = tbase + (static_cast<uint32_t>(quad * 32) << 16);
     // rows [S, M) belong to no group
-    const long long S = args.meta[kWsS], rest = args.M - S, N = args.N;
+    const long long S = grouped_rows(args, tid, staging), rest = args.M - S, N = args.N;
     if (rest > 0) {
       if (args.h) zero_span(args.h + S * N, rest * N * 2, tid);
       if (!FWD) {

@@ -97,24 +97,26 @@ struct TgmmArgs {
 struct SwigluArgs {
   const int32_t* meta;    // workspace words
   const Tile* tiles;      // workspace tile list (128-row tiles)
+  const int32_t* sizes;   // group_sizes, G <= kScanGroups, or NULL: the metadata is in the workspace
   uint16_t* h;            // bf16 [M][N] (backward: may be null)
   uint16_t* gu;           // kept gate | up, bf16 [M][2N], or null:
   uint8_t* guq;           // e4m3 codes [M][2N] with
   float* gus;             // fp32 [2N/128][M] scales
   uint16_t* dgu;          // backward: gradient of gate | up, bf16 [M][2N]
-  int M, K, N;
+  int G, M, K, N;
   uint64_t wait_limit_ns;
 };
 
 struct Mx4Args {
   const int32_t* meta;    // workspace words
   const Tile* tiles;      // workspace tile list (128-row tiles)
+  const int32_t* sizes;   // group_sizes, G <= kScanGroups, or NULL: the metadata is in the workspace
   const uint32_t* xs;     // E8M0 scales of x, words of four blocks [K/128][M]
   const uint8_t* ws;      // E8M0 scales of w, tiles [G][Nw/128][K/128][512]
   uint16_t* out;          // bf16 [M][N] (may be null with hq)
   uint8_t* hq;            // MXFP4 output: codes [M][N/2] (null: none)
   uint32_t* hs;           // and scale words [N/128][M]
-  int M, K, N;            // N = output columns
+  int G, M, K, N;         // N = output columns
   int fuse;               // 1: silu(gate) * up, w has 2N columns
   int bn;                 // weight columns per unit (128 or 256)
   uint64_t wait_limit_ns;

@@ -271,11 +271,51 @@ def test_other_stream_reused_metadata_and_repeat():
     assert work.buf[16:24].view(torch.int32).tolist() == [0, 0]
 
 
+@pytest.mark.parametrize("G", [1, 9, 256, 257, 700])
+def test_metadata_left_for_later_calls(G):
+    """A call with group_sizes leaves the workspace as group_metadata does, whether it read the
+    sizes in the kernel (up to 256 groups) or after a metadata pass, and its results agree with a
+    later call that reuses the metadata."""
+    rng = np.random.default_rng(G)
+    K, N = 128, 128
+    sizes = np.where(rng.random(G) < 0.3, 0, rng.integers(0, 7, G)).astype(np.int32)
+    sizes[rng.integers(G)] = 300
+    M = int(sizes.sum()) + 5
+    x, w = to_dev_bf16(normal_bf16((M, K), 1.0, rng)), to_dev_bf16(normal_bf16((G, K, 2 * N), 0.08, rng))
+    st = to_dev(sizes)
+    want, got = gmm.Workspace(G, M), gmm.Workspace(G, M)
+    gmm.group_metadata(st, M, workspace=want)
+    h, gu = gmm.swiglu_fwd(x, w, st, workspace=got)
+    torch.cuda.synchronize()
+    assert got.header() == want.header() and got.offsets() == want.offsets() and got.order() == want.order()
+    assert torch.equal(got.tiles(), want.tiles()) and torch.equal(got.pair_tiles(), want.pair_tiles())
+    h2, gu2 = gmm.swiglu_fwd(x, w, None, workspace=got)
+    assert torch.equal(h.view(torch.int16), h2.view(torch.int16))
+    assert torch.equal(gu.view(torch.int16), gu2.view(torch.int16))
+    ref, err, _, _ = R.swiglu_fwd(_f64(normal_bits(x)), _f64(normal_bits(w)), sizes)
+    R.check(bf16_to_np64(h), ref, err, "h")
+    mx = gmm.mx4_quantize_lhs(x) + gmm.mx4_quantize_rhs(w)
+    a = gmm.mx4_fwd(*mx, st, fuse=True, workspace=want)
+    b = gmm.mx4_fwd(*mx, None, fuse=True, workspace=got)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert want.status() == got.status() == 0
+
+
+def normal_bits(t):
+    return t.view(torch.int16).cpu().numpy().view(np.uint16)
+
+
 def test_invalid_sizes_are_reported():
     work = gmm.Workspace(2, 256)
     x = torch.zeros((256, 128), dtype=torch.bfloat16, device="cuda")
     w = torch.zeros((2, 128, 256), dtype=torch.bfloat16, device="cuda")
     gmm.swiglu_fwd(x, w, torch.tensor([200, 100], dtype=torch.int32, device="cuda"), workspace=work)
+    assert work.status() == gmm.binding.GMM_ERR_GROUP_SIZES
+    gmm.swiglu_bwd(x, w.transpose(1, 2).contiguous(), torch.zeros((256, 512), dtype=torch.bfloat16, device="cuda"),
+                   torch.tensor([-5, 100], dtype=torch.int32, device="cuda"), workspace=work)
+    assert work.status() == gmm.binding.GMM_ERR_GROUP_SIZES
+    mx = gmm.mx4_quantize_lhs(x) + gmm.mx4_quantize_rhs(w)
+    gmm.mx4_fwd(*mx, torch.tensor([255, 2], dtype=torch.int32, device="cuda"), workspace=work)
     assert work.status() == gmm.binding.GMM_ERR_GROUP_SIZES
     xq, xs = gmm.quantize_lhs(x)
     gmm.tgmm_ckpt(xq, xs, x, torch.tensor([-1, 100], dtype=torch.int32, device="cuda"), workspace=work)
