@@ -80,6 +80,8 @@ EDGE = [
     ([1000, 3, 700, 0, 0, 297], 2100, 1152, 512),
     # enough units for the wide ones: 43 row tiles x 4 column blocks
     ([2500, 31, 0, 2900], 5500, 512, 1024),
+    # an odd number of K blocks over many units
+    ([2500, 31, 0, 1500, 1400], 5500, 640, 2048),
 ]
 
 
