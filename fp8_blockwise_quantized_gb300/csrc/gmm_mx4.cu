@@ -39,11 +39,13 @@ constexpr int kScaleWarp0 = 12;
 constexpr int kScaleWarps = 4;
 constexpr int kQueueReaders = 2 + kEpiWarps + kScaleWarps;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
-// The scales come in slots of kScaleBlocks 128-wide K blocks (two K steps).
-constexpr int kScaleBlocks = 4;
+// The scales come in slots of kScaleBlocks 128-wide K blocks (four K steps): a
+// slot costs its loads' latency and a store to tensor memory, whatever its size
+// (two steps a slot: 99 us for 94 in the gate/up product named above).
+constexpr int kScaleBlocks = 8;
 // Register split: 128 per thread at launch; the epilogue warpgroups take a
 // whole 32 x 128 part of the accumulator into registers at once.
-constexpr uint32_t kControlRegs = 56, kEpiRegs = 184, kScaleRegs = 88;
+constexpr uint32_t kControlRegs = 56, kEpiRegs = 168, kScaleRegs = 120;
 static_assert(128 * (kControlRegs + kScaleRegs) + 256 * kEpiRegs <= kThreads * 128,
               "register split exceeds the launch budget");
 
@@ -60,7 +62,7 @@ struct Mx4Tile {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kScaleCol0 = 256;                               // first tensor-memory column of the scales
   static constexpr int kScaleCols = kScaleBlocks * 4 * (1 + kTilesB);  // columns per scale slot
-  static constexpr int kScaleSlots = 5;
+  static constexpr int kScaleSlots = 256 / kScaleCols;
   static constexpr int kStagingBytes = kEpiWarps * kBoxes * 4096;
   static constexpr int kBarBytes = 512;
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kBarBytes;
@@ -270,8 +272,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint8_t* w1 = w0 + static_cast<long long>(FUSE ? args.N / 128 : 1) * KB * 512;
       for (int k0 = 0; k0 < KB; k0 += kScaleBlocks, ++q) {
         uint32_t v[4 * kScaleBlocks], w[4 * C::kTilesB * kScaleBlocks];
+        const bool upper = k0 + 4 < KB;
 #pragma unroll
         for (int kb = 0; kb < kScaleBlocks; ++kb) {
+          if (kb >= 4 && !upper) break;
           // K blocks past the last one repeat it: stored, but not multiplied
           const long long k = min(k0 + kb, KB - 1);
           const uint32_t* src = xs + k * args.M;
@@ -297,10 +301,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();  // the products that read the slot are done
         const uint32_t t = t_scale + slot * C::kScaleCols;
-        tmem_st_32x16(t, v);
 #pragma unroll
-        for (int n = 0; n < C::kTilesB; ++n)
-          tmem_st_32x16(t + 16 + 16 * n, *reinterpret_cast<uint32_t(*)[16]>(w + 16 * n));
+        for (int h = 0; h < kScaleBlocks / 4; ++h) {
+          if (h > 0 && !upper) break;
+          tmem_st_32x16(t + 16 * h, *reinterpret_cast<uint32_t(*)[16]>(v + 16 * h));
+#pragma unroll
+          for (int n = 0; n < C::kTilesB; ++n)
+            tmem_st_32x16(t + 4 * kScaleBlocks + 16 * (C::kTilesB * h + n),
+                          *reinterpret_cast<uint32_t(*)[16]>(w + 16 * (C::kTilesB * h + n)));
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
