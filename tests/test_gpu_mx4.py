@@ -180,6 +180,31 @@ def test_other_stream_reused_metadata_and_repeat():
     assert work.buf[16:24].view(torch.int32).tolist() == [0, 0]
 
 
+def test_offsets_past_32_bits():
+    """x and the output of more than 2^31 elements: rows on each side of element 2^31 and the last."""
+    K, N = 128, 4096
+    M = 2 ** 31 // N + 300
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    wq, ws = gmm.mx4_quantize_rhs(torch.randn((1, K, N), generator=g, device="cuda", dtype=torch.bfloat16) / 8)
+    st = torch.tensor([M - 5], dtype=torch.int32, device="cuda")
+    rows = torch.tensor([1, 2 ** 31 // N - 1, 2 ** 31 // N, M - 6], device="cuda")
+    xq, xs = gmm.mx4_quantize_lhs(x)
+    out = gmm.mx4_fwd(xq, xs, wq, ws, st)
+    x64 = R.mx4_values(*R.mx4_quantize(x[rows].view(torch.int16).cpu().numpy().view(np.uint16)))
+    w64 = R.mx4_values(R.unpack4(wq.cpu().numpy()), R.mx4_rhs_scales(ws.cpu().numpy())).transpose(0, 2, 1)
+    ref, mag = R.grouped(x64, w64, [len(rows)])
+    R.check(bf16_to_np64(out[rows]), ref, R.BF16 * np.abs(ref) + R.SUM * mag + R.TINY, "out")
+    assert torch.all(out[M - 5:] == 0)
+    # and the quantiser: a wide x
+    wide = torch.randn((2 ** 31 // 8192 + 9, 8192), generator=g, device="cuda", dtype=torch.bfloat16)
+    q, s = gmm.mx4_quantize_lhs(wide)
+    for r in (0, 2 ** 31 // 8192, len(wide) - 1):
+        codes, byte = R.mx4_quantize(wide[r:r + 1].view(torch.int16).cpu().numpy().view(np.uint16))
+        assert np.array_equal(R.unpack4(q[r:r + 1].cpu().numpy()), codes)
+        assert np.array_equal(s[:, r].reshape(1, -1).cpu().numpy(), byte)
+
+
 def test_no_rows():
     wq, ws = gmm.mx4_quantize_rhs(torch.zeros((2, 128, 128), dtype=torch.bfloat16, device="cuda"))
     xq, xs = gmm.mx4_quantize_lhs(torch.zeros((0, 128), dtype=torch.bfloat16, device="cuda"))

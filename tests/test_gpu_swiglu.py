@@ -226,6 +226,32 @@ def test_rows_of_others_do_not_leak():
         assert torch.equal(clean[5][g].view(torch.int16), got[5][g].view(torch.int16))
 
 
+def test_offsets_past_32_bits():
+    """gate | up and dgu of more than 2^31 elements: the last rows, and a row on each side of
+    element 2^31, against the 64-bit formulas."""
+    K, N = 128, 1024
+    M = 2 ** 31 // (2 * N) + 700  # 1,049,276 rows
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn((1, K, 2 * N), generator=g, device="cuda", dtype=torch.bfloat16) / 16
+    w2 = torch.randn((1, N, K), generator=g, device="cuda", dtype=torch.bfloat16) / 16
+    st = torch.tensor([M - 3], dtype=torch.int32, device="cuda")
+    rows = torch.tensor([0, 2 ** 31 // (2 * N) - 1, 2 ** 31 // (2 * N), M - 4], device="cuda")
+    sub = [len(rows)]
+    work = gmm.Workspace(1, M)
+    h, gu = gmm.swiglu_fwd(x, w, st, workspace=work)
+    rh, rh_err, rgu, err = R.swiglu_fwd(bf16_to_np64(x[rows]), bf16_to_np64(w), sub)
+    R.check(bf16_to_np64(h[rows]), rh, rh_err, "h")
+    R.check(bf16_to_np64(gu[rows]), rgu, R.BF16 * np.abs(rgu) + err + R.TINY, "gate | up")
+    assert torch.all(gu[M - 3:] == 0)
+    dgu, h2 = gmm.swiglu_bwd(x, w2, gu, st, workspace=work)
+    rd, rd_err, rh, rh_err = R.swiglu_bwd(bf16_to_np64(x[rows]), bf16_to_np64(w2), bf16_to_np64(gu[rows]), sub)
+    R.check(bf16_to_np64(dgu[rows]), rd, rd_err, "dgu")
+    R.check(bf16_to_np64(h2[rows]), rh, rh_err, "h again")
+    assert torch.all(dgu[M - 3:] == 0)
+    assert work.status() == 0
+
+
 def test_saturated_activation():
     """Gates far outside exp's range give the limits 0 and a, without NaN."""
     M, N, K = 4, 128, 128
