@@ -250,8 +250,8 @@ gmm_status gmm_mx4_quantize_lhs(const void* x, int64_t M, int64_t K, void* xq, v
   const long long steps = (M + 7) / 8 * (K / 128);  // a warp each, 8 warps per CTA
   if (steps >= (1LL << 31)) return GMM_ERR_SHAPE;   // 4 TB of x
   long long grid = (steps + 7) / 8;
-  // many short CTAs: 65536 x 2048 takes 59.8 us with 32 per SM, 63.4 with 16,
-  // 67.0 with 8 and 64.5 with one step per warp
+  // many short CTAs: with an earlier form of the kernel, 65536 x 2048 took 59.8
+  // us with 32 per SM, 63.4 with 16, 67.0 with 8 and 64.5 with one step a warp
   if (grid > static_cast<long long>(sms) * 32) grid = static_cast<long long>(sms) * 32;
   return launched(launch_pdl(mx4_quantize_lhs_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
                              static_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), static_cast<int>(M),

@@ -35,13 +35,23 @@ __device__ __forceinline__ uint32_t mx4_inverse2(uint32_t byte) { return (254u -
 // nearest, ties to even, saturating at 6.  The quotient is a bf16 product with
 // a power of two: exact, or too small for any code but 0.
 __device__ __forceinline__ uint32_t mx4_codes8(const uint32_t (&p)[4], uint32_t inv2) {
-  uint32_t q = 0;
+  float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t s = as_bits(__hmul2(as_bf162(p[i]), as_bf162(inv2)));
-    const float2 v = make_float2(__uint_as_float(s << 16), __uint_as_float(s & 0xffff0000u));
-    q |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest)) << (8 * i);
+    v[2 * i] = __uint_as_float(s << 16);
+    v[2 * i + 1] = __uint_as_float(s & 0xffff0000u);
   }
+  // cvt's first source goes to the upper code of the pair
+  uint32_t q;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(q)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return q;
 }
 

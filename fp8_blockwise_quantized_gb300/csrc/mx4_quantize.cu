@@ -10,11 +10,12 @@ namespace gmm {
 // four scale bytes of 128 columns.  A half-warp takes one row's 128 columns
 // (16 lanes x 16 bytes, four lanes per block of 32); a warp takes the same
 // columns of eight consecutive rows, so that its scale words are 32 contiguous
-// bytes.  59.8 us at 65536 x 2048, 5.7 TB/s of mixed traffic, for 50.7 at the
-// copy rate; packed bf16 arithmetic and 32-bit index arithmetic took it there
-// from 65.5.  Prefetching a warp's next step (69.9 us), rows of 256 columns a
-// load (66 to 79) and streaming through shared memory by bulk copies (69 to 104)
-// were slower.
+// bytes.  52.8 us at 65536 x 2048, 6.4 TB/s of the 6.8 that a copy reaches (floor
+// 50.7).  What bound it was instructions: packed bf16 arithmetic and 32-bit
+// indices took it from 65.5 to 59.8 us, one conversion block for the eight codes
+// and a path without row checks from there.  Prefetching a warp's next step
+// (69.9 us for 65.5), rows of 256 columns a load (66 to 79) and streaming through
+// shared memory by bulk copies (69 to 104) were slower.
 __global__ void __launch_bounds__(256) mx4_quantize_lhs_kernel(const uint4* __restrict__ x, int M, uint32_t KB,
                                                                uint32_t steps, uint32_t* __restrict__ xq,
                                                                uint32_t* __restrict__ xs) {
@@ -26,10 +27,19 @@ __global__ void __launch_bounds__(256) mx4_quantize_lhs_kernel(const uint4* __re
     const uint32_t mg = st / KB, kb = st - mg * KB;
     const int m0 = static_cast<int>(mg * 8) + half * 4;
     const long long at = (static_cast<long long>(m0) * KB + kb) * 16 + l16;  // 16-byte chunk of x, word of xq
+    const uint4* src = x + at;
+    uint32_t* dst = xq + at;
+    const uint32_t ld = 16 * KB;  // a row of x in 16-byte chunks, and of codes in words
+    const int rows = M - m0;      // this half-warp's, when below 4
     uint4 v[4];
+    if (rows >= 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = m0 + i < M ? __ldcs(x + at + static_cast<long long>(i * 16) * KB) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) v[i] = __ldcs(src + static_cast<size_t>(i) * ld);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = i < rows ? __ldcs(src + static_cast<size_t>(i) * ld) : make_uint4(0, 0, 0, 0);
+    }
     uint32_t bytes = 0;  // this lane's block in the four rows
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -41,7 +51,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_lhs_kernel(const uint4* __re
       const uint32_t b = mx4_scale_byte(m2 & 0xffffu);
       const uint32_t q = mx4_codes8(p, mx4_inverse2(b));
       bytes |= b << (8 * i);
-      if (m0 + i < M) xq[at + static_cast<long long>(i * 16) * KB] = q;
+      if (i < rows) dst[static_cast<size_t>(i) * ld] = q;
     }
     // lane i of each half collects row i's word from the four blocks' lanes
     uint32_t word = 0;
@@ -50,7 +60,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_lhs_kernel(const uint4* __re
       const uint32_t t = __shfl_sync(0xffffffffu, bytes, half * 16 + 4 * g);
       word |= (t >> (8 * (l16 & 3)) & 0xffu) << (8 * g);
     }
-    if (l16 < 4 && m0 + l16 < M) xs[static_cast<long long>(kb) * M + m0 + l16] = word;
+    if (l16 < 4 && l16 < rows) xs[static_cast<size_t>(kb) * M + m0 + l16] = word;
   }
 }
 
