@@ -212,7 +212,8 @@ gmm_status tgmm_fp8_ckpt(const void* xq, const float* xs, const void* dy, const 
   const int splits = scratch ? tgmm_ckpt_splits(G, M, K, N, sms) : 1;
   if (splits > 1 && scratch_bytes < static_cast<size_t>(splits) * G * K * N * sizeof(float)) return GMM_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((st = begin(group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
+  const int32_t* sizes = scanned(group_sizes, G, M) ? group_sizes : nullptr;
+  if ((st = begin(sizes ? nullptr : group_sizes, G, M, workspace, workspace_bytes, s, &sms)) != GMM_OK) return st;
   // With M == 0 every group is empty: the kernel only writes zeros and never
   // reads x or dy, so the maps may describe a dummy one-row tensor.
   CUtensorMap map_x, map_dy, map_dw;
@@ -229,6 +230,8 @@ gmm_status tgmm_fp8_ckpt(const void* xq, const float* xs, const void* dy, const 
   a.xs = xs;
   a.parts = static_cast<const float*>(scratch);
   a.splits = splits;
+  a.sizes = sizes;
+  a.tiles = tiles_of(workspace, G);
   a.G = G;
   a.M = static_cast<int>(M);
   a.K = static_cast<int>(K);

@@ -90,6 +90,8 @@ struct TgmmArgs {
   const float* xs;        // 8-bit checkpoint: fp32 [K/128][M] scales of x's codes
   const float* parts;     // 8-bit checkpoint, splits > 1: the parts' sums, fp32 [splits][G][K][N]
   int splits;             // parts that each group's rows are cut into
+  const int32_t* sizes;   // 8-bit checkpoint: group_sizes, G <= kScanGroups, or NULL: the metadata is in the workspace
+  const Tile* tiles;      // 8-bit checkpoint: workspace tile list, filled when sizes is given
 };
 
 // The gated feed-forward block's kernels: the forward (K = columns of x) and

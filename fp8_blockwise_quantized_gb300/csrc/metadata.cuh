@@ -137,6 +137,50 @@ __device__ __forceinline__ void write_group_metadata(const int32_t* __restrict__
   }
 }
 
+// Offsets (G + 1) and the size order (G) of a call with G <= 256 into shared
+// memory, by a whole block; keys: G entries of scratch.  Returns whether the
+// sizes are valid.  sync: a barrier of the block.
+template <typename Sync>
+__device__ __forceinline__ bool share_group_order(const int32_t* __restrict__ sizes, int G, int M, int* offsets,
+                                                  int* order, unsigned long long* keys, int* valid, Sync&& sync) {
+  const int t = threadIdx.x;
+  if (t < 32) {
+    long long r = 0;
+    bool bad = false;
+    int n[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int g = 8 * t + i;
+      n[i] = g < G ? __ldg(sizes + g) : 0;
+      bad |= n[i] < 0;
+      r += n[i];
+    }
+    const long long ri = warp_inclusive_scan(r), total = __shfl_sync(0xffffffffu, ri, 31);
+    const bool ok = !__any_sync(0xffffffffu, bad) && total <= M;
+    int off = static_cast<int>(ri - r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (8 * t + i < G) offsets[8 * t + i] = off;
+      off += n[i];
+    }
+    if (t == 0) {
+      *valid = ok ? 1 : 0;
+      offsets[G] = static_cast<int>(total);
+    }
+  }
+  // as in write_group_metadata: largest first, ties by index
+  if (t < G) keys[t] = (static_cast<unsigned long long>(0x7fffffff - __ldg(sizes + t)) << 32) | static_cast<unsigned>(t);
+  sync();
+  if (t < G) {
+    const unsigned long long mine = keys[t];
+    int rank = 0;
+    for (int j = 0; j < G; ++j) rank += keys[j] < mine ? 1 : 0;
+    order[rank] = t;
+  }
+  sync();
+  return *valid != 0;
+}
+
 // Largest G that a kernel takes straight from group_sizes.
 constexpr int kScanGroups = 256;
 

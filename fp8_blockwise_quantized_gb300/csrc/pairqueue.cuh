@@ -44,10 +44,16 @@ struct PairQueue {
 // group's rows are cut into that many parts of whole chunks: unit u % per_group
 // counts them fastest, and its entry holds the part's rows (none where the
 // group has too few).
+// order and offsets are read with ld (global memory: __ldg).
+struct LoadGlobal {
+  __device__ __forceinline__ int operator()(const int* p) const { return __ldg(p); }
+};
+template <typename Load = LoadGlobal>
 __device__ __forceinline__ void pair_schedule(const PairQueue& queue, volatile int* taken, volatile int* ctaken,
                                               int* claimed, const int* order, const int* offsets, int G,
                                               int per_group, int num_units, int claim_ahead, int max_batch,
-                                              volatile int* abort_word, uint64_t lim, int splits = 1) {
+                                              volatile int* abort_word, uint64_t lim, int splits = 1,
+                                              Load ld = Load{}) {
   const uint32_t odd_full = mapa_shared(smem_u32(queue.full), 1);
   const uint32_t odd_data = mapa_shared(smem_u32(queue.data), 1);
   uint32_t i = 0;
@@ -86,9 +92,9 @@ __device__ __forceinline__ void pair_schedule(const PairQueue& queue, volatile i
   // largest group has more than twice the chunks of the smallest.
   bool mix = false;
   if (num_units > 0) {
-    const int gl = __ldg(order), gs = __ldg(order + G - 1);
-    const int cl = (__ldg(offsets + gl + 1) - __ldg(offsets + gl) + kChunk - 1) / kChunk;
-    const int cs = (__ldg(offsets + gs + 1) - __ldg(offsets + gs) + kChunk - 1) / kChunk;
+    const int gl = ld(order), gs = ld(order + G - 1);
+    const int cl = (ld(offsets + gl + 1) - ld(offsets + gl) + kChunk - 1) / kChunk;
+    const int cs = (ld(offsets + gs + 1) - ld(offsets + gs) + kChunk - 1) / kChunk;
     mix = cl > 2 * cs;
   }
   auto unit_of = [&](int q) { return (mix && (q & 1)) ? num_units - 1 - (q >> 1) : (mix ? (q >> 1) : q); };
@@ -122,11 +128,11 @@ __device__ __forceinline__ void pair_schedule(const PairQueue& queue, volatile i
 #pragma unroll
     for (int j = 0; j < kMaxBatch; ++j) u[j] = j < cnt ? unit_of(k0 + j) : 0;
 #pragma unroll
-    for (int j = 0; j < kMaxBatch; ++j) g[j] = j < cnt ? __ldg(order + u[j] / per_group) : 0;
+    for (int j = 0; j < kMaxBatch; ++j) g[j] = j < cnt ? ld(order + u[j] / per_group) : 0;
 #pragma unroll
     for (int j = 0; j < kMaxBatch; ++j) {
-      r0[j] = j < cnt ? __ldg(offsets + g[j]) : 0;
-      r1[j] = j < cnt ? __ldg(offsets + g[j] + 1) : 0;
+      r0[j] = j < cnt ? ld(offsets + g[j]) : 0;
+      r1[j] = j < cnt ? ld(offsets + g[j] + 1) : 0;
       if (splits > 1) {
         const int part = ((r1[j] - r0[j] + kChunk - 1) / kChunk + splits - 1) / splits * kChunk;
         r0[j] = min(r1[j], r0[j] + part * (u[j] % per_group % splits));

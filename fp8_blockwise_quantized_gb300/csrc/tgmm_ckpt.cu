@@ -33,8 +33,10 @@
 // same bits every time) and rounds once.
 #include "common.cuh"
 #include "kernels.cuh"
+#include "metadata.cuh"
 #include "pairqueue.cuh"
 #include "ptx.cuh"
+#include "unitqueue.cuh"
 
 namespace gmm {
 
@@ -58,7 +60,8 @@ constexpr int kSlotBytes = 3 * kBoxBytes;    // codes, two boxes of dy
 constexpr int kOperBytes = 2 * kBoxBytes;    // 64 rows x 128 bf16
 constexpr int kStagingBytes = kEpiWarps * 4096;
 constexpr int kBarBytes = 1024;
-constexpr int kSmemBytes = 1024 + kRing * kSlotBytes + kOper * kOperBytes + kStagingBytes + kBarBytes;
+constexpr int kGroupBytes = 4 * (2 * kScanGroups + 4);  // offsets and order of a call that scans its sizes
+constexpr int kSmemBytes = 1024 + kRing * kSlotBytes + kOper * kOperBytes + kStagingBytes + kBarBytes + kGroupBytes;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 static_assert(16 * kQueue + 8 * (2 * kRing + kOper + 5 + 2 * kQueue) + 16 <= kBarBytes, "barrier area");
 
@@ -135,8 +138,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int KT = (args.K + 255) / 256, NT = (args.N + BN - 1) / BN;
   const int splits = SPLIT ? args.splits : 1;
   const int per_group = KT * NT * splits;
-  const int num_units = args.meta[kWsValid] != 0 ? args.G * per_group : 0;
-  const int* offsets = args.meta + kWsOffsets;
+  // group offsets and size order: from the workspace, or of group_sizes in
+  // shared memory (the scheduler's CTA alone needs them)
+  int* shared_offsets = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(qdata) + kBarBytes);
+  int* shared_order = shared_offsets + kScanGroups + 1;
+  bool valid;
+  if (args.sizes) {
+    valid = leader && share_group_order(args.sizes, args.G, args.M, shared_offsets, shared_order,
+                                        reinterpret_cast<unsigned long long*>(staging), shared_order + kScanGroups,
+                                        [] { __syncthreads(); });
+  } else {
+    valid = args.meta[kWsValid] != 0;
+  }
+  const int num_units = valid ? args.G * per_group : 0;
   const uint64_t lim = args.wait_limit_ns;
   const PairQueue queue{qfull, qempty, qdata, mapa_shared(smem_u32(qempty), 0), leader};
 
@@ -222,6 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 2 + kEpiWarps) {
+    grouped_rows(args, static_cast<int>(threadIdx.x) - 64, staging);
     const int pw = warp - 2;
     const int half = pw >> 2;
     const int quad = warp & 3;
@@ -301,9 +316,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) bulk_wait_all();
   } else if (warp == kSchedWarp) {
-    if (leader && lane == 0)
-      pair_schedule(queue, taken, ctaken, const_cast<int32_t*>(args.meta) + kWsClaimed, args.order, offsets, args.G,
-                    per_group, num_units, 3, 4, abort_word, lim, splits);
+    if (leader && lane == 0) {
+      int* claimed = const_cast<int32_t*>(args.meta) + kWsClaimed;
+      if (args.sizes)
+        pair_schedule(queue, taken, ctaken, claimed, shared_order, shared_offsets, args.G, per_group, num_units, 3, 4,
+                      abort_word, lim, splits, [](const int* p) { return *p; });
+      else
+        pair_schedule(queue, taken, ctaken, claimed, args.order, args.meta + kWsOffsets, args.G, per_group, num_units,
+                      3, 4, abort_word, lim, splits);
+    }
   } else if (warp >= kExpandWarp0) {
     // thread: row `row` of the chunk, 64 of its 128 codes (half `hb`)
     const int et = static_cast<int>(threadIdx.x) - 32 * kExpandWarp0;

@@ -324,7 +324,13 @@ def test_metadata_left_for_later_calls(G):
     a = gmm.mx4_fwd(*mx, st, fuse=True, workspace=want)
     b = gmm.mx4_fwd(*mx, None, fuse=True, workspace=got)
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
-    assert want.status() == got.status() == 0
+    xq, xs = gmm.quantize_lhs(x)
+    fresh = gmm.Workspace(G, M)
+    dw = gmm.tgmm_ckpt(xq, xs, gu, st, workspace=fresh)
+    assert fresh.header() == want.header() and fresh.order() == want.order()
+    dw2 = gmm.tgmm_ckpt(xq, xs, gu, None, workspace=got)
+    assert torch.equal(dw.view(torch.int16), dw2.view(torch.int16))
+    assert want.status() == got.status() == fresh.status() == 0
 
 
 def normal_bits(t):
