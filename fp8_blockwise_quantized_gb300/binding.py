@@ -552,6 +552,24 @@ def group_metadata(group_sizes, M, workspace=None, stream=None) -> Workspace:
     return ws_
 
 
+def _need(what, t, dtype, *shape):
+    """Refuses what the kernels would read or write wrongly: they take dense
+    CUDA buffers and know neither strides nor types.  One number stands for the
+    elements of a layout that has no shape of its own (MXFP4 scale blocks)."""
+    if len(shape) == 1:
+        same = t.numel() == shape[0]
+    else:
+        same = t.shape == shape
+    if t.dtype is not dtype or not same or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor of {'x'.join(map(str, shape))} {dtype} elements, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _need_sizes(group_sizes, G):
+    if group_sizes is not None:
+        _need("group_sizes", group_sizes, torch.int32, G)
+
+
 def _new2(a, b, dtype, device):
     """torch.empty((a, b)) by way of empty_strided, which takes half the host time."""
     return torch.empty_strided((a, b), (b, 1), dtype=dtype, device=device)
@@ -559,6 +577,19 @@ def _new2(a, b, dtype, device):
 
 def _new3(a, b, c, dtype, device):
     return torch.empty_strided((a, b, c), (b * c, c, 1), dtype=dtype, device=device)
+
+
+def _need_kept(kept, M, N, keep=None):
+    """Checks kept gate | up values (of the form `keep`, if given); returns (gu, guq, gus)."""
+    if isinstance(kept, (tuple, list)) and keep != "bf16":
+        guq, gus = kept
+        _need("kept codes", guq, torch.uint8, M, 2 * N)
+        _need("kept scales", gus, torch.float32, 2 * N // 128, M)
+        return None, guq, gus
+    if keep == "e4m3" or not isinstance(kept, torch.Tensor):
+        raise ValueError("kept: expected the gate | up values in bf16, or their (codes, scales)")
+    _need("kept", kept, torch.bfloat16, M, 2 * N)
+    return kept, None, None
 
 
 def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=None):
@@ -573,8 +604,13 @@ def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=
     G, K2, Nw = w.shape
     assert K2 == K and Nw % 2 == 0
     N = Nw // 2
+    _need("x", x, torch.bfloat16, M, K)
+    _need("w", w, torch.bfloat16, G, K, Nw)
+    _need_sizes(group_sizes, G)
     if out is not None:
         h, kept = out
+        _need("out h", h, torch.bfloat16, M, N)
+        _need_kept(kept, M, N, keep)
     else:
         h = _new2(M, N, torch.bfloat16, x.device)
         if keep == "bf16":
@@ -596,10 +632,15 @@ def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=No
     M, K = dy.shape
     G, N, K2 = w2.shape
     assert K2 == K
-    gu, guq, gus = (None, *kept) if isinstance(kept, (tuple, list)) else (kept, None, None)
-    assert tuple((guq if gu is None else gu).shape) == (M, 2 * N)
+    _need("dy", dy, torch.bfloat16, M, K)
+    _need("w2", w2, torch.bfloat16, G, N, K)
+    _need_sizes(group_sizes, G)
+    gu, guq, gus = _need_kept(kept, M, N)
     if out is not None:
         dgu, h = out
+        _need("out dgu", dgu, torch.bfloat16, M, 2 * N)
+        if h is not None:
+            _need("out h", h, torch.bfloat16, M, N)
     else:
         dgu = _new2(M, 2 * N, torch.bfloat16, dy.device)
         h = _new2(M, N, torch.bfloat16, dy.device) if with_h else None
@@ -615,7 +656,10 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     The scratch that few tiles with many rows need is allocated with torch."""
     M, K = xq.shape
     M2, N = dy.shape
-    assert M2 == M and tuple(xs.shape) == (K // 128, M)
+    assert M2 == M
+    _need("xq", xq, torch.uint8, M, K)
+    _need("xs", xs, torch.float32, K // 128, M)
+    _need("dy", dy, torch.bfloat16, M, N)
     if group_sizes is not None:
         G = group_sizes.numel()
     elif dw is not None:
@@ -624,7 +668,10 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
         G = workspace.G
     else:
         raise ValueError("group_sizes=None reuses the metadata in `workspace`: pass that workspace")
-    if dw is None:
+    _need_sizes(group_sizes, G)
+    if dw is not None:
+        _need("dw", dw, torch.bfloat16, G, K, N)
+    else:
         dw = _new3(G, K, N, torch.bfloat16, dy.device)
     ws_ = _ws_for(group_sizes, workspace, G, M, dy.device)
     nbytes = tgmm_fp8_ckpt_scratch_bytes(G, M, K, N)
@@ -642,8 +689,11 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
 def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
     """x bf16 [M, K] -> (xq uint8 [M, K/2] packed E2M1 codes, xs uint8 [K/128, M, 4] E8M0 scales)."""
     M, K = x.shape
+    _need("x", x, torch.bfloat16, M, K)
     if out is not None:
         xq, xs = out
+        _need("out codes", xq, torch.uint8, M, K // 2)
+        _need("out scales", xs, torch.uint8, M * K // 32)
     else:
         xq = _new2(M, K // 2, torch.uint8, x.device)
         xs = _new3(K // 128, M, 4, torch.uint8, x.device)
@@ -654,10 +704,19 @@ def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
 def mx4_quantize_rhs(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq uint8 [G, N, K/2] packed E2M1 codes, ws uint8 [G, N/128, K/128, 512] E8M0 scales)."""
     G, K, N = w.shape
+    _need("w", w, torch.bfloat16, G, K, N)
     wq = _new3(G, N, K // 2, torch.uint8, w.device)
     ws = torch.empty((G, N // 128, K // 128, 512), dtype=torch.uint8, device=w.device)
     _check(gmm_mx4_quantize_rhs(w, G, K, N, wq, ws, stream), "gmm_mx4_quantize_rhs")
     return wq, ws
+
+
+def _need_mx4(xq, xs, wq, ws, group_sizes, M, K2, G, Nw):
+    _need("xq", xq, torch.uint8, M, K2)
+    _need("xs", xs, torch.uint8, M * K2 // 16)
+    _need("wq", wq, torch.uint8, G, Nw, K2)
+    _need("ws", ws, torch.uint8, G * Nw * K2 // 16)
+    _need_sizes(group_sizes, G)
 
 
 def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, stream=None):
@@ -666,7 +725,10 @@ def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, s
     G, Nw, K3 = wq.shape
     assert K3 == K2
     N = Nw // 2 if fuse else Nw
-    if out is None:
+    _need_mx4(xq, xs, wq, ws, group_sizes, M, K2, G, Nw)
+    if out is not None:
+        _need("out", out, torch.bfloat16, M, N)
+    else:
         out = _new2(M, N, torch.bfloat16, xq.device)
     ws_ = _ws_for(group_sizes, workspace, G, M, xq.device)
     _check(gmm_mx4_fwd(xq, xs, wq, ws, group_sizes, G, M, 2 * K2, N, fuse, out, ws_.buf, ws_.nbytes, stream),
@@ -681,8 +743,13 @@ def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
     G, Nw, K3 = wq.shape
     assert K3 == K2
     N = Nw // 2
+    _need_mx4(xq, xs, wq, ws, group_sizes, M, K2, G, Nw)
     if out is not None:
         h, hq, hs = out
+        if h is not None:
+            _need("out h", h, torch.bfloat16, M, N)
+        _need("out hq", hq, torch.uint8, M, N // 2)
+        _need("out hs", hs, torch.uint8, M * N // 32)
     else:
         h = _new2(M, N, torch.bfloat16, xq.device) if with_h else None
         hq = _new2(M, N // 2, torch.uint8, xq.device)

@@ -124,3 +124,32 @@ def test_reference_gradient_by_differences():
             e[m, j] = 1e-6
             assert abs((loss(gu + e) - loss(gu - e)) / 2e-6 - dgu[m, j]) < 1e-7 * (1 + abs(dgu[m, j]) * 100)
     assert np.allclose(h, R.silu(gu[:, :N]) * gu[:, N:])
+
+
+def test_python_entry_points_refuse_what_kernels_cannot_take():
+    """Tensors on the host, of another type, size or stride are refused before anything reads them."""
+    import torch
+    import fp8_blockwise_quantized_gb300 as g
+    bf, u8 = torch.bfloat16, torch.uint8
+    x, w, w2 = torch.zeros(4, 128, dtype=bf), torch.zeros(2, 128, 256, dtype=bf), torch.zeros(2, 128, 128, dtype=bf)
+    xq, xs = torch.zeros(4, 128, dtype=u8), torch.zeros(1, 4)
+    q4, s4 = torch.zeros(4, 64, dtype=u8), torch.zeros(1, 4, 4, dtype=u8)
+    wq, ws = torch.zeros(2, 128, 64, dtype=u8), torch.zeros(2, 1, 1, 512, dtype=u8)
+    for call in (lambda: g.swiglu_fwd(x, w, None), lambda: g.swiglu_bwd(x, w2, torch.zeros(4, 256, dtype=bf), None),
+                 lambda: g.tgmm_ckpt(xq, xs, x, torch.zeros(2, dtype=torch.int32)), lambda: g.mx4_quantize_lhs(x),
+                 lambda: g.mx4_quantize_rhs(w), lambda: g.mx4_fwd(q4, s4, wq, ws, None),
+                 lambda: g.mx4_fwd_swiglu_quant(q4, s4, torch.zeros(2, 256, 64, dtype=u8),
+                                                torch.zeros(2, 2, 1, 512, dtype=u8), None)):
+        with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+            call()
+
+
+def test_kept_values_of_another_form_are_refused():
+    import torch
+    from fp8_blockwise_quantized_gb300 import binding as b
+    with pytest.raises(ValueError, match="kept"):
+        b._need_kept(None, 4, 128)
+    with pytest.raises(ValueError, match="kept"):
+        b._need_kept(torch.zeros(4, 256, dtype=torch.bfloat16), 4, 128, "e4m3")
+    with pytest.raises(ValueError, match="kept"):
+        b._need_kept((torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(2, 4)), 4, 128, "bf16")

@@ -355,6 +355,24 @@ def test_invalid_sizes_are_reported():
     assert work.status() == 0
 
 
+def test_strides_types_and_sizes_are_refused():
+    x = torch.zeros((64, 256), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((2, 256, 256), dtype=torch.bfloat16, device="cuda")
+    st = torch.tensor([30, 20], dtype=torch.int32, device="cuda")
+    bad = [lambda: gmm.swiglu_fwd(x.float(), w, st), lambda: gmm.swiglu_fwd(x.t().contiguous().t(), w, st),
+           lambda: gmm.swiglu_fwd(x, w[:, :, ::2], st), lambda: gmm.swiglu_fwd(x, w, st.long()),
+           lambda: gmm.swiglu_fwd(x, w, st[:1]), lambda: gmm.swiglu_fwd(x, w, st, out=(x[:32], x)),
+           lambda: gmm.swiglu_bwd(x, w.transpose(1, 2), torch.zeros((64, 512), dtype=torch.bfloat16, device="cuda"), st),
+           lambda: gmm.swiglu_bwd(x, w, torch.zeros((64, 510), dtype=torch.bfloat16, device="cuda"), st),
+           lambda: gmm.tgmm_ckpt(x.view(torch.uint8)[:, ::2], torch.zeros((2, 64), device="cuda"), x, st),
+           lambda: gmm.tgmm_ckpt(x.view(torch.uint8)[:, :256].contiguous(), torch.zeros((2, 63), device="cuda"), x, st),
+           lambda: gmm.mx4_quantize_lhs(x[:, ::2]),
+           lambda: gmm.mx4_fwd(*gmm.mx4_quantize_lhs(x), *[t[:1] for t in gmm.mx4_quantize_rhs(w)], st)]
+    for call in bad:
+        with pytest.raises(ValueError, match="expected a contiguous CUDA tensor"):
+            call()
+
+
 def test_no_rows():
     work = gmm.Workspace(2, 0)
     sizes = torch.zeros(2, dtype=torch.int32, device="cuda")
