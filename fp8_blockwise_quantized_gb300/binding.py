@@ -4,7 +4,9 @@ Every function named like a C entry point passes its tensors' device
 pointers, the sizes and the stream straight to the library; every step of the
 computation runs in the library's CUDA kernels.  The convenience wrappers
 below (``quantize_lhs``, ``fp8_fwd``, ...) additionally allocate the outputs
-with torch, which here is only the device-memory allocator.
+with torch, which here is only the device-memory allocator.  They take a
+``stream`` (a torch stream or a raw handle; the current stream by default), on
+which they both allocate and launch.
 
 The library must have been built (``fp8_blockwise_quantized_gb300.build``);
 without it every call raises: there is no fallback.
@@ -12,6 +14,8 @@ without it every call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -338,8 +342,34 @@ def gmm_mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, G, M, K, N, h, hq, hs,
 # convenience wrappers: allocate outputs with torch, call the C entry points
 # ---------------------------------------------------------------------------
 
+def _on_stream(wrapper):
+    """Makes `stream`, when it is given, the current stream for the wrapper's
+    own allocations (outputs, scratch, a temporary workspace and its zero fill)
+    as well as for its kernels.  Memory taken from another stream's pool would
+    be ordered by nothing: its zero fill could come after the kernel, and once
+    released it could serve that other stream while the kernel still runs.  The
+    outputs belong to `stream`, as those of any torch operation on it."""
+    at = list(inspect.signature(wrapper).parameters).index("stream")
+
+    @functools.wraps(wrapper)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return wrapper(*args, **kw)
+        current = torch.cuda.current_stream()
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=current.device)
+        if stream.cuda_stream == current.cuda_stream and stream.device == current.device:
+            return wrapper(*args, **kw)
+        with torch.cuda.stream(stream):
+            return wrapper(*args, **kw)
+
+    return call
+
+
 class Workspace:
-    """A zero-initialised device workspace sized for (G, M)."""
+    """A zero-initialised device workspace sized for (G, M); the zero fill runs
+    on the current stream, so another stream that uses it waits for that one."""
 
     def __init__(self, G: int, M: int, device="cuda"):
         self.G, self.M = G, M
@@ -394,6 +424,7 @@ def _ws_for(group_sizes, ws, G, M, device):
     return _ws(ws, G, M, device)
 
 
+@_on_stream
 def quantize_lhs(x: torch.Tensor, stream=None):
     """x bf16 [M, K] -> (xq uint8 [M, K] e4m3 codes, xs float32 [K/128, M])."""
     M, K = x.shape
@@ -403,6 +434,7 @@ def quantize_lhs(x: torch.Tensor, stream=None):
     return xq, xs
 
 
+@_on_stream
 def quantize_rhs(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq uint8 [G, N, K] e4m3 codes, ws float32 [G, K/128, N/128])."""
     G, K, N = w.shape
@@ -412,6 +444,7 @@ def quantize_rhs(w: torch.Tensor, stream=None):
     return wq, ws
 
 
+@_on_stream
 def quantize_rhs_w4(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq4 uint8 [G, N, K/2] packed E2M1 codes, ws float32 [G, K/128, N/128])."""
     G, K, N = w.shape
@@ -421,6 +454,7 @@ def quantize_rhs_w4(w: torch.Tensor, stream=None):
     return wq4, ws
 
 
+@_on_stream
 def fp8_w4_fwd(xq, xs, wq4, ws, group_sizes, fuse=False, out=None, workspace=None, stream=None, config=None):
     """The FP8 forward with 4-bit weights (wq4 [G, Nw, K/2] from quantize_rhs_w4)."""
     M, K = xq.shape
@@ -435,6 +469,7 @@ def fp8_w4_fwd(xq, xs, wq4, ws, group_sizes, fuse=False, out=None, workspace=Non
     return out
 
 
+@_on_stream
 def fp8_w4_fwd_swiglu_quant(xq, xs, wq4, ws, group_sizes, with_h=True, workspace=None, stream=None, config=None,
                             out=None):
     """Fused wi with 4-bit weights: returns (h or None, hq, hs) as fp8_fwd_swiglu_quant."""
@@ -454,6 +489,7 @@ def fp8_w4_fwd_swiglu_quant(xq, xs, wq4, ws, group_sizes, with_h=True, workspace
     return h, hq, hs
 
 
+@_on_stream
 def fp8_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, stream=None, config=None):
     """config: a tile configuration (see TileConfig), or None for the defaults."""
     M, K = xq.shape
@@ -472,6 +508,7 @@ def fp8_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, s
     return out
 
 
+@_on_stream
 def fp8_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=None, stream=None, config=None,
                          out=None):
     """Fused wi: returns (h or None, hq [M, N] e4m3 codes, hs [N/128, M]).
@@ -497,6 +534,7 @@ def fp8_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
     return h, hq, hs
 
 
+@_on_stream
 def bf16_fwd(x, w, group_sizes, fuse=False, out=None, workspace=None, stream=None):
     M, K = x.shape
     G, K2, Nw = w.shape
@@ -510,6 +548,7 @@ def bf16_fwd(x, w, group_sizes, fuse=False, out=None, workspace=None, stream=Non
     return out
 
 
+@_on_stream
 def dgrad(dy, w, group_sizes, dx=None, workspace=None, stream=None):
     """dx [M, K] = dy [M, N] . w[g]^T per group, w [G, K, N]."""
     M, N = dy.shape
@@ -522,6 +561,7 @@ def dgrad(dy, w, group_sizes, dx=None, workspace=None, stream=None):
     return dx
 
 
+@_on_stream
 def tgmm(x, dy, group_sizes, dw=None, workspace=None, stream=None, config=None):
     M, K = x.shape
     M2, N = dy.shape
@@ -545,6 +585,7 @@ def tgmm(x, dy, group_sizes, dw=None, workspace=None, stream=None, config=None):
     return dw
 
 
+@_on_stream
 def group_metadata(group_sizes, M, workspace=None, stream=None) -> Workspace:
     G = group_sizes.numel()
     ws_ = _ws(workspace, G, M, group_sizes.device)
@@ -592,6 +633,7 @@ def _need_kept(kept, M, N, keep=None):
     return kept, None, None
 
 
+@_on_stream
 def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=None):
     """The gated block's forward: x bf16 [M, K], w bf16 [G, K, 2N] (gate | up)
     -> (h bf16 [M, N], kept), kept being what swiglu_bwd takes: the gate | up
@@ -624,6 +666,7 @@ def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=
     return h, kept
 
 
+@_on_stream
 def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=None, out=None):
     """Its backward pass: dy bf16 [M, K] (the gradient of y = h W2), w2 bf16
     [G, N, K], kept as swiglu_fwd returned it -> (dgu bf16 [M, 2N], the gradient
@@ -650,6 +693,7 @@ def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=No
     return dgu, h
 
 
+@_on_stream
 def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     """tgmm from the 8-bit checkpoint of x: xq uint8 [M, K] e4m3 codes, xs
     float32 [K/128, M] (quantize_lhs), dy bf16 [M, N] -> dw bf16 [G, K, N].
@@ -678,14 +722,12 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     scratch = None
     if nbytes:
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
-        if stream is not None:  # not the stream that the allocator thinks of
-            scratch.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                  else torch.cuda.ExternalStream(int(stream), device=dy.device))
     _check(tgmm_fp8_ckpt(xq, xs, dy, group_sizes, G, M, K, N, dw, scratch, nbytes, ws_.buf, ws_.nbytes, stream),
            "tgmm_fp8_ckpt")
     return dw
 
 
+@_on_stream
 def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
     """x bf16 [M, K] -> (xq uint8 [M, K/2] packed E2M1 codes, xs uint8 [K/128, M, 4] E8M0 scales)."""
     M, K = x.shape
@@ -701,6 +743,7 @@ def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
     return xq, xs
 
 
+@_on_stream
 def mx4_quantize_rhs(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq uint8 [G, N, K/2] packed E2M1 codes, ws uint8 [G, N/128, K/128, 512] E8M0 scales)."""
     G, K, N = w.shape
@@ -719,6 +762,7 @@ def _need_mx4(xq, xs, wq, ws, group_sizes, M, K2, G, Nw):
     _need_sizes(group_sizes, G)
 
 
+@_on_stream
 def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, stream=None):
     """MXFP4 x MXFP4 grouped product -> bf16 [M, N] (fuse: silu(gate) * up, wq holding gate | up)."""
     M, K2 = xq.shape
@@ -736,6 +780,7 @@ def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, s
     return out
 
 
+@_on_stream
 def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=None, stream=None, out=None):
     """Fused gate/up product: (h bf16 [M, N] or None, hq, hs), hq and hs being h in MXFP4.
     out: an (h, hq, hs) triple to write into instead of new tensors."""
