@@ -593,22 +593,37 @@ def group_metadata(group_sizes, M, workspace=None, stream=None) -> Workspace:
     return ws_
 
 
-def _need(what, t, dtype, *shape):
+def _device():
+    """Index of the current device, on which the kernels will run; None while
+    CUDA has not been used, when there are no CUDA tensors either."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else None
+
+
+def _need(what, t, on, dtype, *shape):
     """Refuses what the kernels would read or write wrongly: they take dense
-    CUDA buffers and know neither strides nor types.  One number stands for the
-    elements of a layout that has no shape of its own (MXFP4 scale blocks)."""
+    buffers of their own device (`on`) and know neither strides nor types.  One
+    number stands for the elements of a layout that has no shape of its own
+    (MXFP4 scale blocks)."""
     if len(shape) == 1:
         same = t.numel() == shape[0]
     else:
         same = t.shape == shape
-    if t.dtype is not dtype or not same or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: expected a contiguous CUDA tensor of {'x'.join(map(str, shape))} {dtype} elements, "
-                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    if t.dtype is not dtype or not same or not t.is_contiguous() or t.get_device() != on:
+        where = "" if on is None else f" on cuda:{on}"
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor of {'x'.join(map(str, shape))} {dtype} elements"
+                         f"{where}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _need_sizes(group_sizes, G):
+def _need_sizes(group_sizes, on, G):
     if group_sizes is not None:
-        _need("group_sizes", group_sizes, torch.int32, G)
+        _need("group_sizes", group_sizes, on, torch.int32, G)
+
+
+def _ws_on(on, group_sizes, ws, G, M, device):
+    """_ws_for, with a workspace given checked for its device."""
+    if ws is not None and ws.buf.get_device() != on:
+        raise ValueError(f"workspace: expected one on cuda:{on}, got one on {ws.buf.device}")
+    return _ws_for(group_sizes, ws, G, M, device)
 
 
 def _new2(a, b, dtype, device):
@@ -620,16 +635,16 @@ def _new3(a, b, c, dtype, device):
     return torch.empty_strided((a, b, c), (b * c, c, 1), dtype=dtype, device=device)
 
 
-def _need_kept(kept, M, N, keep=None):
+def _need_kept(kept, M, N, keep=None, on=None):
     """Checks kept gate | up values (of the form `keep`, if given); returns (gu, guq, gus)."""
     if isinstance(kept, (tuple, list)) and keep != "bf16":
         guq, gus = kept
-        _need("kept codes", guq, torch.uint8, M, 2 * N)
-        _need("kept scales", gus, torch.float32, 2 * N // 128, M)
+        _need("kept codes", guq, on, torch.uint8, M, 2 * N)
+        _need("kept scales", gus, on, torch.float32, 2 * N // 128, M)
         return None, guq, gus
     if keep == "e4m3" or not isinstance(kept, torch.Tensor):
         raise ValueError("kept: expected the gate | up values in bf16, or their (codes, scales)")
-    _need("kept", kept, torch.bfloat16, M, 2 * N)
+    _need("kept", kept, on, torch.bfloat16, M, 2 * N)
     return kept, None, None
 
 
@@ -646,13 +661,14 @@ def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=
     G, K2, Nw = w.shape
     assert K2 == K and Nw % 2 == 0
     N = Nw // 2
-    _need("x", x, torch.bfloat16, M, K)
-    _need("w", w, torch.bfloat16, G, K, Nw)
-    _need_sizes(group_sizes, G)
+    on = _device()
+    _need("x", x, on, torch.bfloat16, M, K)
+    _need("w", w, on, torch.bfloat16, G, K, Nw)
+    _need_sizes(group_sizes, on, G)
     if out is not None:
         h, kept = out
-        _need("out h", h, torch.bfloat16, M, N)
-        _need_kept(kept, M, N, keep)
+        _need("out h", h, on, torch.bfloat16, M, N)
+        _need_kept(kept, M, N, keep, on)
     else:
         h = _new2(M, N, torch.bfloat16, x.device)
         if keep == "bf16":
@@ -660,7 +676,7 @@ def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=
         else:
             kept = (_new2(M, Nw, torch.uint8, x.device), _new2(Nw // 128, M, torch.float32, x.device))
     gu, (guq, gus) = (kept, (None, None)) if keep == "bf16" else (None, kept)
-    ws_ = _ws_for(group_sizes, workspace, G, M, x.device)
+    ws_ = _ws_on(on, group_sizes, workspace, G, M, x.device)
     _check(gmm_bf16_swiglu_fwd(x, w, group_sizes, G, M, K, N, h, gu, guq, gus, ws_.buf, ws_.nbytes, stream),
            "gmm_bf16_swiglu_fwd")
     return h, kept
@@ -675,19 +691,20 @@ def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=No
     M, K = dy.shape
     G, N, K2 = w2.shape
     assert K2 == K
-    _need("dy", dy, torch.bfloat16, M, K)
-    _need("w2", w2, torch.bfloat16, G, N, K)
-    _need_sizes(group_sizes, G)
-    gu, guq, gus = _need_kept(kept, M, N)
+    on = _device()
+    _need("dy", dy, on, torch.bfloat16, M, K)
+    _need("w2", w2, on, torch.bfloat16, G, N, K)
+    _need_sizes(group_sizes, on, G)
+    gu, guq, gus = _need_kept(kept, M, N, on=on)
     if out is not None:
         dgu, h = out
-        _need("out dgu", dgu, torch.bfloat16, M, 2 * N)
+        _need("out dgu", dgu, on, torch.bfloat16, M, 2 * N)
         if h is not None:
-            _need("out h", h, torch.bfloat16, M, N)
+            _need("out h", h, on, torch.bfloat16, M, N)
     else:
         dgu = _new2(M, 2 * N, torch.bfloat16, dy.device)
         h = _new2(M, N, torch.bfloat16, dy.device) if with_h else None
-    ws_ = _ws_for(group_sizes, workspace, G, M, dy.device)
+    ws_ = _ws_on(on, group_sizes, workspace, G, M, dy.device)
     _check(gmm_bf16_swiglu_bwd(dy, w2, gu, guq, gus, group_sizes, G, M, K, N, dgu, h, ws_.buf, ws_.nbytes, stream),
            "gmm_bf16_swiglu_bwd")
     return dgu, h
@@ -701,9 +718,10 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     M, K = xq.shape
     M2, N = dy.shape
     assert M2 == M
-    _need("xq", xq, torch.uint8, M, K)
-    _need("xs", xs, torch.float32, K // 128, M)
-    _need("dy", dy, torch.bfloat16, M, N)
+    on = _device()
+    _need("xq", xq, on, torch.uint8, M, K)
+    _need("xs", xs, on, torch.float32, K // 128, M)
+    _need("dy", dy, on, torch.bfloat16, M, N)
     if group_sizes is not None:
         G = group_sizes.numel()
     elif dw is not None:
@@ -712,12 +730,12 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
         G = workspace.G
     else:
         raise ValueError("group_sizes=None reuses the metadata in `workspace`: pass that workspace")
-    _need_sizes(group_sizes, G)
+    _need_sizes(group_sizes, on, G)
     if dw is not None:
-        _need("dw", dw, torch.bfloat16, G, K, N)
+        _need("dw", dw, on, torch.bfloat16, G, K, N)
     else:
         dw = _new3(G, K, N, torch.bfloat16, dy.device)
-    ws_ = _ws_for(group_sizes, workspace, G, M, dy.device)
+    ws_ = _ws_on(on, group_sizes, workspace, G, M, dy.device)
     nbytes = tgmm_fp8_ckpt_scratch_bytes(G, M, K, N)
     scratch = None
     if nbytes:
@@ -731,11 +749,12 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
 def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
     """x bf16 [M, K] -> (xq uint8 [M, K/2] packed E2M1 codes, xs uint8 [K/128, M, 4] E8M0 scales)."""
     M, K = x.shape
-    _need("x", x, torch.bfloat16, M, K)
+    on = _device()
+    _need("x", x, on, torch.bfloat16, M, K)
     if out is not None:
         xq, xs = out
-        _need("out codes", xq, torch.uint8, M, K // 2)
-        _need("out scales", xs, torch.uint8, M * K // 32)
+        _need("out codes", xq, on, torch.uint8, M, K // 2)
+        _need("out scales", xs, on, torch.uint8, M * K // 32)
     else:
         xq = _new2(M, K // 2, torch.uint8, x.device)
         xs = _new3(K // 128, M, 4, torch.uint8, x.device)
@@ -747,19 +766,20 @@ def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
 def mx4_quantize_rhs(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq uint8 [G, N, K/2] packed E2M1 codes, ws uint8 [G, N/128, K/128, 512] E8M0 scales)."""
     G, K, N = w.shape
-    _need("w", w, torch.bfloat16, G, K, N)
+    on = _device()
+    _need("w", w, on, torch.bfloat16, G, K, N)
     wq = _new3(G, N, K // 2, torch.uint8, w.device)
     ws = torch.empty((G, N // 128, K // 128, 512), dtype=torch.uint8, device=w.device)
     _check(gmm_mx4_quantize_rhs(w, G, K, N, wq, ws, stream), "gmm_mx4_quantize_rhs")
     return wq, ws
 
 
-def _need_mx4(xq, xs, wq, ws, group_sizes, M, K2, G, Nw):
-    _need("xq", xq, torch.uint8, M, K2)
-    _need("xs", xs, torch.uint8, M * K2 // 16)
-    _need("wq", wq, torch.uint8, G, Nw, K2)
-    _need("ws", ws, torch.uint8, G * Nw * K2 // 16)
-    _need_sizes(group_sizes, G)
+def _need_mx4(on, xq, xs, wq, ws, group_sizes, M, K2, G, Nw):
+    _need("xq", xq, on, torch.uint8, M, K2)
+    _need("xs", xs, on, torch.uint8, M * K2 // 16)
+    _need("wq", wq, on, torch.uint8, G, Nw, K2)
+    _need("ws", ws, on, torch.uint8, G * Nw * K2 // 16)
+    _need_sizes(group_sizes, on, G)
 
 
 @_on_stream
@@ -769,12 +789,13 @@ def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, s
     G, Nw, K3 = wq.shape
     assert K3 == K2
     N = Nw // 2 if fuse else Nw
-    _need_mx4(xq, xs, wq, ws, group_sizes, M, K2, G, Nw)
+    on = _device()
+    _need_mx4(on, xq, xs, wq, ws, group_sizes, M, K2, G, Nw)
     if out is not None:
-        _need("out", out, torch.bfloat16, M, N)
+        _need("out", out, on, torch.bfloat16, M, N)
     else:
         out = _new2(M, N, torch.bfloat16, xq.device)
-    ws_ = _ws_for(group_sizes, workspace, G, M, xq.device)
+    ws_ = _ws_on(on, group_sizes, workspace, G, M, xq.device)
     _check(gmm_mx4_fwd(xq, xs, wq, ws, group_sizes, G, M, 2 * K2, N, fuse, out, ws_.buf, ws_.nbytes, stream),
            "gmm_mx4_fwd")
     return out
@@ -788,18 +809,19 @@ def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
     G, Nw, K3 = wq.shape
     assert K3 == K2
     N = Nw // 2
-    _need_mx4(xq, xs, wq, ws, group_sizes, M, K2, G, Nw)
+    on = _device()
+    _need_mx4(on, xq, xs, wq, ws, group_sizes, M, K2, G, Nw)
     if out is not None:
         h, hq, hs = out
         if h is not None:
-            _need("out h", h, torch.bfloat16, M, N)
-        _need("out hq", hq, torch.uint8, M, N // 2)
-        _need("out hs", hs, torch.uint8, M * N // 32)
+            _need("out h", h, on, torch.bfloat16, M, N)
+        _need("out hq", hq, on, torch.uint8, M, N // 2)
+        _need("out hs", hs, on, torch.uint8, M * N // 32)
     else:
         h = _new2(M, N, torch.bfloat16, xq.device) if with_h else None
         hq = _new2(M, N // 2, torch.uint8, xq.device)
         hs = _new3(N // 128, M, 4, torch.uint8, xq.device)
-    ws_ = _ws_for(group_sizes, workspace, G, M, xq.device)
+    ws_ = _ws_on(on, group_sizes, workspace, G, M, xq.device)
     _check(gmm_mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, G, M, 2 * K2, N, h, hq, hs, ws_.buf, ws_.nbytes,
                                     stream), "gmm_mx4_fwd_swiglu_quant")
     return h, hq, hs
