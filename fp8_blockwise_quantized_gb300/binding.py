@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import inspect
+import math
 import os
 
 import torch
@@ -602,8 +603,7 @@ def _device():
 def _need(what, t, on, dtype, *shape):
     """Refuses what the kernels would read or write wrongly: they take dense
     buffers of their own device (`on`) and know neither strides nor types.  One
-    number stands for the elements of a layout that has no shape of its own
-    (MXFP4 scale blocks)."""
+    number: that many elements, in any shape."""
     if len(shape) == 1:
         same = t.numel() == shape[0]
     else:
@@ -612,6 +612,14 @@ def _need(what, t, on, dtype, *shape):
         where = "" if on is None else f" on cuda:{on}"
         raise ValueError(f"{what}: expected a contiguous CUDA tensor of {'x'.join(map(str, shape))} {dtype} elements"
                          f"{where}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _need_scales(what, t, on, *shape):
+    """MXFP4 scale bytes in the kernels' order: of this shape, or flat."""
+    if t.dim() == 1:
+        _need(what, t, on, torch.uint8, math.prod(shape))
+    else:
+        _need(what, t, on, torch.uint8, *shape)
 
 
 def _need_sizes(group_sizes, on, G):
@@ -754,7 +762,7 @@ def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
     if out is not None:
         xq, xs = out
         _need("out codes", xq, on, torch.uint8, M, K // 2)
-        _need("out scales", xs, on, torch.uint8, M * K // 32)
+        _need_scales("out scales", xs, on, K // 128, M, 4)
     else:
         xq = _new2(M, K // 2, torch.uint8, x.device)
         xs = _new3(K // 128, M, 4, torch.uint8, x.device)
@@ -776,9 +784,9 @@ def mx4_quantize_rhs(w: torch.Tensor, stream=None):
 
 def _need_mx4(on, xq, xs, wq, ws, group_sizes, M, K2, G, Nw):
     _need("xq", xq, on, torch.uint8, M, K2)
-    _need("xs", xs, on, torch.uint8, M * K2 // 16)
+    _need_scales("xs", xs, on, K2 // 64, M, 4)
     _need("wq", wq, on, torch.uint8, G, Nw, K2)
-    _need("ws", ws, on, torch.uint8, G * Nw * K2 // 16)
+    _need_scales("ws", ws, on, G, Nw // 128, K2 // 64, 512)
     _need_sizes(group_sizes, on, G)
 
 
@@ -816,7 +824,7 @@ def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
         if h is not None:
             _need("out h", h, on, torch.bfloat16, M, N)
         _need("out hq", hq, on, torch.uint8, M, N // 2)
-        _need("out hs", hs, on, torch.uint8, M * N // 32)
+        _need_scales("out hs", hs, on, N // 128, M, 4)
     else:
         h = _new2(M, N, torch.bfloat16, xq.device) if with_h else None
         hq = _new2(M, N // 2, torch.uint8, xq.device)
