@@ -19,8 +19,8 @@ constexpr int kWsStatus = 0;
 constexpr int kWsValid = 1;
 constexpr int kWsS = 2;
 constexpr int kWsNumTiles = 3;
-// Work counters of the CTA-pair tgmm kernel: units claimed, and CTAs that have
-// finished (the last one resets both to zero for the next launch).
+// Work counters of every kernel that claims its units: units claimed, and CTAs
+// that have finished (the last one resets both to zero for the next launch).
 constexpr int kWsClaimed = 4;
 constexpr int kWsFinished = 5;
 // Number of 256-row tiles (the CTA-pair FP8 kernel's row tiles).

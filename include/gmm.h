@@ -71,7 +71,8 @@ const char* gmm_last_cuda_error(void);
  * Bytes of device workspace the grouped calls need for G groups and M rows:
  * a status word, the group offsets, the row-tile list and the groups ordered
  * by size.  The workspace must be zero-filled once before its first use (its
- * first word is the sticky error word); afterwards it may be reused by any number of calls issued on
+ * first word is the sticky error word, and two others are work counters that
+ * start from 0); afterwards it may be reused by any number of calls issued on
  * one stream.  Two calls that run concurrently need two workspaces.
  */
 size_t gmm_workspace_bytes(int G, int64_t M);
@@ -87,10 +88,11 @@ size_t gmm_workspace_bytes(int G, int64_t M);
  *   int32 word[2]  S = sum(group_sizes)        (M when invalid)
  *   int32 word[3]  T = number of row tiles      (0 when invalid)
  *   int32 word[4], word[5]  set to 0: the work counters of the kernels that
- *                  claim their units (units claimed, CTAs finished: tgmm, the
+ *                  claim their units (units claimed, CTAs finished: tgmm_*, the
  *                  FP8 forward with one CTA per tile, gmm_bf16_swiglu_* and
  *                  gmm_mx4_*); each such launch claims its units from them and
- *                  its last CTA sets them back to 0
+ *                  its last CTA sets them back to 0.  They have to be 0 when it
+ *                  starts: nonzero counters make it skip units without an error.
  *   int32 word[6]  T2 = number of 256-row tiles (0 when invalid)
  *   int32 word[8 + g], g = 0..G  exclusive prefix sums off_g (off_G = S)
  *   int32x4 tiles[T] at byte offset gmm_tiles_offset(G): {g, row0, row1, 0},
@@ -104,7 +106,11 @@ size_t gmm_workspace_bytes(int G, int64_t M);
  *                  rows, the row tiles of the CTA-pair FP8 kernel.
  * The grouped calls below run this step themselves unless they are given
  * group_sizes = NULL, in which case they read what this call (or an earlier
- * grouped call) left in the workspace.
+ * grouped call) left in the workspace.  gmm_bf16_swiglu_*, tgmm_fp8_ckpt and
+ * gmm_mx4_* with at most 256 groups (and M > 0) do it inside their kernel, and
+ * leave all of the above but words 4 and 5: those they only use.  A workspace
+ * whose counters were overwritten is put right by zero-filling it or by
+ * gmm_group_metadata.
  */
 gmm_status gmm_group_metadata(const int32_t* group_sizes, int G, int64_t M, void* workspace,
                               size_t workspace_bytes, void* stream);
