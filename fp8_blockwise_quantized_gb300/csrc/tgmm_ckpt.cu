@@ -7,8 +7,9 @@
 // scale runs along the reduction (one per row and 128 columns), so it cannot
 // be applied to the sums: the codes are expanded to bf16, scaled, on their way
 // from shared memory to shared memory.  Scaling rounds each value once to bf16
-// (relative 2^-9, against the 2^-4 of the e4m3 code it expands).  In exchange
-// x is read at one byte an element.
+// (at most 2^-8 of it, against the 2^-4 of the e4m3 code it expands; the result
+// is 0.0018 off in norm, 0.0017 of which its own rounding to bf16 makes).  In
+// exchange x is read at one byte an element.
 //
 // A cluster of two CTAs on the two SMs of a pair owns the tile (g, 256 rows of
 // K, 256 columns of N) and walks the group's rows in chunks of 64; each CTA
