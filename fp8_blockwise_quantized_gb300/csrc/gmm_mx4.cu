@@ -157,19 +157,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kEpiWarp0) regs_dec<kControlRegs>();
   if (warp == 0) {
     if (lane == 0) {
-      // One K step's boxes: past K (an odd number of 128-wide blocks) the copies
-      // bring zeros.
-      const auto boxes = [&](const int4& u, int ks, auto&& box) {
-        const int brow = u.x * Nw + u.w * kOutCols;
-        box(&map_a, 0, ks * 128, u.y);
-        box(&map_b, C::kABytes, ks * 128, brow);
-        if (FUSE) box(&map_b, C::kABytes + C::kBBytes / 2, ks * 128, brow + args.N);
-      };
       RingPos<kStages> r;
       uint32_t c = 0;
       bool ok = true;
       int4 e;
       for (uint32_t i = 0; ok && queue.get(i, e, false, 0, abort_word, lim) && e.x >= 0; ++i) {
+        const int brow = e.x * Nw + e.w * kOutCols;
         for (int ks = 0; ks < KS; ++ks) {
           if (!mbar_wait(&empty[r.slot], r.phase ^ 1u, abort_word, lim)) {
             ok = false;
@@ -178,7 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* dst = ring + r.slot * C::kStageBytes;
           uint64_t* bar = &full[r.slot];
           mbar_arrive_expect_tx(bar, C::kStageBytes);
-          boxes(e, ks, [&](const CUtensorMap* map, int at, int x, int y) { tma_load_2d(dst + at, map, bar, x, y); });
+          // past K (an odd number of 128-wide blocks) the copies bring zeros
+          tma_load_2d(dst, &map_a, bar, ks * 128, e.y);
+          tma_load_2d(dst + C::kABytes, &map_b, bar, ks * 128, brow);
+          if (FUSE) tma_load_2d(dst + C::kABytes + C::kBBytes / 2, &map_b, bar, ks * 128, brow + args.N);
           r.advance();
           ++c;
         }
