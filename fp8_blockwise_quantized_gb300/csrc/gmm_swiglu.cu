@@ -16,13 +16,16 @@
 //   warp 1      TMEM, tcgen05.mma kind::f16 M=128 K=16, two accumulators, so that
 //               one unit's epilogue overlaps the next unit's products
 //   warp 2      claims the CTA's units and queues them for the other roles
-//   warps 4-11  epilogue: one thread per row and column half
+//   warps 4-11  epilogue: one thread per row and column half.  The forward's
+//               adds up sums over 512 of K in registers; where gate | up are
+//               kept in e4m3, the two threads of a row exchange their halves'
+//               largest values
 // Rows of a tile past its group's end belong to the next group: they are
 // multiplied with the wrong weight and never stored.
 //
 // Both are bound by memory at the production shape (256 experts, 65536 rows, K
-// 2048, N 512, Zipf routing; cold L2).  Forward, e4m3 kept: 289 us, 5.0 TB/s of
-// algorithmic bytes, 0.95 PFLOP/s, bound by the operands that reach the SMs (4.0
+// 2048, N 512, Zipf routing; cold L2).  Forward, e4m3 kept: 291 us, 5.0 TB/s of
+// algorithmic bytes, 0.94 PFLOP/s (bf16 kept 295), bound by the operands that reach the SMs (4.0
 // GB through L2, 1.3 GB of them from HBM): its loads alone take 237, its products
 // alone 162.  Backward, bf16 kept: 206 us, 5.5 TB/s, bound by HBM (without its
 // epilogue 161).  256 weight columns a unit, because every unit reads its 128
@@ -59,7 +62,16 @@ constexpr int kStagingBytes = kEpiWarps * 4096;
 constexpr int kBarBytes = 512;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kBarBytes;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-static_assert(8 * (2 * kStages + 5 + ClaimQueue::kBarriers) + 16 + 16 * kClaimSlots <= kBarBytes, "barrier area");
+static_assert(8 * (2 * kStages + 5 + ClaimQueue::kBarriers + kEpiWarps / 2) + 16 + 16 * kClaimSlots <= kBarBytes,
+              "barrier area");
+// K steps of the forward whose products the tensor core adds up by itself (512
+// of K); the epilogue adds these sums in fp32 registers.  The tensor core's adder
+// truncates, and a sum of 128 of its steps (K 2048) came out 2.3e-6 low, one of
+// 256 (K 4096) twice that, where fp32 products with rounding are 0.6e-6 and
+// 0.9e-6 off: the scales of the 8-bit checkpoint show it.  With 512 of K a sum
+// they are 0.55e-6 off for any K.  It costs 1 % (65536 rows, K 2048: 294 us, 291
+// with one sum for all of K).  The backward's results are all bf16.
+constexpr int kSumSteps = 8;
 
 // The work units.  A wide unit is 128 rows x 256 weight columns (forward: 128
 // gate and 128 up columns; backward: 256 columns of dh), a narrow one half of
@@ -139,7 +151,7 @@ __device__ __forceinline__ void zero_span(void* p, long long bytes, int tid) {
 using Box64 = RowBox<64>;  // 32 rows x 32 bf16, or 64 codes
 using Box32 = RowBox<32>;  // 32 rows x 32 codes
 
-__device__ __forceinline__ void put32(uint8_t* box, int lane, const float (&v)[32]) {
+__device__ __forceinline__ void put32(uint8_t* box, int lane, const float* v) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     Box64::put(box, lane, j,
@@ -147,84 +159,138 @@ __device__ __forceinline__ void put32(uint8_t* box, int lane, const float (&v)[3
                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
 }
 
-// Forward: half of the unit's `cols` (64 or 128) columns of h and of the bf16
-// gate | up, or all 128 codes of gate (half 0) or up (half 1).  The accumulators
-// hold gate in columns [0, cols), up in [cols, 2 cols).
-template <bool E4M3>
-__device__ __forceinline__ void fwd_rows(const SwigluArgs& args, uint8_t* stage, uint32_t t, int half, int lane,
-                                         long long row0, int rows, int n0, int cols) {
-  const long long N = args.N, ldh = 2 * N, ldg = 4 * N;
+// Forward: the sums of one thread's row, half of the unit's gate columns (from
+// column half * cols / 2 on) and the same half of its up columns, 32 or 64 each.
+struct FwdSums {
+  float a[64], b[64];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) a[i] = b[i] = 0.0f;
+  }
+  // adds the chunk's accumulators: gate in columns [0, cols), up in [cols, 2 cols)
+  __device__ __forceinline__ void add(uint32_t t, int half, int cols) {
+    const uint32_t ta = t + half * (cols / 2), tb = ta + cols;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (p == 1 && cols < 128) break;
+      uint32_t r[32];
+      tmem_ld_32x32(ta + 32 * p, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) a[32 * p + i] += __uint_as_float(r[i]);
+      tmem_ld_32x32(tb + 32 * p, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) b[32 * p + i] += __uint_as_float(r[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ float absmax64(const float (&v)[64]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+
+// This lane's 64 sums as e4m3 codes (rounded once, from the fp32 sums) to `g`.
+__device__ __forceinline__ void store_codes64(uint8_t* box, uint8_t* g, long long ld, int rows, int lane,
+                                              const float (&v)[64], float inv) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = 16 * j + 4 * k;
+      q[k] = e4m3x2(__fmul_rn(v[c], inv), __fmul_rn(v[c + 1], inv)) |
+             (e4m3x2(__fmul_rn(v[c + 2], inv), __fmul_rn(v[c + 3], inv)) << 16);
+    }
+    Box64::put(box, lane, j, make_uint4(q[0], q[1], q[2], q[3]));
+  }
+  __syncwarp();
+  Box64::store(box, g, ld, rows, lane);
+  __syncwarp();
+}
+
+// The two warps that hold the halves of 32 rows exchange the halves' largest
+// values: mine and the other's (two slots each, by the unit's parity) and a
+// barrier at which both arrive.  Neither can arrive for the next unit before the
+// other has, which it does after reading this unit's slot: so the barrier is at
+// most one phase ahead of a waiting warp, and a slot written again two units
+// later has been read.
+struct HalfMax {
+  float2 *mine, *other;
+  uint64_t* both;
+  __device__ __forceinline__ void say(uint32_t unit, int lane, float a, float b) const {
+    mine[32 * (unit & 1u) + lane] = make_float2(a, b);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(both);
+  }
+  __device__ __forceinline__ bool hear(uint32_t unit, int lane, float& a, float& b, volatile int* abort_word,
+                                       uint64_t lim) const {
+    if (!__all_sync(0xffffffffu, mbar_wait(both, unit & 1u, abort_word, lim))) return false;
+    const float2 v = other[32 * (unit & 1u) + lane];
+    __syncwarp();
+    a = fmaxf(a, v.x);
+    b = fmaxf(b, v.y);
+    return true;
+  }
+};
+
+// Forward, gate | up kept in bf16: half of the unit's `cols` (64 or 128) columns.
+__device__ __forceinline__ void fwd_rows_bf16(const SwigluArgs& args, uint8_t* stage, const FwdSums& s, int half,
+                                              int lane, long long row0, int rows, int n0, int cols) {
+  const long long N = args.N;
   uint8_t* box0 = stage;
   uint8_t* box1 = stage + Box64::kBytes;
-#pragma unroll 1
-  for (int c0 = half * cols / 2; c0 < (half + 1) * cols / 2; c0 += 32) {
-    uint32_t ra[32], rb[32];
-    tmem_ld_32x32(t + c0, ra);
-    tmem_ld_32x32(t + cols + c0, rb);
-    tmem_ld_wait();
-    const int col = n0 + c0;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if (p == 1 && cols < 128) break;
+    const int col = n0 + half * (cols / 2) + 32 * p;
+    put32(box0, lane, s.a + 32 * p);
+    put32(box1, lane, s.b + 32 * p);
+    __syncwarp();
+    uint8_t* g = reinterpret_cast<uint8_t*>(args.gu + row0 * 2 * N + col);
+    Box64::store(box0, g, 4 * N, rows, lane);
+    Box64::store(box1, g + 2 * N, 4 * N, rows, lane);
+    __syncwarp();
     float v[32];
-    if (!E4M3) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ra[i]);
-      put32(box0, lane, v);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(rb[i]);
-      put32(box1, lane, v);
-      __syncwarp();
-      uint8_t* g = reinterpret_cast<uint8_t*>(args.gu + row0 * 2 * N + col);
-      Box64::store(box0, g, ldg, rows, lane);
-      Box64::store(box1, g + 2 * N, ldg, rows, lane);
-      __syncwarp();
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = silu_f32(__uint_as_float(ra[i])) * __uint_as_float(rb[i]);
+    for (int i = 0; i < 32; ++i) v[i] = silu_f32(s.a[32 * p + i]) * s.b[32 * p + i];
     put32(box0, lane, v);
     __syncwarp();
-    Box64::store(box0, reinterpret_cast<uint8_t*>(args.h + row0 * N + col), ldh, rows, lane);
+    Box64::store(box0, reinterpret_cast<uint8_t*>(args.h + row0 * N + col), 2 * N, rows, lane);
     __syncwarp();
   }
-  if (E4M3) {
-    // absmax of the row's block, then its codes (rounded once, from the fp32 sums)
-    const uint32_t tb = t + half * 128;
-    float amax = 0.0f;
-#pragma unroll 1
-    for (int cc = 0; cc < 4; ++cc) {
-      uint32_t r[32];
-      tmem_ld_32x32(tb + 32 * cc, r);
-      tmem_ld_wait();
+}
+
+// Forward, gate | up kept in e4m3: 64 of the block's 128 columns, unit number
+// `unit` of this warp that has rows.  False: a wait ran out.
+__device__ __forceinline__ bool fwd_rows_e4m3(const SwigluArgs& args, uint8_t* stage, const HalfMax& halves,
+                                              const FwdSums& s, int half, int lane, long long row0, int rows, int n0,
+                                              uint32_t unit, volatile int* abort_word, uint64_t lim) {
+  const long long N = args.N;
+  float amax = absmax64(s.a), bmax = absmax64(s.b);
+  halves.say(unit, lane, amax, bmax);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(__uint_as_float(r[i])));
-    }
-    float s, inv;
-    e4m3_block_scale(amax, s, inv);
-    const long long block = half * (N / 128) + n0 / 128;
-    if (lane < rows) args.gus[block * args.M + row0 + lane] = s;
-    uint8_t* g = args.guq + row0 * 2 * N + block * 128;
-#pragma unroll 1
-    for (int cc = 0; cc < 4; ++cc) {
-      uint32_t r[32];
-      tmem_ld_32x32(tb + 32 * cc, r);
-      tmem_ld_wait();
-      // 64 codes fill a box
+  for (int p = 0; p < 2; ++p) {
+    float v[32];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t q[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int c = 16 * j + 4 * k;
-          q[k] = e4m3x2(__fmul_rn(__uint_as_float(r[c]), inv), __fmul_rn(__uint_as_float(r[c + 1]), inv)) |
-                 (e4m3x2(__fmul_rn(__uint_as_float(r[c + 2]), inv), __fmul_rn(__uint_as_float(r[c + 3]), inv)) << 16);
-        }
-        Box64::put(box0, lane, 2 * (cc & 1) + j, make_uint4(q[0], q[1], q[2], q[3]));
-      }
-      if (cc & 1) {
-        __syncwarp();
-        Box64::store(box0, g + 32 * (cc - 1), 2 * N, rows, lane);
-        __syncwarp();
-      }
-    }
+    for (int i = 0; i < 32; ++i) v[i] = silu_f32(s.a[32 * p + i]) * s.b[32 * p + i];
+    put32(stage, lane, v);
+    __syncwarp();
+    Box64::store(stage, reinterpret_cast<uint8_t*>(args.h + row0 * N + n0 + 64 * half + 32 * p), 2 * N, rows, lane);
+    __syncwarp();
   }
+  if (!halves.hear(unit, lane, amax, bmax, abort_word, lim)) return false;
+  float sa, ia, sb, ib;
+  e4m3_block_scale(amax, sa, ia);
+  e4m3_block_scale(bmax, sb, ib);
+  if (lane < rows) args.gus[(half * (N / 128) + n0 / 128) * args.M + row0 + lane] = half ? sb : sa;
+  uint8_t* g = args.guq + row0 * 2 * N + n0 + 64 * half;
+  store_codes64(stage, g, 2 * N, rows, lane, s.a, ia);
+  store_codes64(stage, g + N, 2 * N, rows, lane, s.b, ib);
+  return true;
 }
 
 // Backward: 32 columns at a time of the kept gate and up.
@@ -321,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = tempty + 2;
   uint64_t* ufull = drain + 1;
   uint64_t* uempty = ufull + kClaimSlots;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(uempty + kClaimSlots);
+  uint64_t* halves = uempty + kClaimSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(halves + kEpiWarps / 2);
   volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int4* udata = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 2) + 15) & ~uintptr_t{15});
   const ClaimQueue queue{ufull, uempty, udata};
@@ -337,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tempty[b], kEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int q = 0; q < kEpiWarps / 2; ++q) mbar_init(&halves[q], 2);
     queue.init(kQueueReaders);
     *abort_word = 0;
     fence_mbar_init();
@@ -355,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();  // inputs and metadata come from earlier kernels
 
   const int KS = args.K / 64;
+  const int chunk = FWD ? kSumSteps : KS;
   const uint64_t lim = args.wait_limit_ns;
 
   if (warp < kEpiWarp0) regs_dec<kControlRegs>();
@@ -416,29 +485,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, any = false, next_ready = false;
       int4 e;
       for (uint32_t i = 0; ok && queue.get(i, e, false, 0, abort_word, lim) && e.x >= 0; ++i) {
-        if (!mbar_wait(&tempty[acc.slot], acc.phase ^ 1u, abort_word, lim)) break;
-        tc_fence_after();
-        const uint32_t d = tbase + acc.slot * 256;
         const uint32_t idesc = (e.w & 3) == 2 ? idesc2 : idesc1;
-        for (int ks = 0; ks < KS; ++ks) {
-          if (!next_ready && !mbar_wait(&full[r.slot], r.phase, abort_word, lim)) {
+        for (int k0 = 0; ok && k0 < KS; k0 += chunk) {
+          if (!mbar_wait(&tempty[acc.slot], acc.phase ^ 1u, abort_word, lim)) {
             ok = false;
             break;
           }
-          const uint32_t a_lo = a_lo0 + r.slot * (kStageBytes >> 4);
-          const uint32_t b_lo = b_lo0 + r.slot * (kStageBytes >> 4);
-          uint64_t* freed = &empty[r.slot];
-          r.advance();
-          next_ready = mbar_test(&full[r.slot], r.phase);  // answered while the products are issued
+          tc_fence_after();
+          const uint32_t d = tbase + acc.slot * 256;
+          const int k1 = min(KS, k0 + chunk);
+          for (int ks = k0; ks < k1; ++ks) {
+            if (!next_ready && !mbar_wait(&full[r.slot], r.phase, abort_word, lim)) {
+              ok = false;
+              break;
+            }
+            const uint32_t a_lo = a_lo0 + r.slot * (kStageBytes >> 4);
+            const uint32_t b_lo = b_lo0 + r.slot * (kStageBytes >> 4);
+            uint64_t* freed = &empty[r.slot];
+            r.advance();
+            next_ready = mbar_test(&full[r.slot], r.phase);  // answered while the products are issued
 #pragma unroll
-          for (uint32_t j = 0; j < 4; ++j)
-            mma_bf16(d, desc_sw128(a_lo + 2 * j), desc_sw128(b_lo + kBStep * j), idesc, (ks > 0 || j > 0) ? 1u : 0u);
-          mma_commit(freed);
-          any = true;
+            for (uint32_t j = 0; j < 4; ++j)
+              mma_bf16(d, desc_sw128(a_lo + 2 * j), desc_sw128(b_lo + kBStep * j), idesc, (ks > k0 || j > 0) ? 1u : 0u);
+            mma_commit(freed);
+            any = true;
+          }
+          if (!ok) break;
+          mma_commit(&tfull[acc.slot]);
+          acc.advance();
         }
-        if (!ok) break;
-        mma_commit(&tfull[acc.slot]);
-        acc.advance();
       }
       if (any) {
         volatile int no_abort = 0;
@@ -475,33 +550,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = staging + (warp - kEpiWarp0) * 4096;
     RingPos<2> acc;
     int4 e;
-    for (uint32_t i = 0; queue.get(i, e, true, lane, abort_word, lim) && e.x >= 0; ++i) {
-      const long long row0 = e.y + quad * 32;
-      const int rows = min(32, e.z - static_cast<int>(row0));  // of this warp; may be <= 0
-      const int cols = (e.w & 3) * (FWD ? 64 : 128);  // of the unit
-      const int col0 = (e.w >> 2) * (FWD ? 64 : 128) + (FWD ? 0 : half * (cols / 2));
-      Kept32<E4M3> kept;
-      float sa = 0.0f, sb = 0.0f;
-      if (!FWD) {  // read while the products run
+    bool ok = true;
+    if (FWD) {
+      const int pw = warp - kEpiWarp0, po = pw ^ 4;  // po holds the other half of these rows (pw % 4 = quad)
+      float2* maxima = reinterpret_cast<float2*>(staging + Box64::kBytes);  // the e4m3 form leaves the second box free
+      const HalfMax halves_of_rows{maxima + pw * 512, maxima + po * 512, &halves[quad]};
+      uint32_t units = 0;  // with rows, so far
+      FwdSums sums;
+      for (uint32_t i = 0; ok && queue.get(i, e, true, lane, abort_word, lim) && e.x >= 0; ++i) {
+        const long long row0 = e.y + quad * 32;
+        const int rows = min(32, e.z - static_cast<int>(row0));  // of this warp; may be <= 0
+        const int cols = (e.w & 3) * 64, n0 = (e.w >> 2) * 64;
+        sums.zero();
+        for (int k0 = 0; k0 < KS; k0 += chunk) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc.slot], acc.phase, abort_word, lim))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (rows > 0) sums.add(t_lane + acc.slot * 256, half, cols);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc.slot]);
+          acc.advance();
+        }
+        if (!ok || rows <= 0) continue;
+        if (E4M3)
+          ok = fwd_rows_e4m3(args, stage, halves_of_rows, sums, half, lane, row0, rows, n0, units++, abort_word, lim);
+        else
+          fwd_rows_bf16(args, stage, sums, half, lane, row0, rows, n0, cols);
+      }
+    } else {
+      for (uint32_t i = 0; queue.get(i, e, true, lane, abort_word, lim) && e.x >= 0; ++i) {
+        const long long row0 = e.y + quad * 32;
+        const int rows = min(32, e.z - static_cast<int>(row0));  // of this warp; may be <= 0
+        const int cols = (e.w & 3) * 64;  // of this warp
+        const int col0 = (e.w >> 2) * 128 + half * cols;
+        // read while the products run
+        Kept32<E4M3> kept;
         kept.fetch(args, row0, rows, col0, lane);
+        float sa = 0.0f, sb = 0.0f;
         if (E4M3 && lane < rows) {
           sa = args.gus[(col0 / 128) * static_cast<long long>(args.M) + row0 + lane];
           sb = args.gus[(N / 128 + col0 / 128) * args.M + row0 + lane];
         }
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc.slot], acc.phase, abort_word, lim))) break;
+        tc_fence_after();
+        if (rows > 0)
+          bwd_rows<E4M3>(args, stage, t_lane + acc.slot * 256 + half * cols, lane, row0, rows, col0, cols, kept, sa, sb);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[acc.slot]);
+        acc.advance();
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc.slot], acc.phase, abort_word, lim))) break;
-      tc_fence_after();
-      const uint32_t tb = t_lane + acc.slot * 256;
-      if (rows > 0) {
-        if (FWD)
-          fwd_rows<E4M3>(args, stage, tb, half, lane, row0, rows, col0, cols);
-        else
-          bwd_rows<E4M3>(args, stage, tb + half * (cols / 2), lane, row0, rows, col0, cols / 2, kept, sa, sb);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc.slot]);
-      acc.advance();
     }
   }
 
