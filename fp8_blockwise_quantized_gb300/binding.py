@@ -343,6 +343,14 @@ def gmm_mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, G, M, K, N, h, hq, hs,
 # convenience wrappers: allocate outputs with torch, call the C entry points
 # ---------------------------------------------------------------------------
 
+def _stream_of(handle, device):
+    """torch's stream of a raw handle.  0 and 1 (cudaStreamLegacy) are the default
+    stream, for which torch makes no external stream: of 0 it makes a new one."""
+    if handle in (0, 1):
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
 def _on_stream(wrapper):
     """Makes `stream`, when it is given, the current stream for the wrapper's
     own allocations (outputs, scratch, a temporary workspace and its zero fill)
@@ -359,7 +367,7 @@ def _on_stream(wrapper):
             return wrapper(*args, **kw)
         current = torch.cuda.current_stream()
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=current.device)
+            stream = _stream_of(int(stream), current.device)
         if stream.cuda_stream == current.cuda_stream and stream.device == current.device:
             return wrapper(*args, **kw)
         with torch.cuda.stream(stream):

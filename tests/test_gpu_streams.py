@@ -69,3 +69,19 @@ def test_a_busy_stream_that_is_not_current(data, name, as_handle):
     for a, b in zip(want, got, strict=True):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     assert all(bool((j == 0xFF).all()) for j in junk)
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2])
+@pytest.mark.parametrize("name", ["swiglu_fwd e4m3", "tgmm_ckpt in parts", "mx4_fwd", "fp8_fwd"])
+def test_handles_of_the_default_streams(data, name, handle):
+    """The legacy default stream (0 and 1) and the calling thread's (2), while another one is current."""
+    want = [t.clone() for t in _flat(CALLS[name](data))]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = _flat(CALLS[name](data, stream=handle))
+        junk = [torch.full((1 << i,), 0xFF, dtype=torch.uint8, device="cuda") for i in range(9, 24)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got, strict=True):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert all(bool((j == 0xFF).all()) for j in junk)

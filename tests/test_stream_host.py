@@ -128,3 +128,21 @@ def test_the_callers_stream_is_current_again_after_a_refusal(machine, monkeypatc
     with pytest.raises(g.GmmError):
         CASES["swiglu_fwd"](g, stream=Stream(SIDE))
     assert len(now) == 1
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+@pytest.mark.parametrize("name", ["swiglu_fwd", "tgmm_ckpt", "mx4_fwd", "fp8_fwd", "quantize_lhs"])
+def test_the_default_streams_handles(machine, monkeypatch, name, handle):
+    """cudaStreamLegacy and 0 both name the default stream; torch has no external stream for
+    them: it makes a new stream of 0 and refuses 1."""
+    g, log, now = machine
+
+    def external(h, device=None):
+        assert h > 1, "torch would make a new stream" if h == 0 else "torch refuses this handle"
+        return Stream(h)
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: Stream(0))
+    CASES[name](g, stream=handle)
+    assert {s for k, s in log if k == "alloc"} == {0} and {s for k, s in log if k == "launch"} <= {0, 1}, log
+    assert len(now) == 1
