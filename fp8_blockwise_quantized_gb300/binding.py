@@ -14,8 +14,6 @@ without it every call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 import math
 import os
 
@@ -351,29 +349,21 @@ def _stream_of(handle, device):
     return torch.cuda.ExternalStream(handle, device=device)
 
 
-def _on_stream(wrapper):
-    """Makes `stream`, when it is given, the current stream for the wrapper's
-    own allocations (outputs, scratch, a temporary workspace and its zero fill)
-    as well as for its kernels.  Memory taken from another stream's pool would
-    be ordered by nothing: its zero fill could come after the kernel, and once
+def _other(stream):
+    """The context that makes `stream` current, or None where it is already.
+
+    A wrapper that is given a stream starts over inside it: its own allocations
+    (outputs, scratch, a temporary workspace and its zero fill) then come from
+    that stream's memory.  Memory taken from another stream's pool would be
+    ordered by nothing: its zero fill could come after the kernel, and once
     released it could serve that other stream while the kernel still runs.  The
     outputs belong to `stream`, as those of any torch operation on it."""
-    at = list(inspect.signature(wrapper).parameters).index("stream")
-
-    @functools.wraps(wrapper)
-    def call(*args, **kw):
-        stream = args[at] if len(args) > at else kw.get("stream")
-        if stream is None:
-            return wrapper(*args, **kw)
-        current = torch.cuda.current_stream()
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = _stream_of(int(stream), current.device)
-        if stream.cuda_stream == current.cuda_stream and stream.device == current.device:
-            return wrapper(*args, **kw)
-        with torch.cuda.stream(stream):
-            return wrapper(*args, **kw)
-
-    return call
+    current = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = _stream_of(int(stream), current.device)
+    if stream.cuda_stream == current.cuda_stream and stream.device == current.device:
+        return None
+    return torch.cuda.stream(stream)
 
 
 class Workspace:
@@ -433,9 +423,11 @@ def _ws_for(group_sizes, ws, G, M, device):
     return _ws(ws, G, M, device)
 
 
-@_on_stream
 def quantize_lhs(x: torch.Tensor, stream=None):
     """x bf16 [M, K] -> (xq uint8 [M, K] e4m3 codes, xs float32 [K/128, M])."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return quantize_lhs(x, stream)
     M, K = x.shape
     xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     xs = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
@@ -443,9 +435,11 @@ def quantize_lhs(x: torch.Tensor, stream=None):
     return xq, xs
 
 
-@_on_stream
 def quantize_rhs(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq uint8 [G, N, K] e4m3 codes, ws float32 [G, K/128, N/128])."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return quantize_rhs(w, stream)
     G, K, N = w.shape
     wq = torch.empty((G, N, K), dtype=torch.uint8, device=w.device)
     ws = torch.empty((G, K // 128, N // 128), dtype=torch.float32, device=w.device)
@@ -453,9 +447,11 @@ def quantize_rhs(w: torch.Tensor, stream=None):
     return wq, ws
 
 
-@_on_stream
 def quantize_rhs_w4(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq4 uint8 [G, N, K/2] packed E2M1 codes, ws float32 [G, K/128, N/128])."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return quantize_rhs_w4(w, stream)
     G, K, N = w.shape
     wq4 = torch.empty((G, N, K // 2), dtype=torch.uint8, device=w.device)
     ws = torch.empty((G, K // 128, N // 128), dtype=torch.float32, device=w.device)
@@ -463,9 +459,11 @@ def quantize_rhs_w4(w: torch.Tensor, stream=None):
     return wq4, ws
 
 
-@_on_stream
 def fp8_w4_fwd(xq, xs, wq4, ws, group_sizes, fuse=False, out=None, workspace=None, stream=None, config=None):
     """The FP8 forward with 4-bit weights (wq4 [G, Nw, K/2] from quantize_rhs_w4)."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return fp8_w4_fwd(xq, xs, wq4, ws, group_sizes, fuse, out, workspace, stream, config)
     M, K = xq.shape
     G, Nw, K2 = wq4.shape
     assert 2 * K2 == K
@@ -478,10 +476,12 @@ def fp8_w4_fwd(xq, xs, wq4, ws, group_sizes, fuse=False, out=None, workspace=Non
     return out
 
 
-@_on_stream
 def fp8_w4_fwd_swiglu_quant(xq, xs, wq4, ws, group_sizes, with_h=True, workspace=None, stream=None, config=None,
                             out=None):
     """Fused wi with 4-bit weights: returns (h or None, hq, hs) as fp8_fwd_swiglu_quant."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return fp8_w4_fwd_swiglu_quant(xq, xs, wq4, ws, group_sizes, with_h, workspace, stream, config, out)
     M, K = xq.shape
     G, Nw, K2 = wq4.shape
     assert 2 * K2 == K
@@ -498,9 +498,11 @@ def fp8_w4_fwd_swiglu_quant(xq, xs, wq4, ws, group_sizes, with_h=True, workspace
     return h, hq, hs
 
 
-@_on_stream
 def fp8_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, stream=None, config=None):
     """config: a tile configuration (see TileConfig), or None for the defaults."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return fp8_fwd(xq, xs, wq, ws, group_sizes, fuse, out, workspace, stream, config)
     M, K = xq.shape
     G, Nw, K2 = wq.shape
     assert K2 == K
@@ -517,12 +519,14 @@ def fp8_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, s
     return out
 
 
-@_on_stream
 def fp8_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=None, stream=None, config=None,
                          out=None):
     """Fused wi: returns (h or None, hq [M, N] e4m3 codes, hs [N/128, M]).
     config: a tile configuration (see TileConfig), or None for the defaults;
     out: an (h, hq, hs) triple to write into instead of new tensors."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return fp8_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h, workspace, stream, config, out)
     M, K = xq.shape
     G, Nw, K2 = wq.shape
     assert K2 == K
@@ -543,8 +547,10 @@ def fp8_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
     return h, hq, hs
 
 
-@_on_stream
 def bf16_fwd(x, w, group_sizes, fuse=False, out=None, workspace=None, stream=None):
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return bf16_fwd(x, w, group_sizes, fuse, out, workspace, stream)
     M, K = x.shape
     G, K2, Nw = w.shape
     assert K2 == K
@@ -557,9 +563,11 @@ def bf16_fwd(x, w, group_sizes, fuse=False, out=None, workspace=None, stream=Non
     return out
 
 
-@_on_stream
 def dgrad(dy, w, group_sizes, dx=None, workspace=None, stream=None):
     """dx [M, K] = dy [M, N] . w[g]^T per group, w [G, K, N]."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return dgrad(dy, w, group_sizes, dx, workspace, stream)
     M, N = dy.shape
     G, K, N2 = w.shape
     assert N2 == N
@@ -570,8 +578,10 @@ def dgrad(dy, w, group_sizes, dx=None, workspace=None, stream=None):
     return dx
 
 
-@_on_stream
 def tgmm(x, dy, group_sizes, dw=None, workspace=None, stream=None, config=None):
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return tgmm(x, dy, group_sizes, dw, workspace, stream, config)
     M, K = x.shape
     M2, N = dy.shape
     assert M2 == M
@@ -594,40 +604,37 @@ def tgmm(x, dy, group_sizes, dw=None, workspace=None, stream=None, config=None):
     return dw
 
 
-@_on_stream
 def group_metadata(group_sizes, M, workspace=None, stream=None) -> Workspace:
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return group_metadata(group_sizes, M, workspace, stream)
     G = group_sizes.numel()
     ws_ = _ws(workspace, G, M, group_sizes.device)
     _check(gmm_group_metadata(group_sizes, G, M, ws_.buf, ws_.nbytes, stream), "gmm_group_metadata")
     return ws_
 
 
-def _device():
-    """Index of the current device, on which the kernels will run; None while
-    CUDA has not been used, when there are no CUDA tensors either."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else None
-
-
-def _need(what, t, on, dtype, *shape):
+def _need(what, t, on, dtype, *shape, flat=False):
     """Refuses what the kernels would read or write wrongly: they take dense
-    buffers of their own device (`on`) and know neither strides nor types.  One
-    number: that many elements, in any shape."""
+    buffers of their own device (`on`: the index of the call's first tensor,
+    which _here compares with the current device) and know neither strides nor
+    types.  One number: that many elements, in any shape; flat: or as many in
+    one dimension."""
     if len(shape) == 1:
         same = t.numel() == shape[0]
     else:
-        same = t.shape == shape
-    if t.dtype is not dtype or not same or not t.is_contiguous() or t.get_device() != on:
-        where = "" if on is None else f" on cuda:{on}"
+        same = t.shape == shape or (flat and t.dim() == 1 and t.numel() == math.prod(shape))
+    if t.dtype is not dtype or not same or not t.is_contiguous() or t.get_device() != on or on < 0:
+        where = "" if on < 0 else f" on cuda:{on}"
         raise ValueError(f"{what}: expected a contiguous CUDA tensor of {'x'.join(map(str, shape))} {dtype} elements"
                          f"{where}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _need_scales(what, t, on, *shape):
-    """MXFP4 scale bytes in the kernels' order: of this shape, or flat."""
-    if t.dim() == 1:
-        _need(what, t, on, torch.uint8, math.prod(shape))
-    else:
-        _need(what, t, on, torch.uint8, *shape)
+def _here(on):
+    """Refuses tensors of a device that is not current: the kernels run on that one."""
+    dev = torch.cuda.current_device()
+    if dev != on:
+        raise ValueError(f"the tensors are on cuda:{on}, the current device is cuda:{dev}")
 
 
 def _need_sizes(group_sizes, on, G):
@@ -637,8 +644,11 @@ def _need_sizes(group_sizes, on, G):
 
 def _ws_on(on, group_sizes, ws, G, M, device):
     """_ws_for, with a workspace given checked for its device."""
-    if ws is not None and ws.buf.get_device() != on:
-        raise ValueError(f"workspace: expected one on cuda:{on}, got one on {ws.buf.device}")
+    if ws is not None:
+        if ws.buf.get_device() != on:
+            raise ValueError(f"workspace: expected one on cuda:{on}, got one on {ws.buf.device}")
+        if ws.fits(G, M):
+            return ws
     return _ws_for(group_sizes, ws, G, M, device)
 
 
@@ -651,7 +661,7 @@ def _new3(a, b, c, dtype, device):
     return torch.empty_strided((a, b, c), (b * c, c, 1), dtype=dtype, device=device)
 
 
-def _need_kept(kept, M, N, keep=None, on=None):
+def _need_kept(kept, M, N, keep=None, on=-1):
     """Checks kept gate | up values (of the form `keep`, if given); returns (gu, guq, gus)."""
     if isinstance(kept, (tuple, list)) and keep != "bf16":
         guq, gus = kept
@@ -664,21 +674,24 @@ def _need_kept(kept, M, N, keep=None, on=None):
     return kept, None, None
 
 
-@_on_stream
 def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=None):
     """The gated block's forward: x bf16 [M, K], w bf16 [G, K, 2N] (gate | up)
     -> (h bf16 [M, N], kept), kept being what swiglu_bwd takes: the gate | up
     values in bf16 [M, 2N] (keep="bf16"), or their 8-bit checkpoint (codes
     uint8 [M, 2N], scales float32 [2N/128, M]) (keep="e4m3").
     out: an (h, kept) pair to write into instead of new tensors."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return swiglu_fwd(x, w, group_sizes, keep, workspace, stream, out)
     if keep not in ("bf16", "e4m3"):
         raise ValueError(f"keep must be 'bf16' or 'e4m3', got {keep!r}")
     M, K = x.shape
     G, K2, Nw = w.shape
     assert K2 == K and Nw % 2 == 0
     N = Nw // 2
-    on = _device()
+    on = x.get_device()
     _need("x", x, on, torch.bfloat16, M, K)
+    _here(on)
     _need("w", w, on, torch.bfloat16, G, K, Nw)
     _need_sizes(group_sizes, on, G)
     if out is not None:
@@ -698,17 +711,20 @@ def swiglu_fwd(x, w, group_sizes, keep="bf16", workspace=None, stream=None, out=
     return h, kept
 
 
-@_on_stream
 def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=None, out=None):
     """Its backward pass: dy bf16 [M, K] (the gradient of y = h W2), w2 bf16
     [G, N, K], kept as swiglu_fwd returned it -> (dgu bf16 [M, 2N], the gradient
     of gate | up; h bf16 [M, N], recomputed, or None).
     out: a (dgu, h) pair to write into instead of new tensors."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return swiglu_bwd(dy, w2, kept, group_sizes, with_h, workspace, stream, out)
     M, K = dy.shape
     G, N, K2 = w2.shape
     assert K2 == K
-    on = _device()
+    on = dy.get_device()
     _need("dy", dy, on, torch.bfloat16, M, K)
+    _here(on)
     _need("w2", w2, on, torch.bfloat16, G, N, K)
     _need_sizes(group_sizes, on, G)
     gu, guq, gus = _need_kept(kept, M, N, on=on)
@@ -726,16 +742,19 @@ def swiglu_bwd(dy, w2, kept, group_sizes, with_h=True, workspace=None, stream=No
     return dgu, h
 
 
-@_on_stream
 def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     """tgmm from the 8-bit checkpoint of x: xq uint8 [M, K] e4m3 codes, xs
     float32 [K/128, M] (quantize_lhs), dy bf16 [M, N] -> dw bf16 [G, K, N].
     The scratch that few tiles with many rows need is allocated with torch."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return tgmm_ckpt(xq, xs, dy, group_sizes, dw, workspace, stream)
     M, K = xq.shape
     M2, N = dy.shape
     assert M2 == M
-    on = _device()
+    on = xq.get_device()
     _need("xq", xq, on, torch.uint8, M, K)
+    _here(on)
     _need("xs", xs, on, torch.float32, K // 128, M)
     _need("dy", dy, on, torch.bfloat16, M, N)
     if group_sizes is not None:
@@ -761,16 +780,19 @@ def tgmm_ckpt(xq, xs, dy, group_sizes, dw=None, workspace=None, stream=None):
     return dw
 
 
-@_on_stream
 def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
     """x bf16 [M, K] -> (xq uint8 [M, K/2] packed E2M1 codes, xs uint8 [K/128, M, 4] E8M0 scales)."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return mx4_quantize_lhs(x, stream, out)
     M, K = x.shape
-    on = _device()
+    on = x.get_device()
     _need("x", x, on, torch.bfloat16, M, K)
+    _here(on)
     if out is not None:
         xq, xs = out
         _need("out codes", xq, on, torch.uint8, M, K // 2)
-        _need_scales("out scales", xs, on, K // 128, M, 4)
+        _need("out scales", xs, on, torch.uint8, K // 128, M, 4, flat=True)
     else:
         xq = _new2(M, K // 2, torch.uint8, x.device)
         xs = _new3(K // 128, M, 4, torch.uint8, x.device)
@@ -778,12 +800,15 @@ def mx4_quantize_lhs(x: torch.Tensor, stream=None, out=None):
     return xq, xs
 
 
-@_on_stream
 def mx4_quantize_rhs(w: torch.Tensor, stream=None):
     """w bf16 [G, K, N] -> (wq uint8 [G, N, K/2] packed E2M1 codes, ws uint8 [G, N/128, K/128, 512] E8M0 scales)."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return mx4_quantize_rhs(w, stream)
     G, K, N = w.shape
-    on = _device()
+    on = w.get_device()
     _need("w", w, on, torch.bfloat16, G, K, N)
+    _here(on)
     wq = _new3(G, N, K // 2, torch.uint8, w.device)
     ws = torch.empty((G, N // 128, K // 128, 512), dtype=torch.uint8, device=w.device)
     _check(gmm_mx4_quantize_rhs(w, G, K, N, wq, ws, stream), "gmm_mx4_quantize_rhs")
@@ -792,20 +817,23 @@ def mx4_quantize_rhs(w: torch.Tensor, stream=None):
 
 def _need_mx4(on, xq, xs, wq, ws, group_sizes, M, K2, G, Nw):
     _need("xq", xq, on, torch.uint8, M, K2)
-    _need_scales("xs", xs, on, K2 // 64, M, 4)
+    _here(on)
+    _need("xs", xs, on, torch.uint8, K2 // 64, M, 4, flat=True)
     _need("wq", wq, on, torch.uint8, G, Nw, K2)
-    _need_scales("ws", ws, on, G, Nw // 128, K2 // 64, 512)
+    _need("ws", ws, on, torch.uint8, G, Nw // 128, K2 // 64, 512, flat=True)
     _need_sizes(group_sizes, on, G)
 
 
-@_on_stream
 def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, stream=None):
     """MXFP4 x MXFP4 grouped product -> bf16 [M, N] (fuse: silu(gate) * up, wq holding gate | up)."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return mx4_fwd(xq, xs, wq, ws, group_sizes, fuse, out, workspace, stream)
     M, K2 = xq.shape
     G, Nw, K3 = wq.shape
     assert K3 == K2
     N = Nw // 2 if fuse else Nw
-    on = _device()
+    on = xq.get_device()
     _need_mx4(on, xq, xs, wq, ws, group_sizes, M, K2, G, Nw)
     if out is not None:
         _need("out", out, on, torch.bfloat16, M, N)
@@ -817,22 +845,24 @@ def mx4_fwd(xq, xs, wq, ws, group_sizes, fuse=False, out=None, workspace=None, s
     return out
 
 
-@_on_stream
 def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=None, stream=None, out=None):
     """Fused gate/up product: (h bf16 [M, N] or None, hq, hs), hq and hs being h in MXFP4.
     out: an (h, hq, hs) triple to write into instead of new tensors."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h, workspace, stream, out)
     M, K2 = xq.shape
     G, Nw, K3 = wq.shape
     assert K3 == K2
     N = Nw // 2
-    on = _device()
+    on = xq.get_device()
     _need_mx4(on, xq, xs, wq, ws, group_sizes, M, K2, G, Nw)
     if out is not None:
         h, hq, hs = out
         if h is not None:
             _need("out h", h, on, torch.bfloat16, M, N)
         _need("out hq", hq, on, torch.uint8, M, N // 2)
-        _need_scales("out hs", hs, on, N // 128, M, 4)
+        _need("out hs", hs, on, torch.uint8, N // 128, M, 4, flat=True)
     else:
         h = _new2(M, N, torch.bfloat16, xq.device) if with_h else None
         hq = _new2(M, N // 2, torch.uint8, xq.device)

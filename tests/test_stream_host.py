@@ -91,8 +91,9 @@ def machine(monkeypatch):
 
     for name in ("empty", "zeros", "empty_strided"):
         monkeypatch.setattr(torch, name, spy(getattr(torch, name)))
-    monkeypatch.setattr(g, "_need", lambda *a: None)
+    monkeypatch.setattr(g, "_need", lambda *a, **k: None)
     monkeypatch.setattr(g, "_need_sizes", lambda *a: None)
+    monkeypatch.setattr(g, "_here", lambda on: None)  # the tensors' device
     for name in g.EXPORTED:
         if name.startswith(("gmm_", "tgmm_")) and name not in ("gmm_workspace_bytes", "gmm_tiles_offset") and hasattr(g, name):
             def launch(*a, **k):
