@@ -17,7 +17,12 @@ from .binding import (EXPORTED, GmmError, LIB_PATH, STATUS_NAMES, Workspace, bf1
                       gmm_bf16_swiglu_fwd, gmm_bf16_swiglu_bwd, tgmm_fp8_ckpt, tgmm_fp8_ckpt_scratch_bytes, gmm_mx4_quantize_lhs,
                       gmm_mx4_quantize_rhs, gmm_mx4_fwd, gmm_mx4_fwd_swiglu_quant,
                       swiglu_fwd, swiglu_bwd, tgmm_ckpt, mx4_quantize_lhs,
-                      mx4_quantize_rhs, mx4_fwd, mx4_fwd_swiglu_quant)
+                      mx4_quantize_rhs, mx4_fwd, mx4_fwd_swiglu_quant,
+                      gmm_route, gmm_route_bwd, gmm_sort_rows, gmm_sort_rows_scratch_bytes, gmm_gather_rows,
+                      gmm_gather_quantize, gmm_combine_rows, gmm_combine_rows_bwd, gmm_norm_join, gmm_norm_join_bwd,
+                      gmm_norm_join_bwd_scratch_bytes, gmm_clip_grads, gmm_clip_grads_scratch_bytes,
+                      route, route_bwd, sort_rows, gather_rows, gather_quantize, combine_rows, combine_rows_bwd,
+                      norm_join, norm_join_bwd, clip_grads)
 
 __all__ = ["EXPORTED", "GmmError", "LIB_PATH", "STATUS_NAMES", "Workspace", "bf16_fwd", "dgrad", "fp8_fwd",
            "gmm_bf16_dgrad", "gmm_selftest_wait_timeout", "gmm_fp8_fwd_swiglu_quant", "fp8_fwd_swiglu_quant",
@@ -31,4 +36,9 @@ __all__ = ["EXPORTED", "GmmError", "LIB_PATH", "STATUS_NAMES", "Workspace", "bf1
            "gmm_bf16_swiglu_fwd", "gmm_bf16_swiglu_bwd", "tgmm_fp8_ckpt", "tgmm_fp8_ckpt_scratch_bytes", "gmm_mx4_quantize_lhs",
            "gmm_mx4_quantize_rhs", "gmm_mx4_fwd", "gmm_mx4_fwd_swiglu_quant",
            "swiglu_fwd", "swiglu_bwd", "tgmm_ckpt", "mx4_quantize_lhs",
-           "mx4_quantize_rhs", "mx4_fwd", "mx4_fwd_swiglu_quant"]
+           "mx4_quantize_rhs", "mx4_fwd", "mx4_fwd_swiglu_quant",
+           "gmm_route", "gmm_route_bwd", "gmm_sort_rows", "gmm_sort_rows_scratch_bytes", "gmm_gather_rows",
+           "gmm_gather_quantize", "gmm_combine_rows", "gmm_combine_rows_bwd", "gmm_norm_join", "gmm_norm_join_bwd",
+           "gmm_norm_join_bwd_scratch_bytes", "gmm_clip_grads", "gmm_clip_grads_scratch_bytes",
+           "route", "route_bwd", "sort_rows", "gather_rows", "gather_quantize", "combine_rows", "combine_rows_bwd",
+           "norm_join", "norm_join_bwd", "clip_grads"]

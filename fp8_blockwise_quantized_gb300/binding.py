@@ -13,6 +13,7 @@ without it every call raises: there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -36,7 +37,9 @@ EXPORTED = ["gmm_status_string", "gmm_last_cuda_error", "gmm_workspace_bytes", "
             "gmm_fp8_fwd_swiglu_quant_tiled", "gmm_quantize_rhs_w4", "gmm_fp8_w4_fwd",
             "gmm_fp8_w4_fwd_swiglu_quant", "tgmm_bf16_tiled", "gmm_bf16_swiglu_fwd", "gmm_bf16_swiglu_bwd",
             "tgmm_fp8_ckpt", "tgmm_fp8_ckpt_scratch_bytes", "gmm_mx4_quantize_lhs", "gmm_mx4_quantize_rhs", "gmm_mx4_fwd",
-            "gmm_mx4_fwd_swiglu_quant"]
+            "gmm_mx4_fwd_swiglu_quant", "gmm_route", "gmm_route_bwd", "gmm_sort_rows_scratch_bytes", "gmm_sort_rows",
+            "gmm_gather_rows", "gmm_gather_quantize", "gmm_combine_rows", "gmm_combine_rows_bwd", "gmm_norm_join",
+            "gmm_norm_join_bwd_scratch_bytes", "gmm_norm_join_bwd", "gmm_clip_grads_scratch_bytes", "gmm_clip_grads"]
 
 
 class TileConfig(ctypes.Structure):
@@ -145,6 +148,33 @@ def load():
     lib.gmm_mx4_fwd.argtypes = [P, P, P, P, P, I, I64, I64, I64, I, P, P, SZ, P]
     lib.gmm_mx4_fwd_swiglu_quant.restype = I
     lib.gmm_mx4_fwd_swiglu_quant.argtypes = [P, P, P, P, P, I, I64, I64, I64, P, P, P, P, SZ, P]
+    F = ctypes.c_float
+    lib.gmm_route.restype = I
+    lib.gmm_route.argtypes = [P, I, P, I64, I, I, I, I, F, P, P, P]
+    lib.gmm_route_bwd.restype = I
+    lib.gmm_route_bwd.argtypes = [P, P, I, P, I64, I, I, I, I, F, P, P]
+    lib.gmm_sort_rows_scratch_bytes.restype = SZ
+    lib.gmm_sort_rows_scratch_bytes.argtypes = [I64, I]
+    lib.gmm_sort_rows.restype = I
+    lib.gmm_sort_rows.argtypes = [P, I64, I, P, P, P, SZ, P]
+    lib.gmm_gather_rows.restype = I
+    lib.gmm_gather_rows.argtypes = [P, P, I64, I, I64, P, P]
+    lib.gmm_gather_quantize.restype = I
+    lib.gmm_gather_quantize.argtypes = [P, P, I64, I, I64, P, P, P]
+    lib.gmm_combine_rows.restype = I
+    lib.gmm_combine_rows.argtypes = [P, P, P, I64, I, I64, P, P]
+    lib.gmm_combine_rows_bwd.restype = I
+    lib.gmm_combine_rows_bwd.argtypes = [P, P, P, P, I64, I, I64, P, P, P]
+    lib.gmm_norm_join.restype = I
+    lib.gmm_norm_join.argtypes = [P, I, P, P, P, I, P, I64, I64, F, F, F, P, P, P]
+    lib.gmm_norm_join_bwd_scratch_bytes.restype = SZ
+    lib.gmm_norm_join_bwd_scratch_bytes.argtypes = [I64, I64]
+    lib.gmm_norm_join_bwd.restype = I
+    lib.gmm_norm_join_bwd.argtypes = [P, P, P, I, P, P, P, I, P, I64, I64, F, F, F, P, P, P, P, P, P, SZ, P]
+    lib.gmm_clip_grads_scratch_bytes.restype = SZ
+    lib.gmm_clip_grads_scratch_bytes.argtypes = [I]
+    lib.gmm_clip_grads.restype = I
+    lib.gmm_clip_grads.argtypes = [P, P, P, P, I, F, P, P, SZ, P]
     _lib = lib
     return lib
 
@@ -335,6 +365,69 @@ def gmm_mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, G, M, K, N, h, hq, hs,
                              stream=None) -> int:
     return load().gmm_mx4_fwd_swiglu_quant(_p(xq), _p(xs), _p(wq), _p(ws), _p(group_sizes), G, M, K, N, _p(h),
                                            _p(hq), _p(hs), _p(workspace), workspace_bytes, _s(stream))
+
+
+def gmm_route(logits, logits_type, bias, T, E, k, score, renorm, scale, ids, weights, stream=None) -> int:
+    return load().gmm_route(_p(logits), logits_type, _p(bias), T, E, k, score, int(renorm), scale, _p(ids),
+                            _p(weights), _s(stream))
+
+
+def gmm_route_bwd(dweights, logits, logits_type, ids, T, E, k, score, renorm, scale, dlogits, stream=None) -> int:
+    return load().gmm_route_bwd(_p(dweights), _p(logits), logits_type, _p(ids), T, E, k, score, int(renorm), scale,
+                                _p(dlogits), _s(stream))
+
+
+def gmm_sort_rows_scratch_bytes(N: int, G: int) -> int:
+    return int(load().gmm_sort_rows_scratch_bytes(N, G))
+
+
+def gmm_sort_rows(ids, N, G, rows, group_sizes, scratch, scratch_bytes, stream=None) -> int:
+    return load().gmm_sort_rows(_p(ids), N, G, _p(rows), _p(group_sizes), _p(scratch), scratch_bytes, _s(stream))
+
+
+def gmm_gather_rows(x, rows, T, k, K, out, stream=None) -> int:
+    return load().gmm_gather_rows(_p(x), _p(rows), T, k, K, _p(out), _s(stream))
+
+
+def gmm_gather_quantize(x, rows, T, k, K, xq, xs, stream=None) -> int:
+    return load().gmm_gather_quantize(_p(x), _p(rows), T, k, K, _p(xq), _p(xs), _s(stream))
+
+
+def gmm_combine_rows(y, rows, weights, T, k, K, out, stream=None) -> int:
+    return load().gmm_combine_rows(_p(y), _p(rows), _p(weights), T, k, K, _p(out), _s(stream))
+
+
+def gmm_combine_rows_bwd(dout, y, rows, weights, T, k, K, dy, dweights, stream=None) -> int:
+    return load().gmm_combine_rows_bwd(_p(dout), _p(y), _p(rows), _p(weights), T, k, K, _p(dy), _p(dweights),
+                                       _s(stream))
+
+
+def gmm_norm_join(x, stream_type, b, w_post, gate, gate_rows, w_next, T, K, residual_scale, block_scale, eps, out, n,
+                  stream=None) -> int:
+    return load().gmm_norm_join(_p(x), stream_type, _p(b), _p(w_post), _p(gate), int(gate_rows), _p(w_next), T, K,
+                                residual_scale, block_scale, eps, _p(out), _p(n), _s(stream))
+
+
+def gmm_norm_join_bwd_scratch_bytes(T: int, K: int) -> int:
+    return int(load().gmm_norm_join_bwd_scratch_bytes(T, K))
+
+
+def gmm_norm_join_bwd(dout, dn, out, stream_type, b, w_post, gate, gate_rows, w_next, T, K, residual_scale,
+                      block_scale, eps, dx, db, dw_post, dgate, dw_next, scratch, scratch_bytes, stream=None) -> int:
+    return load().gmm_norm_join_bwd(_p(dout), _p(dn), _p(out), stream_type, _p(b), _p(w_post), _p(gate),
+                                    int(gate_rows), _p(w_next), T, K, residual_scale, block_scale, eps, _p(dx),
+                                    _p(db), _p(dw_post), _p(dgate), _p(dw_next), _p(scratch), scratch_bytes,
+                                    _s(stream))
+
+
+def gmm_clip_grads_scratch_bytes(n: int) -> int:
+    return int(load().gmm_clip_grads_scratch_bytes(n))
+
+
+def gmm_clip_grads(grads, out, counts, types, n, max_norm, norm, scratch, scratch_bytes, stream=None) -> int:
+    """grads, out, counts, types: addresses of the HOST arrays (out may be None)."""
+    return load().gmm_clip_grads(grads, out, counts, types, n, max_norm, _p(norm), _p(scratch), scratch_bytes,
+                                 _s(stream))
 
 
 # ---------------------------------------------------------------------------
@@ -871,3 +964,332 @@ def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
     _check(gmm_mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, G, M, 2 * K2, N, h, hq, hs, ws_.buf, ws_.nbytes,
                                     stream), "gmm_mx4_fwd_swiglu_quant")
     return h, hq, hs
+
+
+# ---------------------------------------------------------------------------
+# around the experts: router, sorted rows, norms, clipping
+# ---------------------------------------------------------------------------
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _type_of(what, t):
+    """gmm_type of a tensor that may be bf16 or fp32."""
+    if t.dtype is torch.bfloat16:
+        return 0
+    if t.dtype is torch.float32:
+        return 1
+    raise ValueError(f"{what}: expected bfloat16 or float32 elements, got {t.dtype}")
+
+
+def _score_of(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return _SCORES[score]
+
+
+def _new1(a, dtype, device):
+    return torch.empty_strided((a,), (1,), dtype=dtype, device=device)
+
+
+def route(logits, top_k, bias=None, score="softmax", renorm=False, scale=1.0, stream=None, out=None):
+    """The top_k experts of each token and their weights: logits bf16 or float32
+    [T, E] -> (ids int32 [T, top_k], weights float32 [T, top_k]), largest logit +
+    bias (float32 [E]) first, ties to the lower id; -1 and 0 where fewer than top_k
+    are above -inf.  The weights are the softmax or sigmoid of the logits without
+    the bias (renorm: divided by the chosen ones' sum) times scale.
+    out: an (ids, weights) pair to write into instead of new tensors."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return route(logits, top_k, bias, score, renorm, scale, stream, out)
+    T, E = logits.shape
+    kind, how, on = _type_of("logits", logits), _score_of(score), logits.get_device()
+    _need("logits", logits, on, logits.dtype, T, E)
+    _here(on)
+    if bias is not None:
+        _need("bias", bias, on, torch.float32, E)
+    if out is not None:
+        ids, weights = out
+        _need("out ids", ids, on, torch.int32, T, top_k)
+        _need("out weights", weights, on, torch.float32, T, top_k)
+    else:
+        ids = _new2(T, top_k, torch.int32, logits.device)
+        weights = _new2(T, top_k, torch.float32, logits.device)
+    _check(gmm_route(logits, kind, bias, T, E, top_k, how, renorm, scale, ids, weights, stream), "gmm_route")
+    return ids, weights
+
+
+def route_bwd(dweights, logits, ids, score="softmax", renorm=False, scale=1.0, stream=None, out=None):
+    """Its gradient, the choice held fixed: dweights float32 [T, k], logits and ids
+    as in the forward -> dlogits [T, E], of the logits' type.  out: a tensor for it."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return route_bwd(dweights, logits, ids, score, renorm, scale, stream, out)
+    T, E = logits.shape
+    T2, k = ids.shape
+    assert T2 == T
+    kind, how, on = _type_of("logits", logits), _score_of(score), logits.get_device()
+    _need("logits", logits, on, logits.dtype, T, E)
+    _here(on)
+    _need("ids", ids, on, torch.int32, T, k)
+    _need("dweights", dweights, on, torch.float32, T, k)
+    if out is not None:
+        _need("out", out, on, logits.dtype, T, E)
+    else:
+        out = _new2(T, E, logits.dtype, logits.device)
+    _check(gmm_route_bwd(dweights, logits, kind, ids, T, E, k, how, renorm, scale, out, stream), "gmm_route_bwd")
+    return out
+
+
+def sort_rows(ids, G, stream=None, out=None):
+    """Places of the choices among the rows sorted by expert: ids int32 [T, k] (or
+    [N]) -> (rows int32 of ids' shape, group_sizes int32 [G]).  Group g holds the
+    choices of expert g in their order; an id outside 0..G-1 belongs to no group: its
+    row r lies behind them, and rows holds -1 - r.
+    out: a (rows, group_sizes) pair to write into instead of new tensors."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return sort_rows(ids, G, stream, out)
+    N, on = ids.numel(), ids.get_device()
+    _need("ids", ids, on, torch.int32, N)
+    _here(on)
+    if out is not None:
+        rows, sizes = out
+        _need("out rows", rows, on, torch.int32, *ids.shape)
+        _need("out group_sizes", sizes, on, torch.int32, G)
+    else:
+        rows = torch.empty_strided(ids.shape, ids.stride(), dtype=torch.int32, device=ids.device)
+        sizes = _new1(G, torch.int32, ids.device)
+    nbytes = gmm_sort_rows_scratch_bytes(N, G)
+    scratch = _new1(nbytes, torch.uint8, ids.device) if nbytes else None
+    _check(gmm_sort_rows(ids, N, G, rows, sizes, scratch, nbytes, stream), "gmm_sort_rows")
+    return rows, sizes
+
+
+def _need_rows(rows, on):
+    T, k = rows.shape
+    _need("rows", rows, on, torch.int32, T, k)
+    return T, k
+
+
+def gather_rows(x, rows, stream=None, out=None):
+    """x bf16 [T, K] by token, rows int32 [T, k] (sort_rows) -> bf16 [T k, K]: each
+    token's row at the places of its choices, zeros behind the groups."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return gather_rows(x, rows, stream, out)
+    on = x.get_device()
+    T, k = _need_rows(rows, on)
+    T2, K = x.shape
+    assert T2 == T
+    _need("x", x, on, torch.bfloat16, T, K)
+    _here(on)
+    if out is not None:
+        _need("out", out, on, torch.bfloat16, T * k, K)
+    else:
+        out = _new2(T * k, K, torch.bfloat16, x.device)
+    _check(gmm_gather_rows(x, rows, T, k, K, out, stream), "gmm_gather_rows")
+    return out
+
+
+def gather_quantize(x, rows, stream=None, out=None):
+    """quantize_lhs(gather_rows(x, rows)) in one pass: (xq uint8 [T k, K] e4m3 codes,
+    xs float32 [K/128, T k]).  out: an (xq, xs) pair to write into."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return gather_quantize(x, rows, stream, out)
+    on = x.get_device()
+    T, k = _need_rows(rows, on)
+    T2, K = x.shape
+    assert T2 == T
+    _need("x", x, on, torch.bfloat16, T, K)
+    _here(on)
+    if out is not None:
+        xq, xs = out
+        _need("out codes", xq, on, torch.uint8, T * k, K)
+        _need("out scales", xs, on, torch.float32, K // 128, T * k)
+    else:
+        xq = _new2(T * k, K, torch.uint8, x.device)
+        xs = _new2(K // 128, T * k, torch.float32, x.device)
+    _check(gmm_gather_quantize(x, rows, T, k, K, xq, xs, stream), "gmm_gather_quantize")
+    return xq, xs
+
+
+def combine_rows(y, rows, weights=None, stream=None, out=None):
+    """The sorted rows joined by token: y bf16 [T k, K], rows int32 [T, k], weights
+    float32 [T, k] (None: 1 each, the gradient of gather_rows) -> bf16 [T, K]."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return combine_rows(y, rows, weights, stream, out)
+    on = y.get_device()
+    T, k = _need_rows(rows, on)
+    K = y.shape[1]
+    _need("y", y, on, torch.bfloat16, T * k, K)
+    _here(on)
+    if weights is not None:
+        _need("weights", weights, on, torch.float32, T, k)
+    if out is not None:
+        _need("out", out, on, torch.bfloat16, T, K)
+    else:
+        out = _new2(T, K, torch.bfloat16, y.device)
+    _check(gmm_combine_rows(y, rows, weights, T, k, K, out, stream), "gmm_combine_rows")
+    return out
+
+
+def combine_rows_bwd(dout, y, rows, weights, stream=None, out=None):
+    """Its gradient: dout bf16 [T, K], the forward's y, rows and weights -> (dy bf16
+    [T k, K], dweights float32 [T, k]).  out: a (dy, dweights) pair to write into."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return combine_rows_bwd(dout, y, rows, weights, stream, out)
+    on = dout.get_device()
+    T, k = _need_rows(rows, on)
+    T2, K = dout.shape
+    assert T2 == T
+    _need("dout", dout, on, torch.bfloat16, T, K)
+    _here(on)
+    _need("y", y, on, torch.bfloat16, T * k, K)
+    _need("weights", weights, on, torch.float32, T, k)
+    if out is not None:
+        dy, dweights = out
+        _need("out dy", dy, on, torch.bfloat16, T * k, K)
+        _need("out dweights", dweights, on, torch.float32, T, k)
+    else:
+        dy = _new2(T * k, K, torch.bfloat16, dout.device)
+        dweights = _new2(T, k, torch.float32, dout.device)
+    _check(gmm_combine_rows_bwd(dout, y, rows, weights, T, k, K, dy, dweights, stream), "gmm_combine_rows_bwd")
+    return dy, dweights
+
+
+def _need_join(on, T, K, b, w_post, gate, w_next):
+    """Checks what the norms' two directions share; whether the gate has a row per token."""
+    if b is not None:
+        _need("b", b, on, torch.bfloat16, T, K)
+    elif w_post is not None or gate is not None:
+        raise ValueError("w_post and gate apply to the block's output: pass b")
+    if w_post is not None:
+        _need("w_post", w_post, on, torch.float32, K)
+    if w_next is not None:
+        _need("w_next", w_next, on, torch.float32, K)
+    if gate is None:
+        return False
+    if gate.dim() == 2:
+        _need("gate", gate, on, torch.bfloat16, T, K)
+        return True
+    _need("gate", gate, on, torch.float32, K)
+    return False
+
+
+def norm_join(x, b=None, w_post=None, gate=None, w_next=None, residual_scale=1.0, block_scale=1.0, eps=1e-6,
+              stream=None, out=None):
+    """The norms before and after a block, its gate and the residual stream:
+        out = residual_scale * x + block_scale * gate * (norm(b) * w_post),
+        n = norm(out) * w_next,  norm(v) = v / sqrt(mean(v^2) + eps)
+    x bf16 or float32 [T, K]; b bf16 [T, K]; w_post, w_next float32 [K]; gate
+    float32 [K] or bf16 [T, K] -> (out, of x's type; n bf16).  Without w_post b is
+    not normed, without gate it is 1, without w_next n is None; without b, out is x
+    and n the norm in front of a first block.
+    out: an (out, n) pair to write into instead of new tensors (out may be x, n b)."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return norm_join(x, b, w_post, gate, w_next, residual_scale, block_scale, eps, stream, out)
+    T, K = x.shape
+    kind, on = _type_of("x", x), x.get_device()
+    _need("x", x, on, x.dtype, T, K)
+    _here(on)
+    full = _need_join(on, T, K, b, w_post, gate, w_next)
+    if b is None and w_next is None:
+        raise ValueError("without b and w_next there is nothing to compute")
+    if out is not None:
+        o, n = out
+        if b is not None:
+            _need("out", o, on, x.dtype, T, K)
+        if w_next is not None:
+            _need("out n", n, on, torch.bfloat16, T, K)
+    else:
+        o = x if b is None else _new2(T, K, x.dtype, x.device)
+        n = None if w_next is None else _new2(T, K, torch.bfloat16, x.device)
+    _check(gmm_norm_join(x, kind, b, w_post, gate, full, w_next, T, K, residual_scale, block_scale, eps,
+                         None if b is None else o, n, stream), "gmm_norm_join")
+    return (x if b is None else o), n
+
+
+def norm_join_bwd(dout, dn, out, b=None, w_post=None, gate=None, w_next=None, residual_scale=1.0, block_scale=1.0,
+                  eps=1e-6, stream=None, into=None):
+    """Its gradient: dout (of out, and of its type) and dn (of n, bf16), one of which
+    may be None (zero); out as the forward gave it; the other arguments as in the
+    forward -> (dx of out's type, db bf16, dw_post float32 [K], dgate of the gate's
+    shape and type, dw_next float32 [K]), None for what the forward was not given.
+    into: a (dx, db) pair to write into instead of new tensors (dx may be dout, db dn or b)."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return norm_join_bwd(dout, dn, out, b, w_post, gate, w_next, residual_scale, block_scale, eps, stream,
+                                 into)
+    T, K = out.shape
+    kind, on = _type_of("out", out), out.get_device()
+    _need("out", out, on, out.dtype, T, K)
+    _here(on)
+    if dout is None and dn is None:
+        raise ValueError("one of dout and dn must be given")
+    if dout is not None:
+        _need("dout", dout, on, out.dtype, T, K)
+    if dn is not None:
+        _need("dn", dn, on, torch.bfloat16, T, K)
+        if w_next is None:
+            raise ValueError("dn is the gradient of n: pass w_next")
+    full = _need_join(on, T, K, b, w_post, gate, w_next)
+    dx = db = dw_post = dgate = dw_next = None
+    if into is not None:
+        dx, db = into
+        _need("into dx", dx, on, out.dtype, T, K)
+        if b is not None:
+            _need("into db", db, on, torch.bfloat16, T, K)
+    else:
+        dx = _new2(T, K, out.dtype, out.device)
+        db = None if b is None else _new2(T, K, torch.bfloat16, out.device)
+    if w_post is not None:
+        dw_post = _new1(K, torch.float32, out.device)
+    if gate is not None:
+        dgate = _new2(T, K, torch.bfloat16, out.device) if full else _new1(K, torch.float32, out.device)
+    if w_next is not None:
+        dw_next = _new1(K, torch.float32, out.device)
+    nbytes = gmm_norm_join_bwd_scratch_bytes(T, K)
+    scratch = _new1(nbytes, torch.uint8, out.device) if nbytes else None
+    _check(gmm_norm_join_bwd(dout, dn, out, kind, b, w_post, gate, full, w_next, T, K, residual_scale, block_scale,
+                             eps, dx, None if b is None else db, dw_post, dgate, dw_next, scratch, nbytes, stream),
+           "gmm_norm_join_bwd")
+    return dx, (None if b is None else db), dw_post, dgate, dw_next
+
+
+def clip_grads(grads, max_norm, out=None, stream=None):
+    """Gradients scaled by min(1, max_norm / norm), norm being the root of the sum of
+    all their squares, in place or into the tensors of `out` -> norm, float32 [1].
+    grads: contiguous bf16 or float32 tensors of any shapes.  A norm that is not
+    finite scales nothing; max_norm = math.inf computes the norm only."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return clip_grads(grads, max_norm, out, stream)
+    grads = list(grads)
+    n = len(grads)
+    if out is not None and len(out) != n:
+        raise ValueError(f"out: expected {n} tensors, got {len(out)}")
+    device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    on = grads[0].get_device() if n else device.index
+    types, counts = array.array("i"), array.array("q")
+    for i, g in enumerate(grads):
+        types.append(_type_of(f"grads[{i}]", g))
+        counts.append(g.numel())
+        if not g.is_contiguous() or g.get_device() != on or on < 0:
+            _need(f"grads[{i}]", g, on, g.dtype, *g.shape)
+        if out is not None and (out[i].dtype is not g.dtype or out[i].shape != g.shape or
+                                not out[i].is_contiguous() or out[i].get_device() != on):
+            _need(f"out[{i}]", out[i], on, g.dtype, *g.shape)
+    _here(on)
+    src = array.array("Q", [g.data_ptr() for g in grads])
+    dst = None if out is None else array.array("Q", [o.data_ptr() for o in out])
+    norm = _new1(1, torch.float32, device)
+    nbytes = gmm_clip_grads_scratch_bytes(n)
+    scratch = _new1(nbytes, torch.uint8, device) if nbytes else None
+    _check(gmm_clip_grads(src.buffer_info()[0], dst.buffer_info()[0] if dst else None, counts.buffer_info()[0],
+                          types.buffer_info()[0], n, max_norm, norm, scratch, nbytes, stream), "gmm_clip_grads")
+    return norm

@@ -1,0 +1,278 @@
+// The global norm of many gradients, and their scaling to a largest norm.
+//
+// The tensors come as a table in the launch's parameters, cut into chunks of one
+// length; a CTA finds a chunk's tensor by bisection.  The first pass leaves a sum
+// of squares a CTA, in double; each CTA of the second adds them all up in their
+// order, so that the norm is one number whatever the schedule, and scales.  The
+// second pass takes the chunks backwards: the ones that the first read last are
+// still in the L2.
+#include "common.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "rowvec.cuh"
+
+namespace gmm {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int N>
+struct ClipTable {
+  const void* src[N];
+  void* dst[N];
+  long long count[N];
+  int first[N + 1];  // chunks before
+  uint32_t f32[(N + 31) / 32];
+  int n, chunk;
+};
+
+struct Piece {
+  const void* src;
+  void* dst;
+  long long at;  // first element
+  int n;
+  bool f32;
+};
+
+template <int N>
+__device__ __forceinline__ Piece piece_of(const ClipTable<N>& tab, int c) {
+  int lo = 0, hi = tab.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab.first[mid] <= c) lo = mid; else hi = mid - 1;
+  }
+  Piece p;
+  p.src = tab.src[lo];
+  p.dst = tab.dst[lo];
+  p.at = static_cast<long long>(c - tab.first[lo]) * tab.chunk;
+  p.n = static_cast<int>(min(static_cast<long long>(tab.chunk), tab.count[lo] - p.at));
+  p.f32 = tab.f32[lo >> 5] >> (lo & 31) & 1u;
+  return p;
+}
+
+__device__ __forceinline__ float value_of(const float* p, long long i) { return p[i]; }
+__device__ __forceinline__ float value_of(const uint16_t* p, long long i) {
+  return __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+}
+__device__ __forceinline__ void put(float* p, long long i, float v) { p[i] = v; }
+__device__ __forceinline__ void put(uint16_t* p, long long i, float v) {
+  p[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xffffu);
+}
+
+// This thread's share of a chunk's squares.  The sum is fp32 over at most a few
+// hundred values (relative error below 2^-18 / 8, and of either sign); where that
+// left the range in which squares keep their bits, the share is added up again in
+// double: 1e-25 is 2^43 times the smallest normal square's.
+template <typename T>
+__device__ double squares_of(const T* __restrict__ p, int n) {
+  constexpr int W = 16 / sizeof(T);
+  float s = 0.0f;
+  bool some = false;
+  const bool wide = (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+  const int nv = wide ? n / W : 0;
+  const uint4* v = reinterpret_cast<const uint4*>(p);
+  for (int i0 = 0; i0 < nv; i0 += 4 * kThreads) {
+    uint4 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kThreads + threadIdx.x;
+      u[j] = i < nv ? __ldg(v + i) : make_uint4(0, 0, 0, 0);
+    }
+    float a[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      some |= (u[j].x | u[j].y | u[j].z | u[j].w) != 0;
+      a[j] = 0.0f;
+      if constexpr (sizeof(T) == 2) {
+        float f[8];
+        unpack8(u[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[j] = fmaf(f[e], f[e], a[j]);
+      } else {
+        const float f[4] = {__uint_as_float(u[j].x), __uint_as_float(u[j].y), __uint_as_float(u[j].z),
+                            __uint_as_float(u[j].w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[j] = fmaf(f[e], f[e], a[j]);
+      }
+    }
+    s += (a[0] + a[1]) + (a[2] + a[3]);
+  }
+  for (int i = nv * W + threadIdx.x; i < n; i += kThreads) {
+    const float f = value_of(p, i);
+    some |= f != 0.0f;
+    s = fmaf(f, f, s);
+  }
+  if (!some || (s > 1e-25f && s < 1e37f)) return s;
+  double d = 0.0;
+  for (int i0 = 0; i0 < nv; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    if (i < nv)
+      for (int e = 0; e < W; ++e) {
+        const double f = value_of(p, static_cast<long long>(i) * W + e);
+        d += f * f;
+      }
+  }
+  for (int i = nv * W + threadIdx.x; i < n; i += kThreads) {
+    const double f = value_of(p, i);
+    d += f * f;
+  }
+  return d;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+  return s;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_constant__ ClipTable<N> tab,
+                                                             double* __restrict__ parts) {
+  __shared__ double red[kThreads / 32];
+  griddep_launch_dependents();
+  griddep_wait();
+  double s = 0.0;
+  for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
+    const Piece p = piece_of(tab, c);
+    s += p.f32 ? squares_of(static_cast<const float*>(p.src) + p.at, p.n)
+               : squares_of(static_cast<const uint16_t*>(p.src) + p.at, p.n);
+  }
+  s = block_sum(s, red);
+  if (threadIdx.x == 0) parts[blockIdx.x] = s;
+}
+
+// dst = src * by; a factor of 1 copies the bits (a product would give NaNs another payload).
+template <typename T>
+__device__ void scale_piece(const T* src, T* dst, int n, float by) {
+  const bool copy = by == 1.0f;
+  constexpr int W = 16 / sizeof(T);
+  const bool wide = ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15u) == 0;
+  const int nv = wide ? n / W : 0;
+  const uint4* v = reinterpret_cast<const uint4*>(src);
+  uint4* o = reinterpret_cast<uint4*>(dst);
+  for (int i0 = 0; i0 < nv; i0 += 4 * kThreads) {
+    uint4 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kThreads + threadIdx.x;
+      if (i < nv) u[j] = v[i];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kThreads + threadIdx.x;
+      if (i >= nv) continue;
+      if (copy) {
+        __stcs(o + i, u[j]);
+        continue;
+      }
+      if constexpr (sizeof(T) == 2) {
+        float f[8];
+        unpack8(u[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= by;
+        __stcs(o + i, pack8(f));
+      } else {
+        const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+        uint32_t r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = __float_as_uint(__uint_as_float(w[e]) * by);
+        __stcs(o + i, make_uint4(r[0], r[1], r[2], r[3]));
+      }
+    }
+  }
+  for (int i = nv * W + threadIdx.x; i < n; i += kThreads) if (copy) dst[i] = src[i]; else put(dst, i, value_of(src, i) * by);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ ClipTable<N> tab,
+                                                              const double* __restrict__ parts, int P, float max_norm,
+                                                              int in_place, float* __restrict__ norm) {
+  __shared__ double red[kThreads / 32];
+  griddep_launch_dependents();
+  griddep_wait();
+  double s = 0.0;
+  for (int i = threadIdx.x; i < P; i += kThreads) s += parts[i];
+  const float whole = static_cast<float>(sqrt(block_sum(s, red)));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
+  // a norm that is not finite scales nothing
+  const float by = whole > max_norm && whole <= 3.402823466e38f ? max_norm / whole : 1.0f;
+  if (in_place && by == 1.0f) return;
+  for (int c = tab.first[tab.n] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+    const Piece p = piece_of(tab, c);
+    if (p.f32)
+      scale_piece(static_cast<const float*>(p.src) + p.at, static_cast<float*>(p.dst) + p.at, p.n, by);
+    else
+      scale_piece(static_cast<const uint16_t*>(p.src) + p.at, static_cast<uint16_t*>(p.dst) + p.at, p.n, by);
+  }
+}
+
+constexpr int kSmallTable = 64, kLargeTable = 1000;  // 1.9 and 28.2 KB of parameters
+
+// Chunks of one launch's tensors.
+template <int N>
+void fill(ClipTable<N>& tab, const ClipTensor* t, int n, int chunk) {
+  tab.n = n;
+  tab.chunk = chunk;
+  for (uint32_t& w : tab.f32) w = 0;
+  long long first = 0;
+  for (int i = 0; i < n; ++i) {
+    tab.src[i] = t[i].src;
+    tab.dst[i] = t[i].dst;
+    tab.count[i] = t[i].count;
+    tab.first[i] = static_cast<int>(first);
+    if (t[i].f32) tab.f32[i >> 5] |= 1u << (i & 31);
+    first += (t[i].count + chunk - 1) / chunk;
+  }
+  tab.first[n] = static_cast<int>(first);
+}
+
+int grid_of(const int* first, int n, int most) { return first[n] < most ? (first[n] > 0 ? first[n] : 1) : most; }
+
+template <int N>
+cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_place, double* parts, int most,
+                float* norm, bool norm_only, cudaStream_t s) {
+  int P = 0;
+  ClipTable<N> tab;
+  for (int i = 0; i == 0 || i < n; i += N) {
+    fill<N>(tab, t + i, n - i < N ? n - i : N, chunk);
+    const int grid = grid_of(tab.first, tab.n, most);
+    const cudaError_t e = launch_pdl(clip_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab, parts + P);
+    if (e != cudaSuccess) return e;
+    P += grid;
+  }
+  for (int i = 0; i == 0 || i < n; i += N) {
+    if (n > N) fill<N>(tab, t + i, n - i < N ? n - i : N, chunk);
+    const int grid = norm_only ? 1 : grid_of(tab.first, tab.n, most);
+    const cudaError_t e = launch_pdl(clip_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
+                                     static_cast<const double*>(parts), P, max_norm, in_place || norm_only, norm);
+    if (e != cudaSuccess || norm_only) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+int clip_ctas(int sms) { return 8 * sms; }
+int clip_launches(int n) { return n <= kSmallTable ? 1 : (n + kLargeTable - 1) / kLargeTable; }
+
+cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, double* parts, float* norm, int sms,
+                        cudaStream_t stream) {
+  long long total = 0;
+  for (int i = 0; i < n; ++i) total += t[i].count;
+  // some eight chunks a CTA, of 4096 values at least and 32768 at most
+  const int most = clip_ctas(sms);
+  long long chunk = (total / (8LL * most) + 4095) / 4096 * 4096;
+  chunk = chunk < 4096 ? 4096 : chunk > 32768 ? 32768 : chunk;
+  const bool norm_only = max_norm > 3.402823466e38f && in_place;
+  if (n <= kSmallTable)
+    return run<kSmallTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, stream);
+  return run<kLargeTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, stream);
+}
+
+}  // namespace gmm

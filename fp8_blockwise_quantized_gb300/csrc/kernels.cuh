@@ -167,6 +167,86 @@ __global__ void mx4_quantize_rhs_kernel(const uint16_t* w, int K, int N, uint8_t
 cudaError_t launch_gmm_mx4(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_out,
                            const Mx4Args& args, int grid, cudaStream_t stream);
 
+// ---- the layer around the experts: router, sorted rows, norms, clipping --------
+struct RouteArgs {
+  const void* logits;      // fp32 or bf16 [T][E]
+  const float* bias;       // [E] or null (forward)
+  const float* dweights;   // [T][k] (backward)
+  const int32_t* ids;      // [T][k] (backward)
+  int32_t* ids_out;        // forward
+  float* weights;          // [T][k], forward
+  void* dlogits;           // [T][E], backward
+  long long T;
+  int E, k;
+  int f32, softmax, renorm;
+  float scale;
+};
+cudaError_t launch_route(const RouteArgs& args, cudaStream_t stream);
+cudaError_t launch_route_bwd(const RouteArgs& args, cudaStream_t stream);
+
+// Device bytes that the sort of N ids needs besides its outputs (0: none).
+size_t sort_scratch_bytes(int64_t N, int G);
+cudaError_t launch_sort_rows(const int32_t* ids, int64_t N, int G, int32_t* rows, int32_t* sizes, void* scratch,
+                             cudaStream_t stream);
+// T tokens of K columns, k choices each; M = T * k sorted rows.
+cudaError_t launch_gather_rows(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* out,
+                               cudaStream_t stream);
+cudaError_t launch_gather_quantize(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, float* xs,
+                                   cudaStream_t stream);
+cudaError_t launch_combine_rows(const void* y, const int32_t* rows, const float* weights, int64_t T, int k, int64_t K,
+                                void* out, cudaStream_t stream);
+cudaError_t launch_combine_rows_bwd(const void* dout, const void* y, const int32_t* rows, const float* weights,
+                                    int64_t T, int k, int64_t K, void* dy, float* dweights, int sms,
+                                    cudaStream_t stream);
+
+struct NormJoinArgs {
+  const void* x;              // residual stream [T][K], fp32 or bf16
+  const uint16_t* b;          // the block's output, bf16 [T][K], or null
+  const float* w_post;        // [K] or null
+  const float* gate_col;      // [K] or null
+  const uint16_t* gate_full;  // bf16 [T][K] or null
+  const float* w_next;        // [K] or null
+  void* out;                  // as x; written when b is given
+  uint16_t* n;                // bf16 [T][K]; written when w_next is given
+  long long T;
+  int K, f32;
+  float alpha, beta, eps;
+};
+struct NormJoinBwdArgs {
+  const void* dout;           // as out, or null
+  const uint16_t* dn;         // bf16 [T][K] or null
+  const void* out;            // the forward's out (its x without a block); read when dn is given
+  const uint16_t* b;
+  const float* w_post;
+  const float* gate_col;
+  const uint16_t* gate_full;
+  const float* w_next;
+  void* dx;                   // as out, or null
+  uint16_t* db;               // bf16 [T][K] (with b)
+  float* dw_post;             // [K] or null
+  float* dgate_col;           // [K] or null
+  uint16_t* dgate_full;       // bf16 [T][K] (with gate_full)
+  float* dw_next;             // [K] or null
+  float* parts;               // [norm_join_parts][3][K]
+  long long T;
+  int K, f32;
+  float alpha, beta, eps;
+};
+cudaError_t launch_norm_join(const NormJoinArgs& args, int sms, cudaStream_t stream);
+int norm_join_parts(int64_t T, int64_t K, int sms);
+cudaError_t launch_norm_join_bwd(const NormJoinBwdArgs& args, int sms, cudaStream_t stream);
+
+struct ClipTensor {
+  const void* src;
+  void* dst;
+  int64_t count;
+  int f32;
+};
+int clip_ctas(int sms);     // sums of squares that a launch leaves, at most
+int clip_launches(int n);   // launches that n tensors take
+cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, double* parts, float* norm, int sms,
+                        cudaStream_t stream);
+
 // Tile geometry the host needs to build tensor maps and size grids.
 struct Fp8Geometry {
   int bn_mma;      // MMA N (columns of W per stage)

@@ -1,0 +1,218 @@
+// The router: the k experts of each token and their weights, and the gradient
+// of the logits.
+//
+// A warp takes a token and holds its E logits in registers, expert i * 32 + lane
+// in lane's word i, so that every load and store of a word is contiguous.  The
+// choice compares logit + bias as whole numbers in an order of the floats, so
+// that a round is one warp-wide maximum of 32-bit words and one minimum of the
+// ids that reach it (ties to the lower id).
+#include "common.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "rowvec.cuh"
+
+namespace gmm {
+
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr uint32_t kOrderMinusInf = 0x007fffffu;  // ordered(-inf): every number is above it
+
+// Whole numbers in the order of the floats; v is not NaN, and -0 counts as 0.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000); }
+// A logit in fp32; NaN stands for an expert that is not there.
+__device__ __forceinline__ float logit_of(const float* p) {
+  const float v = __ldg(p);
+  return v != v ? minus_inf() : v;
+}
+__device__ __forceinline__ float logit_of(const uint16_t* p) {
+  const float v = __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+  return v != v ? minus_inf() : v;
+}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(uint16_t* p, float v) {
+  *p = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xffffu);
+}
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+// The score that renorm divides by the chosen ones' sum, as its logarithm: the
+// logit itself (softmax), or log sigmoid(v), which keeps its value where the
+// sigmoid is below the smallest float.
+__device__ __forceinline__ float log_score(float v, bool softmax) {
+  return softmax ? v : fminf(v, 0.0f) - log1pf(expf(-fabsf(v)));
+}
+
+// exp(v - the warp's largest) over its sum: 0 at -inf, and everywhere when all are -inf.
+__device__ __forceinline__ float share_of(float v) {
+  const float top = warp_max(v);
+  const float e = v > minus_inf() ? expf(v - top) : 0.0f;
+  const float sum = warp_sum(e);
+  return e > 0.0f || e != e ? e / sum : 0.0f;
+}
+
+// Largest logit of the row and the sum of exp(logit - largest).
+template <int V>
+__device__ __forceinline__ void row_sum(const float (&l)[V], float* top, float* sum) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+  m = warp_max(m);
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) s += l[i] > minus_inf() ? expf(l[i] - m) : 0.0f;
+  *top = m;
+  *sum = warp_sum(s);
+}
+
+constexpr int kWarps = 4;
+
+template <typename L, int V>
+__global__ void __launch_bounds__(32 * kWarps) route_kernel(const L* __restrict__ logits,
+                                                            const float* __restrict__ bias, long long T, int E, int k,
+                                                            int softmax, int renorm, float scale,
+                                                            int32_t* __restrict__ ids, float* __restrict__ weights) {
+  griddep_launch_dependents();
+  griddep_wait();  // the logits may come from the previous kernel
+  const int lane = threadIdx.x & 31;
+  const long long t = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const L* row = logits + t * E;
+  float l[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = 32 * i + lane < E ? logit_of(row + 32 * i + lane) : minus_inf();
+  float top = 0.0f, sum = 1.0f;
+  if (softmax && !renorm) row_sum<V>(l, &top, &sum);
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float v = l[i];
+    if (bias && 32 * i + lane < E) v += __ldg(bias + 32 * i + lane);
+    key[i] = v != v ? kOrderMinusInf : ordered(v);
+  }
+  int mine = -1;  // lane j: the id of choice j
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      if (key[i] > best) best = key[i], at = i;
+    const uint32_t most = __reduce_max_sync(kAll, best);
+    if (most <= kOrderMinusInf) break;
+    const uint32_t id = __reduce_min_sync(kAll, best == most ? 32u * at + lane : ~0u);
+    if (lane == j) mine = static_cast<int>(id);
+    const int gone = lane == (id & 31u) ? static_cast<int>(id >> 5) : -1;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i == gone) key[i] = 0;
+  }
+  const float v = mine >= 0 ? logit_of(row + mine) : minus_inf();
+  float w;
+  if (renorm)
+    w = share_of(mine >= 0 ? log_score(v, softmax) : minus_inf());
+  else
+    w = mine < 0 ? 0.0f : softmax ? expf(v - top) / sum : sigmoid(v);
+  if (lane < k) {
+    ids[t * k + lane] = mine;
+    weights[t * k + lane] = scale * w;
+  }
+}
+
+template <typename L, int V>
+__global__ void __launch_bounds__(32 * kWarps) route_bwd_kernel(const float* __restrict__ dweights,
+                                                                const L* __restrict__ logits,
+                                                                const int32_t* __restrict__ ids, long long T, int E,
+                                                                int k, int softmax, int renorm, float scale,
+                                                                L* __restrict__ dlogits) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long t = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const L* row = logits + t * E;
+  int id = lane < k ? __ldg(ids + t * k + lane) : -1;
+  if (id >= E) id = -1;
+  const float g = id >= 0 ? scale * __ldg(dweights + t * k + lane) : 0.0f;
+  const float v = id >= 0 ? logit_of(row + id) : minus_inf();
+  const bool whole = softmax && !renorm;  // every expert's logit counts
+  float p[V], top, sum, total = 0.0f;
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = 32 * i + lane < E ? logit_of(row + 32 * i + lane) : minus_inf();
+    row_sum<V>(p, &top, &sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = p[i] > minus_inf() ? expf(p[i] - top) / sum : 0.0f;
+    total = warp_sum(id >= 0 && v > minus_inf() ? g * (expf(v - top) / sum) : 0.0f);
+  }
+  float d = g;  // what choice `lane` adds to its expert
+  if (renorm) {
+    const float q = share_of(id >= 0 ? log_score(v, softmax) : minus_inf());
+    d = q * (g - warp_sum(g * q));
+    if (!softmax) d *= sigmoid(-v);
+  } else if (!softmax) {
+    const float e = expf(-fabsf(v));
+    d = g * (e / ((1.0f + e) * (1.0f + e)));
+  }
+  // in the order of the choices: an expert that a token names twice gets both
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const int to = __shfl_sync(kAll, id, j);
+    const float add = __shfl_sync(kAll, d, j);
+    const int word = to >= 0 && lane == (to & 31) ? to >> 5 : -1;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i == word) acc[i] += add;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (32 * i + lane < E) put(dlogits + t * E + 32 * i + lane, whole ? p[i] * (acc[i] - total) : acc[i]);
+}
+
+template <typename F>
+cudaError_t by_words(int E, F&& launch) {
+  if (E <= 32) return launch(std::integral_constant<int, 1>());
+  if (E <= 64) return launch(std::integral_constant<int, 2>());
+  if (E <= 128) return launch(std::integral_constant<int, 4>());
+  if (E <= 256) return launch(std::integral_constant<int, 8>());
+  if (E <= 512) return launch(std::integral_constant<int, 16>());
+  if (E <= 1024) return launch(std::integral_constant<int, 32>());
+  if (E <= 2048) return launch(std::integral_constant<int, 64>());
+  return launch(std::integral_constant<int, 128>());
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((a.T + kWarps - 1) / kWarps)), block(32 * kWarps);
+  return by_words(a.E, [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    if (a.f32)
+      return launch_pdl(route_kernel<float, V>, grid, block, 0, stream, static_cast<const float*>(a.logits), a.bias, a.T,
+                        a.E, a.k, a.softmax, a.renorm, a.scale, a.ids_out, a.weights);
+    return launch_pdl(route_kernel<uint16_t, V>, grid, block, 0, stream, static_cast<const uint16_t*>(a.logits), a.bias,
+                      a.T, a.E, a.k, a.softmax, a.renorm, a.scale, a.ids_out, a.weights);
+  });
+}
+
+cudaError_t launch_route_bwd(const RouteArgs& a, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((a.T + kWarps - 1) / kWarps)), block(32 * kWarps);
+  return by_words(a.E, [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    if (a.f32)
+      return launch_pdl(route_bwd_kernel<float, V>, grid, block, 0, stream, a.dweights,
+                        static_cast<const float*>(a.logits), a.ids, a.T, a.E, a.k, a.softmax, a.renorm, a.scale,
+                        static_cast<float*>(a.dlogits));
+    return launch_pdl(route_bwd_kernel<uint16_t, V>, grid, block, 0, stream, a.dweights,
+                      static_cast<const uint16_t*>(a.logits), a.ids, a.T, a.E, a.k, a.softmax, a.renorm, a.scale,
+                      static_cast<uint16_t*>(a.dlogits));
+  });
+}
+
+}  // namespace gmm

@@ -1,0 +1,412 @@
+// Rows sorted by expert and joined again: the places of a batch's choices among
+// the sorted rows, x's rows at their places, and the weighted sums back.
+#include "common.cuh"
+#include "kernels.cuh"
+#include "metadata.cuh"
+#include "ptx.cuh"
+#include "rowvec.cuh"
+
+namespace gmm {
+
+namespace {
+
+// ---- places -------------------------------------------------------------------
+// A stable counting sort of N ids into G + 1 bins, the last for the ids outside
+// 0 .. G - 1.  A CTA takes a chunk of consecutive ids, each of its warps a run of
+// the chunk; within a warp, the lanes with one id find each other with a match,
+// and the warp's count of that id so far gives their places in the run.  The
+// places' bases are the ids before in the chunk (summed over the warps), in the
+// chunks before (a table that a first kernel fills) and in the bins before.
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDirectChunks = 64;  // so many rows of the table each CTA sums itself
+
+__device__ __forceinline__ int bin_of(int id, int G) { return static_cast<unsigned>(id) < static_cast<unsigned>(G) ? id : G; }
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int32_t* __restrict__ ids, int N, int G,
+                                                                  int chunk, int32_t* __restrict__ table) {
+  extern __shared__ int hist[];
+  griddep_launch_dependents();
+  const int B = G + 1;
+  for (int b = threadIdx.x; b < B; b += kSortThreads) hist[b] = 0;
+  __syncthreads();
+  griddep_wait();  // the ids may come from the previous kernel
+  const long long first = static_cast<long long>(blockIdx.x) * chunk;
+  const int n = static_cast<int>(min(static_cast<long long>(chunk), N - first));
+  for (int i = threadIdx.x; i < n; i += kSortThreads) atomicAdd(hist + bin_of(__ldg(ids + first + i), G), 1);
+  __syncthreads();
+  for (int b = threadIdx.x; b < B; b += kSortThreads) table[static_cast<long long>(blockIdx.x) * B + b] = hist[b];
+}
+
+// Many chunks: the table's columns as sums of the rows before, and their totals behind the last row.
+__global__ void __launch_bounds__(64) sort_scan_kernel(int32_t* __restrict__ table, int B, int chunks) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int b = blockIdx.x * 64 + threadIdx.x;
+  if (b >= B) return;
+  int run = 0;
+  int32_t* p = table + b;
+#pragma unroll 8
+  for (int c = 0; c < chunks; ++c, p += B) {
+    const int v = *p;
+    *p = run;
+    run += v;
+  }
+  *p = run;
+}
+
+template <int R>
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t* __restrict__ ids, int N, int G,
+                                                                  int chunks, const int32_t* __restrict__ table,
+                                                                  int32_t* __restrict__ rows,
+                                                                  int32_t* __restrict__ sizes) {
+  extern __shared__ int smem[];
+  __shared__ int warp_sums[kSortWarps];
+  const int B = G + 1, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  int* base = smem;                                           // [B]
+  uint16_t* runs = reinterpret_cast<uint16_t*>(smem + B);     // [kSortWarps][B]; a chunk has at most 8192 ids
+  uint16_t* mine = runs + warp * B;
+  griddep_launch_dependents();
+  for (int b = t; b < kSortWarps * B; b += kSortThreads) runs[b] = 0;
+  __syncthreads();
+  griddep_wait();
+  const long long first = static_cast<long long>(blockIdx.x) * (kSortThreads * R) + warp * (32 * R) + lane;
+  int bin[R], rank[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) bin[r] = first + 32 * r < N ? bin_of(__ldg(ids + first + 32 * r), G) : -1;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const unsigned peers = __match_any_sync(0xffffffffu, bin[r]);
+    const int before = __popc(peers & ((1u << lane) - 1u));
+    const int so_far = bin[r] >= 0 ? mine[bin[r]] : 0;
+    __syncwarp();
+    if (before == 0 && bin[r] >= 0) mine[bin[r]] = static_cast<uint16_t>(so_far + __popc(peers));
+    __syncwarp();
+    rank[r] = so_far + before;
+  }
+  __syncthreads();
+  // per bin: the warps' counts as sums of those before, the chunks before, all chunks
+  const int per = (B + kSortThreads - 1) / kSortThreads, b0 = min(B, t * per), b1 = min(B, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    int run = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int c = runs[w * B + b];
+      runs[w * B + b] = static_cast<uint16_t>(run);
+      run += c;
+    }
+    int earlier = 0, total = run;
+    if (chunks > kDirectChunks) {
+      earlier = table[static_cast<long long>(blockIdx.x) * B + b];
+      total = table[static_cast<long long>(chunks) * B + b];
+    } else if (chunks > 1) {
+      total = 0;
+#pragma unroll 8
+      for (int c = 0; c < chunks; ++c) {
+        const int v = table[c * B + b];
+        if (c < static_cast<int>(blockIdx.x)) earlier += v;
+        total += v;
+      }
+    }
+    if (blockIdx.x == 0 && b < G) sizes[b] = total;
+    base[b] = sum + earlier;
+    sum += total;
+  }
+  const int inc = warp_inclusive_scan(sum);
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int start = inc - sum;
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) start += w < warp ? warp_sums[w] : 0;
+  for (int b = b0; b < b1; ++b) base[b] += start;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (bin[r] < 0) continue;
+    const int row = base[bin[r]] + mine[bin[r]] + rank[r];
+    rows[first + 32 * r] = bin[r] < G ? row : -1 - row;
+  }
+}
+
+// ---- x by token -> sorted rows --------------------------------------------------
+// The place of a choice, or -1 where rows holds what no sort gives.
+__device__ __forceinline__ long long place_of(int row, long long M) {
+  const long long p = row >= 0 ? row : -1LL - row;
+  return p < M ? p : -1;
+}
+
+// A thread takes 8 values of a token and writes them to the token's k places.
+template <typename I>
+__global__ void __launch_bounds__(256) gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ rows,
+                                                     I vectors, int k, unsigned KV, long long M,
+                                                     uint4* __restrict__ out) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const I v = static_cast<I>(blockIdx.x) * 256 + threadIdx.x;
+  if (v >= vectors) return;
+  const I t = v / KV;
+  const unsigned c = static_cast<unsigned>(v - t * KV);
+  const uint4 val = __ldcs(x + v);
+  const int32_t* at = rows + static_cast<long long>(t) * k;
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int row = __ldg(at + j);
+    const long long p = place_of(row, M);
+    if (p >= 0) out[p * KV + c] = row >= 0 ? val : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// The same with the 1x128 e4m3 quantisation of gmm_quantize_lhs in between: each
+// token is quantised once, whatever its number of places.  Eight lanes take a
+// block of 128 values.
+template <typename I>
+__global__ void __launch_bounds__(256) gather_quantize_kernel(const uint4* __restrict__ x,
+                                                              const int32_t* __restrict__ rows, I units, int k,
+                                                              unsigned KB, long long M, uint4* __restrict__ xq,
+                                                              float* __restrict__ xs) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const I v = static_cast<I>(blockIdx.x) * 256 + threadIdx.x;
+  const I u = v >> 3;
+  const unsigned l8 = threadIdx.x & 7;
+  const bool live = u < units;
+  const I t = u / KB;
+  const unsigned kb = static_cast<unsigned>(u - t * KB);
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  if (live) {
+    a = __ldcs(x + 2 * static_cast<long long>(v));
+    b = __ldcs(x + 2 * static_cast<long long>(v) + 1);
+  }
+  float m = fmaxf(bf16x8_absmax(a), bf16x8_absmax(b));
+#pragma unroll
+  for (int d = 4; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (!live) return;
+  float s, inv;
+  e4m3_block_scale(m, s, inv);
+  const uint2 qa = bf16x8_to_e4m3(a, inv), qb = bf16x8_to_e4m3(b, inv);
+  const uint4 q = make_uint4(qa.x, qa.y, qb.x, qb.y);
+  const int32_t* at = rows + static_cast<long long>(t) * k;
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int row = __ldg(at + j);
+    const long long p = place_of(row, M);
+    if (p < 0) continue;
+    xq[(p * KB + kb) * 8 + l8] = row >= 0 ? q : make_uint4(0, 0, 0, 0);
+    if (l8 == (j & 7)) xs[kb * M + p] = row >= 0 ? s : 0.0f;
+  }
+}
+
+// ---- sorted rows -> tokens --------------------------------------------------------
+// A thread sums 8 columns of a token over its choices, in their order.
+template <typename I>
+__global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ y, const int32_t* __restrict__ rows,
+                                                      const float* __restrict__ weights, I vectors, int k, unsigned KV,
+                                                      long long M, uint4* __restrict__ out) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const I v = static_cast<I>(blockIdx.x) * 256 + threadIdx.x;
+  if (v >= vectors) return;
+  const I t = v / KV;
+  const unsigned c = static_cast<unsigned>(v - t * KV);
+  const long long e0 = static_cast<long long>(t) * k;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    uint4 val[4];
+    float w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = j0 + j < k ? __ldg(rows + e0 + j0 + j) : -1;
+      const bool live = row >= 0 && row < M;
+      w[j] = live ? (weights ? __ldg(weights + e0 + j0 + j) : 1.0f) : 0.0f;
+      // a row of no group adds nothing, whatever its weight holds
+      val[j] = live ? __ldcs(y + static_cast<long long>(row) * KV + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[8];
+      unpack8(val[j], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+    }
+  }
+  out[v] = pack8(acc);
+}
+
+// The gradient: dy = weight * dout at each place (zero at those of no group), and
+// the weight's gradient, the product of dout's row and y's.  A group of `span`
+// warps takes a token, so that the products' sums stay in registers; dout's row is
+// read once for 8 choices.
+constexpr int kBwdWarps = 8;
+__global__ void __launch_bounds__(32 * kBwdWarps) combine_bwd_kernel(const uint4* __restrict__ dout,
+                                                                     const uint4* __restrict__ y,
+                                                                     const int32_t* __restrict__ rows,
+                                                                     const float* __restrict__ weights, long long T,
+                                                                     int k, unsigned KV, int span,
+                                                                     uint4* __restrict__ dy,
+                                                                     float* __restrict__ dweights) {
+  __shared__ float part[kBwdWarps][8];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / span, in = warp - team * span;
+  const long long t = static_cast<long long>(blockIdx.x) * (kBwdWarps / span) + team, M = T * k;
+  const long long e0 = t * k;
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    const int many = min(8, k - j0);
+    float dot[8], w[8];
+    int row[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dot[j] = w[j] = 0.0f;
+      row[j] = INT32_MIN;
+      if (t < T && j < many) {
+        row[j] = __ldg(rows + e0 + j0 + j);
+        w[j] = row[j] >= 0 ? __ldg(weights + e0 + j0 + j) : 0.0f;
+      }
+    }
+    if (t < T) {
+      for (unsigned c = in * 32 + lane; c < KV; c += span * 32) {
+        float d[8];
+        unpack8(__ldg(dout + t * KV + c), d);
+        uint4 val[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          val[j] = row[j] >= 0 && row[j] < M ? __ldcs(y + static_cast<long long>(row[j]) * KV + c)
+                                             : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j >= many) break;
+          float f[8], o[8];
+          unpack8(val[j], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot[j] = fmaf(d[i], f[i], dot[j]);
+            o[i] = w[j] * d[i];
+          }
+          const long long p = place_of(row[j], M);
+          if (p >= 0) dy[p * KV + c] = row[j] >= 0 ? pack8(o) : make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dot[j] = warp_sum(dot[j]);
+    if (span > 1) {
+      __syncthreads();  // the previous choices' sums have been read
+      if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[warp][j] = dot[j];
+      }
+      __syncthreads();
+      if (in == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          for (int s = 1; s < span; ++s) dot[j] += part[warp + s][j];
+      }
+    }
+    if (t < T && in == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (lane == j && j < many) dweights[e0 + j0 + j] = row[j] >= 0 ? dot[j] : 0.0f;
+    }
+  }
+}
+
+constexpr long long kNarrow = 1LL << 31;  // indices below it are 32 bits
+
+unsigned blocks_of(long long threads) { return static_cast<unsigned>((threads + 255) / 256); }
+
+int sort_chunk(int64_t N) { return N <= 512 ? 512 : N <= 131072 ? 2048 : 8192; }
+// one CTA's chunk may hold all
+int sort_chunks(int64_t N) { return N <= 8192 ? 1 : static_cast<int>((N + sort_chunk(N) - 1) / sort_chunk(N)); }
+
+}  // namespace
+
+size_t sort_scratch_bytes(int64_t N, int G) {
+  const int chunks = sort_chunks(N);
+  return chunks > 1 ? static_cast<size_t>(chunks + 1) * (G + 1) * sizeof(int32_t) : 0;
+}
+
+cudaError_t launch_sort_rows(const int32_t* ids, int64_t N, int G, int32_t* rows, int32_t* sizes, void* scratch,
+                             cudaStream_t stream) {
+  const int B = G + 1, n = static_cast<int>(N), chunks = sort_chunks(N);
+  int32_t* table = static_cast<int32_t*>(scratch);
+  cudaError_t e;
+  if (chunks > 1) {
+    e = launch_pdl(sort_count_kernel, dim3(chunks), dim3(kSortThreads), B * sizeof(int), stream, ids, n, G,
+                   sort_chunk(N), table);
+    if (e != cudaSuccess) return e;
+    if (chunks > kDirectChunks &&
+        (e = launch_pdl(sort_scan_kernel, dim3((B + 63) / 64), dim3(64), 0, stream, table, B, chunks)) != cudaSuccess)
+      return e;
+  }
+  const int smem = B * sizeof(int) + kSortWarps * B * sizeof(uint16_t);
+  static std::atomic<uint64_t> done1, done4, done16;
+  auto place = [&](auto kernel, std::atomic<uint64_t>& done) {
+    if (smem > 40 * 1024) {
+      const cudaError_t err = allow_smem(kernel, kSortWarps * (kMaxGroups + 1) * 2 + (kMaxGroups + 1) * 4, done);
+      if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(kernel, dim3(chunks), dim3(kSortThreads), smem, stream, ids, n, G, chunks,
+                      static_cast<const int32_t*>(table), rows, sizes);
+  };
+  const int per_cta = chunks > 1 ? sort_chunk(N) : n;
+  if (per_cta <= 512) return place(sort_place_kernel<1>, done1);
+  if (per_cta <= 2048) return place(sort_place_kernel<4>, done4);
+  return place(sort_place_kernel<16>, done16);
+}
+
+cudaError_t launch_gather_rows(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* out,
+                               cudaStream_t stream) {
+  const long long vectors = T * (K / 8), M = T * k;
+  const unsigned KV = static_cast<unsigned>(K / 8);
+  if (vectors < kNarrow)
+    return launch_pdl(gather_kernel<uint32_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
+                      static_cast<const uint4*>(x), rows, static_cast<uint32_t>(vectors), k, KV, M,
+                      static_cast<uint4*>(out));
+  return launch_pdl(gather_kernel<uint64_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
+                    static_cast<const uint4*>(x), rows, static_cast<uint64_t>(vectors), k, KV, M,
+                    static_cast<uint4*>(out));
+}
+
+cudaError_t launch_gather_quantize(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, float* xs,
+                                   cudaStream_t stream) {
+  const long long units = T * (K / 128), M = T * k;
+  const unsigned KB = static_cast<unsigned>(K / 128);
+  if (units < kNarrow / 8)
+    return launch_pdl(gather_quantize_kernel<uint32_t>, dim3(blocks_of(units * 8)), dim3(256), 0, stream,
+                      static_cast<const uint4*>(x), rows, static_cast<uint32_t>(units), k, KB, M,
+                      static_cast<uint4*>(xq), xs);
+  return launch_pdl(gather_quantize_kernel<uint64_t>, dim3(blocks_of(units * 8)), dim3(256), 0, stream,
+                    static_cast<const uint4*>(x), rows, static_cast<uint64_t>(units), k, KB, M,
+                    static_cast<uint4*>(xq), xs);
+}
+
+cudaError_t launch_combine_rows(const void* y, const int32_t* rows, const float* weights, int64_t T, int k, int64_t K,
+                                void* out, cudaStream_t stream) {
+  const long long vectors = T * (K / 8), M = T * k;
+  const unsigned KV = static_cast<unsigned>(K / 8);
+  if (vectors < kNarrow)
+    return launch_pdl(combine_kernel<uint32_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
+                      static_cast<const uint4*>(y), rows, weights, static_cast<uint32_t>(vectors), k, KV, M,
+                      static_cast<uint4*>(out));
+  return launch_pdl(combine_kernel<uint64_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
+                    static_cast<const uint4*>(y), rows, weights, static_cast<uint64_t>(vectors), k, KV, M,
+                    static_cast<uint4*>(out));
+}
+
+cudaError_t launch_combine_rows_bwd(const void* dout, const void* y, const int32_t* rows, const float* weights,
+                                    int64_t T, int k, int64_t K, void* dy, float* dweights, int sms,
+                                    cudaStream_t stream) {
+  // a warp a token once that gives every SM 16 warps; more of them for few tokens
+  int span = 1;
+  while (span < kBwdWarps && T * span < 16LL * sms && span * 256 < K) span *= 2;
+  const long long per = kBwdWarps / span;
+  return launch_pdl(combine_bwd_kernel, dim3(static_cast<unsigned>((T + per - 1) / per)), dim3(32 * kBwdWarps), 0,
+                    stream, static_cast<const uint4*>(dout), static_cast<const uint4*>(y), rows, weights,
+                    static_cast<long long>(T), k, static_cast<unsigned>(K / 8), span, static_cast<uint4*>(dy), dweights);
+}
+
+}  // namespace gmm

@@ -30,8 +30,9 @@
  *   - On GMM_ERR_CUDA (and the host-side errors that name a cause),
  *     gmm_last_cuda_error() gives the calling thread's last message.
  *   - Row-major layouts; bf16 = IEEE bfloat16; e4m3 = OCP FP8 E4M3 (max 448).
- *   - K and N are multiples of 128 (the quantization block); 1 <= G <= 4096;
- *     0 <= M < 2^31.  M = 0, or every group empty, is valid.
+ *   - K and N are multiples of 128 (the quantization block), unless a call says
+ *     otherwise; 1 <= G <= 4096; 0 <= M < 2^31.  M = 0, or every group empty, is
+ *     valid.
  *   - The grouped calls first derive the group metadata (offsets, row tiles)
  *     from group_sizes into the workspace.  group_sizes = NULL skips that step
  *     and reuses the metadata already in the workspace: written by
@@ -438,6 +439,144 @@ gmm_status gmm_mx4_fwd(const void* xq, const void* xs, const void* wq, const voi
 gmm_status gmm_mx4_fwd_swiglu_quant(const void* xq, const void* xs, const void* wq, const void* ws,
                                     const int32_t* group_sizes, int G, int64_t M, int64_t K, int64_t N, void* h,
                                     void* hq, void* hs, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * What surrounds the experts in an MoE layer ("MoE 优化的探索" §1: router,
+ * dispatch, experts, combine; the pages print no formula of a router or a norm).
+ * These calls take T tokens (0 <= T), E experts (1 .. 4096) and k choices a token
+ * (1 .. 32, T * k < 2^31); K is a multiple of 8 (of 128 where rows are quantised) up
+ * to 2^24 (8192 for the norms); T * k = M is the number of sorted rows.  They need
+ * no workspace.  Element types are given as
+ */
+typedef enum { GMM_BF16 = 0, GMM_F32 = 1 } gmm_type;
+
+/*
+ * The router: each token's k experts and their weights.
+ *   key[e] = logits[t,e] + bias[e] in fp32 (bias NULL: 0); a NaN logit counts as
+ *   -inf.  The choices are the k largest keys above -inf, in falling order, ties
+ *   to the lower id; where there are fewer, ids is -1 and the weight 0.
+ *   score GMM_SOFTMAX: weight = scale * exp(l - m) / sum_e exp(l_e - m) over all E
+ *   logits (without the bias), or with renorm over the chosen ones;
+ *   score GMM_SIGMOID: weight = scale / (1 + exp(-l)), with renorm divided by the
+ *   chosen ones' sum (of the sigmoids).
+ *   logits  fp32 or bf16 [T, E];  bias  fp32 [E] or NULL
+ *   ids     int32 [T, k];  weights  fp32 [T, k]
+ * GMM_ERR_SHAPE also when k > E.
+ */
+typedef enum { GMM_SOFTMAX = 0, GMM_SIGMOID = 1 } gmm_score;
+gmm_status gmm_route(const void* logits, gmm_type logits_type, const float* bias, int64_t T, int E, int k,
+                     gmm_score score, int renorm, float scale, int32_t* ids, float* weights, void* stream);
+
+/*
+ * Its gradient with the choice held fixed: dlogits of the weights' formula above,
+ * from dweights fp32 [T, k].  An id outside 0 .. E - 1 adds nothing; an expert that
+ * a token names twice gets both gradients.
+ *   logits, dlogits  fp32 or bf16 [T, E];  ids  int32 [T, k]
+ */
+gmm_status gmm_route_bwd(const float* dweights, const void* logits, gmm_type logits_type, const int32_t* ids, int64_t T,
+                         int E, int k, gmm_score score, int renorm, float scale, void* dlogits, void* stream);
+
+/*
+ * Places of N choices among the rows sorted by expert (the layout every grouped
+ * call takes): group g holds the choices of expert g, in their order.
+ *   ids    int32 [N]; an id outside 0 .. G - 1 belongs to no group
+ *   rows   int32 [N]: the row of each choice, or -1 - r for a choice of no group, r
+ *          being its row behind the groups: S <= r < N, in the choices' order
+ *   group_sizes  int32 [G]
+ *   scratch  gmm_sort_rows_scratch_bytes(N, G) bytes, or NULL where that is 0; its
+ *          contents do not matter, before or after
+ */
+size_t gmm_sort_rows_scratch_bytes(int64_t N, int G);
+gmm_status gmm_sort_rows(const int32_t* ids, int64_t N, int G, int32_t* rows, int32_t* group_sizes, void* scratch,
+                         size_t scratch_bytes, void* stream);
+
+/*
+ * The tokens' rows at the places of their choices: out[rows[t,j]] = x[t], and
+ * zeros at the places of no group (-1 - rows[t,j]).  With rows from gmm_sort_rows
+ * every row of out is written.  A value of rows that names no row of out is skipped.
+ *   x  bf16 [T, K];  rows  int32 [T, k];  out  bf16 [T k, K]
+ * It is the gradient of gmm_combine_rows without weights, too.
+ */
+gmm_status gmm_gather_rows(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* out, void* stream);
+
+/*
+ * gmm_quantize_lhs of gmm_gather_rows' result, bit for bit, each token quantised
+ * once: the operands of gmm_fp8_fwd, or the checkpoint that tgmm_fp8_ckpt takes.
+ *   xq  e4m3 [T k, K];  xs  fp32 [K/128, T k];  K a multiple of 128
+ */
+gmm_status gmm_gather_quantize(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, float* xs,
+                               void* stream);
+
+/*
+ * The sorted rows joined by token:
+ *   out[t] = bf16( sum_j weights[t,j] * y[rows[t,j]] ),  fp32, j rising;
+ * weights NULL: 1 each (the gradient of gmm_gather_rows).  A choice of no group adds
+ * nothing, whatever its weight and row hold.
+ *   y  bf16 [T k, K];  rows  int32 [T, k];  weights  fp32 [T, k];  out  bf16 [T, K]
+ */
+gmm_status gmm_combine_rows(const void* y, const int32_t* rows, const float* weights, int64_t T, int k, int64_t K,
+                            void* out, void* stream);
+
+/*
+ * Its gradient:
+ *   dy[rows[t,j]] = bf16( weights[t,j] * dout[t] ), zeros at the places of no group;
+ *   dweights[t,j] = sum_c dout[t,c] * y[rows[t,j],c] in fp32, 0 for a choice of no group.
+ *   dout  bf16 [T, K];  y, dy  bf16 [T k, K];  dweights  fp32 [T, k]
+ */
+gmm_status gmm_combine_rows_bwd(const void* dout, const void* y, const int32_t* rows, const float* weights, int64_t T,
+                                int k, int64_t K, void* dy, float* dweights, void* stream);
+
+/*
+ * The norms before and after a block, joined with its gate and the residual stream:
+ *   z   = b / sqrt(mean_c(b^2) + eps) * w_post        (w_post NULL: z = b)
+ *   out = residual_scale * x + block_scale * gate * z  (gate NULL: 1)
+ *   n   = bf16( out / sqrt(mean_c(out^2) + eps) * w_next ),  out not yet rounded
+ * b NULL: out = x, nothing is written to it, and n is the norm in front of a first
+ * block (w_post and gate are then NULL).  w_next NULL: no n.
+ *   x, out  bf16 or fp32 (stream_type) [T, K];  b, n  bf16 [T, K]
+ *   w_post, w_next  fp32 [K]
+ *   gate    gate_rows = 0: fp32 [K], one value per column; gate_rows = 1: bf16 [T, K]
+ * out may be x; n may be b.  eps >= 0.
+ */
+gmm_status gmm_norm_join(const void* x, gmm_type stream_type, const void* b, const float* w_post, const void* gate,
+                         int gate_rows, const float* w_next, int64_t T, int64_t K, float residual_scale,
+                         float block_scale, float eps, void* out, void* n, void* stream);
+
+/*
+ * Its gradient, from dout (of out; NULL: zero) and dn (of n; NULL: zero):
+ *   D = dout + the norm's gradient of dn;  dx = residual_scale * D (b NULL: D)
+ *   db, and by column sums over the tokens (fp32) dw_post, dw_next and a column
+ *   gate's dgate; for gate_rows = 1, dgate is bf16 [T, K].
+ *   out  the forward's out (b NULL: its x), read when dn is given
+ * dx may be NULL, and any of dw_post, dgate (gate_rows = 0), dw_next; what is not
+ * NULL is written (dw_next as zeros without dn).  dx may be dout, db may be dn or b.
+ *   scratch  gmm_norm_join_bwd_scratch_bytes(T, K) bytes; its contents do not matter
+ */
+size_t gmm_norm_join_bwd_scratch_bytes(int64_t T, int64_t K);
+gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, gmm_type stream_type, const void* b,
+                             const float* w_post, const void* gate, int gate_rows, const float* w_next, int64_t T,
+                             int64_t K, float residual_scale, float block_scale, float eps, void* dx, void* db,
+                             float* dw_post, void* dgate, float* dw_next, void* scratch, size_t scratch_bytes,
+                             void* stream);
+
+/*
+ * Gradients scaled to a largest global norm:
+ *   norm = sqrt( sum over all tensors and elements of g^2 ),
+ *   out  = g * (max_norm / norm) where norm > max_norm, else g.
+ * A norm that is not finite scales nothing (the caller sees it in `norm`).  The
+ * squares are summed so that no finite gradients overflow or vanish in them.
+ * max_norm = +infinity with out = NULL computes the norm only.
+ *   grads, out  HOST arrays of n device pointers, aligned to their elements (not to
+ *            16 bytes; those that are not go a slower way); out NULL: in place.  A
+ *            pointer with count 0 may be NULL.  n may be 0 (norm 0).
+ *   counts   HOST array: elements of each tensor;  types  HOST array of gmm_type
+ *   norm     fp32 [1], device
+ *   scratch  gmm_clip_grads_scratch_bytes(n) bytes; its contents do not matter
+ * The host arrays are read before the call returns.
+ */
+size_t gmm_clip_grads_scratch_bytes(int n);
+gmm_status gmm_clip_grads(const void* const* grads, void* const* out, const int64_t* counts, const int32_t* types,
+                          int n, float max_norm, float* norm, void* scratch, size_t scratch_bytes, void* stream);
 
 /*
  * gmm_fp8_fwd without a workspace argument, for callers that cannot allocate
