@@ -184,7 +184,7 @@ gmm_status gmm_norm_join(const void* x, gmm_type stream_type, const void* b, con
   a.T = T;
   a.K = static_cast<int>(K);
   a.f32 = stream_type == GMM_F32;
-  a.alpha = residual_scale;
+  a.alpha = b ? residual_scale : 1.0f;
   a.beta = block_scale;
   a.eps = eps;
   return launched(launch_norm_join(a, sms, static_cast<cudaStream_t>(stream)), "norm_join_kernel launch");
@@ -195,7 +195,7 @@ size_t gmm_norm_join_bwd_scratch_bytes(int64_t T, int64_t K) {
   if (T < 0 || T > INT32_MAX || check_columns(K, 8) != GMM_OK || K > kMaxNormColumns ||
       host_device_sms(&sms) != GMM_OK)
     return 0;
-  return static_cast<size_t>(norm_join_parts(T, K, sms)) * 3 * K * sizeof(float);
+  return static_cast<size_t>(norm_join_parts(T, K, sms)) * 2 * K * sizeof(float);
 }
 
 gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, gmm_type stream_type, const void* b,
@@ -211,7 +211,7 @@ gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, 
     return GMM_ERR_ALIGN;
   int sms = 0;
   if ((st = host_device_sms(&sms)) != GMM_OK) return st;
-  const size_t need = static_cast<size_t>(norm_join_parts(T, K, sms)) * 3 * K * sizeof(float);
+  const size_t need = static_cast<size_t>(norm_join_parts(T, K, sms)) * 2 * K * sizeof(float);
   if (need && (!scratch || scratch_bytes < need)) return GMM_ERR_WORKSPACE;
   NormJoinBwdArgs a{};
   a.dout = dout;

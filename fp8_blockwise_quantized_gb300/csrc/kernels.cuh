@@ -210,6 +210,7 @@ struct NormJoinArgs {
   uint16_t* n;                // bf16 [T][K]; written when w_next is given
   long long T;
   int K, f32;
+  int row_threads;            // set by the launcher
   float alpha, beta, eps;
 };
 struct NormJoinBwdArgs {
@@ -227,9 +228,10 @@ struct NormJoinBwdArgs {
   float* dgate_col;           // [K] or null
   uint16_t* dgate_full;       // bf16 [T][K] (with gate_full)
   float* dw_next;             // [K] or null
-  float* parts;               // [norm_join_parts][3][K]
+  float* parts;               // [norm_join_parts][2][K]
   long long T;
   int K, f32;
+  int row_threads;            // set by the launcher
   float alpha, beta, eps;
 };
 cudaError_t launch_norm_join(const NormJoinArgs& args, int sms, cudaStream_t stream);

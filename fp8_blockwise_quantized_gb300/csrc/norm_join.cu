@@ -5,10 +5,20 @@
 //   out = alpha x + beta gate z
 //   n = out * ro * w_next,  ro = 1 / sqrt(mean(out^2) + eps)
 //
-// A CTA takes a row at a time, a thread the same 8 columns of every row, so that the
-// sums of the parameters' gradients over the rows stay in its registers, and up to
-// 4096 columns (512 threads of 128 registers) the parameters too.  n is rounded
-// once, from out before its rounding.
+// A thread takes the same columns of every row it takes, so that what is constant in a
+// column (beta, w_post, a gate per column: one factor) and the sums of the parameters'
+// gradients over the rows stay in its registers.  n is rounded once, from out before
+// its rounding.
+//
+// Bound by HBM, with the instructions close behind: two columns an instruction, sums
+// of two values for five exchanges, loads without predicates.  At 8192 x 2048 (floor
+// at the measured copy rate in brackets): forward 20.9 us (20.1) with a bf16 stream,
+// 33.5 (30.2) with an fp32 stream and a gate per column; backward 39.4 (30.2) and 52.6
+// (45.2), 8 of them the sums over the rows.  The next row's values are on their way to
+// registers while a row is worked on: through shared memory (asynchronous copies, two
+// to six rows ahead) they pass the SM's load path twice, and the same calls took 22.0,
+// 40.2, 42.1 and 71.4 us; rows asked for in the L2 further ahead, 22.6 to 25.6 and
+// 36.0 to 40.8 us forward.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -18,287 +28,485 @@ namespace gmm {
 
 namespace {
 
-// Sum over the CTA of two values; red: two buffers in turn, so that one barrier a sum is enough.
-__device__ __forceinline__ float2 block_sum2(float a, float b, float2 (*red)[32], int& turn, int warps) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (warps == 1) return make_float2(a, b);
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) red[turn][threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  const float2 v = lane < warps ? red[turn][lane] : make_float2(0.0f, 0.0f);
-  turn ^= 1;
-  return make_float2(warp_sum(v.x), warp_sum(v.y));
-}
-
-__device__ __forceinline__ float inv_rms(float squares, int K, float eps) {
-  return 1.0f / sqrtf(squares / static_cast<float>(K) + eps);
-}
-
-// A thread's 8 values of a parameter: from its registers, or where a CTA of NT
-// threads has no room for them, from the cache for each row.
-template <bool HELD>
-struct Param {
-  const float* at = nullptr;
-  float v[HELD ? 8 : 1];
-  __device__ __forceinline__ void set(const float* p, int col) {
-    if (!p) return;
-    at = p + col;
-    if constexpr (HELD) load_params8(at, v);
-  }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    if constexpr (HELD) {
+// 8 columns, and arithmetic on pairs of them (one instruction a pair).
+struct Cols {
+  float2 v[4];
+  __device__ __forceinline__ static Cols of(float f) {
+    Cols c;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = v[e];
-    } else {
-      load_params8(at, f);
-    }
+    for (int i = 0; i < 4; ++i) c.v[i] = make_float2(f, f);
+    return c;
   }
 };
-constexpr int kHeldThreads = 512;
+__device__ __forceinline__ Cols operator*(const Cols& a, const Cols& b) {
+  Cols c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+  return c;
+}
+__device__ __forceinline__ Cols operator*(const Cols& a, float f) {
+  Cols c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c.v[i] = __fmul2_rn(a.v[i], make_float2(f, f));
+  return c;
+}
+__device__ __forceinline__ Cols fma8(const Cols& a, const Cols& b, const Cols& c) {
+  Cols r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
+  return r;
+}
+__device__ __forceinline__ Cols fma8(const Cols& a, float f, const Cols& c) {
+  Cols r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], make_float2(f, f), c.v[i]);
+  return r;
+}
+// sum of a * b over the 8 columns
+__device__ __forceinline__ float dot8(const Cols& a, const Cols& b) {
+  float2 s = __fmul2_rn(a.v[0], b.v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = __ffma2_rn(a.v[i], b.v[i], s);
+  return s.x + s.y;
+}
+__device__ __forceinline__ Cols cols_of(const float4& a, const float4& b) {
+  Cols c;
+  c.v[0] = make_float2(a.x, a.y), c.v[1] = make_float2(a.z, a.w);
+  c.v[2] = make_float2(b.x, b.y), c.v[3] = make_float2(b.z, b.w);
+  return c;
+}
+__device__ __forceinline__ Cols cols_of(const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  Cols c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return c;
+}
 
-template <typename S, int NT>
-__global__ void __launch_bounds__(NT) norm_join_kernel(NormJoinArgs a) {
-  __shared__ float2 red[2][32];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int warps = blockDim.x >> 5, col = 8 * threadIdx.x;
-  const bool on = col < a.K;
-  int turn = 0;
-  Param<NT <= kHeldThreads> wp, wn, gc;
-  if (on) {
-    wp.set(a.w_post, col);
-    wn.set(a.w_next, col);
-    gc.set(a.gate_col, col);
+// Where a thread stands: its row among the CTA's, its columns, its row's warps.
+struct Place {
+  int team, rows, col, warps, warp;
+  __device__ __forceinline__ explicit Place(int row_threads) {
+    team = threadIdx.x / row_threads;
+    rows = blockDim.x / row_threads;
+    const int in_row = threadIdx.x - team * row_threads;
+    col = 8 * in_row;
+    warp = in_row >> 5;
+    warps = row_threads >> 5;
   }
-  const S* x = static_cast<const S*>(a.x);
-  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const long long at = t * a.K + col;
-    typename RawOf<S>::type rx;
-    Raw8Bf16 rb, rg;
-    if (on) {
-      rx.load(x + at);
-      if (a.b) rb.load(a.b + at);
-      if (a.gate_full) rg.load(a.gate_full + at);
+};
+
+// N sums (1 or 2) over a row's threads.  Of two, neighbours 16 lanes apart exchange one
+// each, so that the lower half of a warp goes on with the first and the upper half with
+// the second.  The warps' sums lie in 32 words a row, 32 / N a value; every warp adds
+// them up, a lane a word.  red: two buffers in turn, so that one barrier is enough;
+// zeros where no warp writes.
+constexpr int kMaxTeams = 8;
+using SumBuffer = float[2][kMaxTeams + 1][32];
+template <int N>
+struct Sums {
+  float (*red)[kMaxTeams + 1][32];
+  int turn = 0;
+  __device__ __forceinline__ void operator()(float (&s)[N], const Place& p) {
+    constexpr int kSpan = 32 / N;
+    const int lane = threadIdx.x & 31;
+    float v = s[0];
+    if constexpr (N == 2) {
+      const bool up = lane & 16;
+      v = (up ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, up ? s[0] : s[1], 16);
     }
-    float o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = 0.0f;
-    if (on) rx.get(o);
+    for (int d = kSpan / 2; d >= 1; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (p.warps > 1) {
+      float* row = red[turn][p.team];
+      if ((lane & (kSpan - 1)) == 0) row[lane + p.warp] = v;
+      __syncthreads();
+      turn ^= 1;
+      v = row[lane];
+      if (p.warps > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
+      if (p.warps > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xffffffffu, v, kSpan * i);
+  }
+};
+// Zeros for a kernel's buffers.
+__device__ __forceinline__ void clear(SumBuffer& red) {
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / sizeof(float)); i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+  __syncthreads();
+}
+
+// Eight columns as they lie in memory.
+template <typename S>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ Cols get() const { return cols_of(v); }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ Cols get() const { return cols_of(a, b); }
+};
+__device__ __forceinline__ void put8(uint16_t* p, const Cols& c) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(c.v[0].x, c.v[0].y), pack_bf16x2(c.v[1].x, c.v[1].y),
+                                            pack_bf16x2(c.v[2].x, c.v[2].y), pack_bf16x2(c.v[3].x, c.v[3].y));
+}
+__device__ __forceinline__ void put8(float* p, const Cols& c) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(c.v[0].x, c.v[0].y, c.v[1].x, c.v[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(c.v[2].x, c.v[2].y, c.v[3].x, c.v[3].y);
+}
+
+// factor * p * q of 8 columns (a null pointer counts as 1).
+__device__ __forceinline__ Cols factors8(const float* p, const float* q, float factor, int col) {
+  Cols c = Cols::of(factor);
+  if (p) c = c * cols_of(__ldg(reinterpret_cast<const float4*>(p + col)), __ldg(reinterpret_cast<const float4*>(p + col) + 1));
+  if (q) c = c * cols_of(__ldg(reinterpret_cast<const float4*>(q + col)), __ldg(reinterpret_cast<const float4*>(q + col) + 1));
+  return c;
+}
+
+// rsqrt is within 2 units of the last place.
+__device__ __forceinline__ float inv_rms(float squares, float inv_k, float eps) { return rsqrtf(fmaf(squares, inv_k, eps)); }
+
+// V vectors of 8 columns a thread, at most NT threads a CTA.  A thread without columns
+// reads those of others and adds nothing; the row ahead of the last is the last again.
+template <typename S, int V, int NT, bool FULL>
+__global__ void __launch_bounds__(NT, 512 / NT) norm_join_kernel(NormJoinArgs a) {
+  __shared__ SumBuffer red;
+  griddep_launch_dependents();
+  clear(red);
+  const Place me(a.row_threads);
+  griddep_wait();
+  const long long step = static_cast<long long>(gridDim.x) * me.rows;
+  const float inv_k = 1.0f / static_cast<float>(a.K);
+  bool on[V];
+  int col[V];
+  Cols pw[V], wn[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    col[v] = me.col + 8 * a.row_threads * v;
+    on[v] = me.team < me.rows && col[v] < a.K;
+    if (!on[v]) col[v] = 0;
+    pw[v] = factors8(a.w_post, a.gate_col, a.beta, col[v]);
+    wn[v] = factors8(a.w_next, nullptr, 1.0f, col[v]);
+  }
+  Raw<S> x[V];
+  Raw<uint16_t> b[V], g[V];
+  auto fetch = [&](long long t) {
+    const long long at = (t < a.T ? t : a.T - 1) * a.K;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v].load(static_cast<const S*>(a.x) + at + col[v]);
+      if (a.b) b[v].load(a.b + at + col[v]);
+      if (FULL) g[v].load(a.gate_full + at + col[v]);
+    }
+  };
+  long long t = static_cast<long long>(blockIdx.x) * me.rows + me.team;
+  fetch(t);
+  Sums<1> sums{red};
+  for (long long t0 = t - me.team; t0 < a.T; t0 += step, t += step) {
+    const long long at = t * a.K;
+    Cols o[V], z[V];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = x[v].get() * a.alpha;
     if (a.b) {
-      float z[8], w[8], scale = 1.0f;
+      float r = 1.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = 0.0f;
-      if (on) rb.get(z);
+      for (int v = 0; v < V; ++v) {
+        z[v] = b[v].get();
+        if (on[v]) s[0] += dot8(z[v], z[v]);
+        z[v] = z[v] * pw[v];
+        if (FULL) z[v] = z[v] * g[v].get();
+      }
+      fetch(t + step);
       if (a.w_post) {
-        float sq = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sq = fmaf(z[e], z[e], sq);
-        scale = inv_rms(block_sum2(sq, 0.0f, red, turn, warps).x, a.K, a.eps);
+        sums(s, me);
+        r = inv_rms(s[0], inv_k, a.eps);
       }
-      if (on) {
-        if (a.w_post) {
-          wp.get(w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = z[e] * scale * w[e];
-        }
-        if (a.gate_full || a.gate_col) {
-          if (a.gate_full) rg.get(w); else gc.get(w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] *= w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = fmaf(a.beta, z[e], a.alpha * o[e]);
-        store8(static_cast<S*>(a.out) + at, o);
+      for (int v = 0; v < V; ++v) {
+        o[v] = fma8(z[v], r, o[v]);
+        if (on[v] && t < a.T) put8(static_cast<S*>(a.out) + at + col[v], o[v]);
       }
+    } else {
+      fetch(t + step);
     }
     if (a.w_next) {
-      float sq = 0.0f;
+      s[0] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sq = fmaf(o[e], o[e], sq);
-      const float scale = inv_rms(block_sum2(sq, 0.0f, red, turn, warps).x, a.K, a.eps);
-      if (on) {
-        float w[8];
-        wn.get(w);
+      for (int v = 0; v < V; ++v)
+        if (on[v]) s[0] += dot8(o[v], o[v]);
+      sums(s, me);
+      const float r = inv_rms(s[0], inv_k, a.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = o[e] * scale * w[e];
-        store8(a.n + at, o);
-      }
+      for (int v = 0; v < V; ++v)
+        if (on[v] && t < a.T) put8(a.n + at + col[v], o[v] * r * wn[v]);
     }
   }
 }
 
-// With c = dn * w_next, D = dout + ro c - out ro^3 / K sum(c out); dx = alpha D,
-// u = beta D, dgate = u z, and b's gradient from dz = u gate by the same rule.
-// A part of the parameters' gradients a CTA, joined by norm_join_reduce_kernel.
-template <typename S, int NT>
-__global__ void __launch_bounds__(NT) norm_join_bwd_kernel(NormJoinBwdArgs a) {
-  __shared__ float2 red[2][32];
+// With c = dn * w_next, D = dout + ro c - out ro^3 / K sum(c out); dx = alpha D.
+// With p = beta * w_post * gate, b's gradient is that of its norm from t = D p:
+// db = rb t - b rb^3 / K sum(t b).  With s = sum over the rows of D b rb (times a
+// gate per element), dw_post = beta gate s and a column gate's gradient beta w_post s:
+// one sum for both, a part of it a CTA row (and of dw_next's), joined by
+// norm_join_reduce_kernel.
+// A row of an input on its way to the L2, asked for by one thread.
+__device__ __forceinline__ void row_to_l2(const void* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// V = 2 (over 4096 columns): the registers hold the sums, but neither the factors,
+// which come from the cache for each row, nor the row ahead.
+template <typename S, int V, int NT, bool FULL>
+__global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwdArgs a) {
+  constexpr bool kHeld = V == 1;
+  __shared__ SumBuffer red;
   griddep_launch_dependents();
+  clear(red);
+  const Place me(a.row_threads);
   griddep_wait();
-  const int warps = blockDim.x >> 5, col = 8 * threadIdx.x;
-  const bool on = col < a.K;
-  int turn = 0;
-  Param<NT <= kHeldThreads> wp, wn, gc;
-  if (on) {
-    wp.set(a.w_post, col);
-    wn.set(a.w_next, col);
-    gc.set(a.gate_col, col);
-  }
-  float sp[8], sn[8], sg[8];
+  const long long step = static_cast<long long>(gridDim.x) * me.rows;
+  const float inv_k = 1.0f / static_cast<float>(a.K);
+  bool on[V];
+  int col[V];
+  Cols held_p, held_n, sb[V], sn[V];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sp[e] = sn[e] = sg[e] = 0.0f;
-  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const long long at = t * a.K + col;
-    typename RawOf<S>::type ro, rd;
-    Raw8Bf16 rb, rn, rg;
-    if (on) {
-      if (a.dout) rd.load(static_cast<const S*>(a.dout) + at);
+  for (int v = 0; v < V; ++v) {
+    col[v] = me.col + 8 * a.row_threads * v;
+    on[v] = me.team < me.rows && col[v] < a.K;
+    if (!on[v]) col[v] = 0;
+    sb[v] = sn[v] = Cols::of(0.0f);
+  }
+  if constexpr (kHeld) {
+    held_p = factors8(a.w_post, a.gate_col, a.beta, col[0]);
+    held_n = factors8(a.w_next, nullptr, 1.0f, col[0]);
+  }
+  auto post = [&](int v) { return kHeld ? held_p : factors8(a.w_post, a.gate_col, a.beta, col[v]); };
+  auto next = [&](int v) { return kHeld ? held_n : factors8(a.w_next, nullptr, 1.0f, col[v]); };
+  Raw<S> rd[V], ro[V];
+  Raw<uint16_t> rn[V], rb[V], rg[V];
+  auto fetch = [&](long long t) {
+    const long long row = (t < a.T ? t : a.T - 1) * a.K;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const long long at = row + col[v];
+      if (a.dout) rd[v].load(static_cast<const S*>(a.dout) + at);
       if (a.dn) {
-        rn.load(a.dn + at);
-        ro.load(static_cast<const S*>(a.out) + at);
+        rn[v].load(a.dn + at);
+        ro[v].load(static_cast<const S*>(a.out) + at);
       }
-      if (a.b) rb.load(a.b + at);
-      if (a.gate_full) rg.load(a.gate_full + at);
+      if (a.b) rb[v].load(a.b + at);
+      if (FULL) rg[v].load(a.gate_full + at);
     }
-    float d[8], f[8], w[8];
+  };
 #pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] = 0.0f;
-    if (on && a.dout) rd.get(d);
+  for (int v = 0; v < V; ++v) rd[v].zero();
+  long long t = static_cast<long long>(blockIdx.x) * me.rows + me.team;
+  if (kHeld) fetch(t);
+  Sums<2> sums{red};
+  for (long long t0 = t - me.team; t0 < a.T; t0 += step, t += step) {
+    const long long row = t * a.K;
+    if (!kHeld) {
+      fetch(t);
+      if (threadIdx.x == 0 && t + step < a.T) {
+        const long long at = row + step * a.K;
+        const int wide = a.K * static_cast<int>(sizeof(S)), narrow = 2 * a.K;
+        if (a.dout) row_to_l2(static_cast<const S*>(a.dout) + at, wide);
+        if (a.dn) {
+          row_to_l2(a.dn + at, narrow);
+          row_to_l2(static_cast<const S*>(a.out) + at, wide);
+        }
+        if (a.b) row_to_l2(a.b + at, narrow);
+        if (FULL) row_to_l2(a.gate_full + at, narrow);
+      }
+    }
+    Cols c_[V], o_[V], f_[V], d[V], g_[V];
+    if (kHeld) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        c_[v] = rn[v].get(), o_[v] = ro[v].get(), f_[v] = rb[v].get(), d[v] = rd[v].get();
+        if (FULL) g_[v] = rg[v].get();
+      }
+      fetch(t + step);
+    }
+    auto c = [&](int v) { return kHeld ? c_[v] : rn[v].get(); };
+    auto o = [&](int v) { return kHeld ? o_[v] : ro[v].get(); };
+    auto f = [&](int v) { return kHeld ? f_[v] : rb[v].get(); };
+    auto g = [&](int v) { return kHeld ? g_[v] : rg[v].get(); };
+    float s[2];
     if (a.dn) {
-      float c[8], sq = 0.0f, dot = 0.0f;
-      if (on) {
-        ro.get(f);
-        rn.get(c);
-        wn.get(w);
+      s[0] = s[1] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sq = fmaf(f[e], f[e], sq);
-          dot = fmaf(c[e] * w[e], f[e], dot);
+      for (int v = 0; v < V; ++v)
+        if (on[v]) {
+          s[0] += dot8(o(v), o(v));
+          s[1] += dot8(next(v), c(v) * o(v));
         }
-      }
-      const float2 s = block_sum2(sq, dot, red, turn, warps);
-      const float r = inv_rms(s.x, a.K, a.eps), q = s.y * r * r / static_cast<float>(a.K);
-      if (on) {
+      sums(s, me);
+      const float r = inv_rms(s[0], inv_k, a.eps), q = s[1] * r * r * r * inv_k;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sn[e] = fmaf(c[e], f[e] * r, sn[e]);
-          d[e] = fmaf(r, fmaf(c[e], w[e], -f[e] * q), d[e]);
+      for (int v = 0; v < V; ++v) {
+        if (on[v] && t < a.T) sn[v] = fma8(c(v) * o(v), r, sn[v]);
+        d[v] = fma8(c(v) * next(v), r, fma8(o(v), -q, kHeld ? d[v] : rd[v].get()));
+      }
+    } else if (!kHeld) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = rd[v].get();
+    }
+    if (a.dx) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (on[v] && t < a.T) put8(static_cast<S*>(a.dx) + row + col[v], d[v] * a.alpha);
+    }
+    if (a.b) {
+      float r = 1.0f, q = 0.0f;
+      if (a.w_post) {
+        s[0] = s[1] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (on[v]) {
+            s[0] += dot8(f(v), f(v));
+            s[1] += dot8(FULL ? post(v) * g(v) : post(v), d[v] * f(v));
+          }
+        sums(s, me);
+        r = inv_rms(s[0], inv_k, a.eps);
+        q = s[1] * r * r * r * inv_k;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (!on[v] || t >= a.T) continue;
+        Cols e = d[v] * post(v), df = d[v] * f(v);
+        if (FULL) {
+          put8(a.dgate_full + row + col[v], df * r * post(v));
+          df = df * g(v);
+          e = e * g(v);
         }
+        sb[v] = fma8(df, r, sb[v]);
+        put8(a.db + row + col[v], fma8(e, r, f(v) * -q));
       }
-    }
-    if (on && a.dx) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = a.alpha * d[e];
-      store8(static_cast<S*>(a.dx) + at, f);
-    }
-    if (!a.b) continue;
-    // from here d is u = beta D
-    float g[8], r = 1.0f, q = 0.0f, sq = 0.0f, dot = 0.0f;
-    if (on) {
-      rb.get(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[e] *= a.beta;
-        g[e] = w[e] = 1.0f;
-      }
-      if (a.gate_full) rg.get(g);
-      if (a.gate_col) gc.get(g);
-      if (a.w_post) wp.get(w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sq = fmaf(f[e], f[e], sq);
-        dot = fmaf(d[e] * g[e] * w[e], f[e], dot);
-      }
-    }
-    if (a.w_post) {
-      const float2 s = block_sum2(sq, dot, red, turn, warps);
-      r = inv_rms(s.x, a.K, a.eps);
-      q = s.y * r * r / static_cast<float>(a.K);
-    }
-    if (on) {
-      float dg[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float unit = f[e] * r, dz = d[e] * g[e];  // unit: b over its root mean square, or b without w_post
-        dg[e] = d[e] * (unit * w[e]);
-        sg[e] += dg[e];
-        sp[e] = fmaf(dz, unit, sp[e]);
-        f[e] = r * fmaf(dz, w[e], -f[e] * q);
-      }
-      store8(a.db + at, f);
-      if (a.gate_full) store8(a.dgate_full + at, dg);
     }
   }
-  if (!on) return;
-  float* p = a.parts + static_cast<long long>(blockIdx.x) * 3 * a.K + col;
-  if (a.dw_post) store8(p, sp);
-  if (a.dgate_col) store8(p + a.K, sg);
-  if (a.dw_next) store8(p + 2 * a.K, sn);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (!on[v]) continue;
+    float* p = a.parts + (static_cast<long long>(blockIdx.x) * me.rows + me.team) * 2 * a.K + col[v];
+    if (a.dw_post || a.dgate_col) put8(p, sb[v]);
+    if (a.dw_next) put8(p + a.K, sn[v]);
+  }
 }
 
-// Sums the CTAs' parts of one parameter's gradient, in their order: 32 columns a
-// CTA, 16 warps with every 16th part each.
-__global__ void __launch_bounds__(512) norm_join_reduce_kernel(const float* __restrict__ parts, int P, int K,
-                                                               float* dw_post, float* dgate, float* dw_next) {
-  __shared__ float sums[16][33];
+// Sums the parts in their order and gives the parameters' gradients: 8 columns a CTA,
+// 32 threads a column with every 32nd part each, a warp a column for what they have.
+__global__ void __launch_bounds__(256) norm_join_reduce_kernel(const float* __restrict__ parts, int P, int K, float beta,
+                                                               const float* w_post, const float* gate, float* dw_post,
+                                                               float* dgate, float* dw_next) {
+  __shared__ float sums[32][9];
   griddep_launch_dependents();
   griddep_wait();
-  float* out = blockIdx.y == 0 ? dw_post : blockIdx.y == 1 ? dgate : dw_next;
-  if (!out) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  const bool next = blockIdx.y == 1;
+  if (next ? !dw_next : !dw_post && !dgate) return;
+  const int c = threadIdx.x & 7, group = threadIdx.x >> 3;
+  const float* p = parts + static_cast<long long>(blockIdx.y) * K + blockIdx.x * 8 + c;
   float s = 0.0f;
-  if (col < K) {
-    const float* p = parts + static_cast<long long>(blockIdx.y) * K + col;
-#pragma unroll 8
-    for (int c = warp; c < P; c += 16) s += p[static_cast<long long>(c) * 3 * K];
-  }
-  sums[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && col < K) {
-    float total = 0.0f;
+  for (int i = group; i < P; i += 32 * 10) {
+    float v[10];  // all on their way at once: up to 320 parts in one round
 #pragma unroll
-    for (int w = 0; w < 16; ++w) total += sums[w][lane];
-    out[col] = total;
+    for (int j = 0; j < 10; ++j) v[j] = i + 32 * j < P ? p[static_cast<long long>(i + 32 * j) * 2 * K] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 10; ++j) s += v[j];
+  }
+  sums[group][c] = s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 8 + warp;
+  float g = 1.0f, w = 1.0f;
+  if (!next && dw_post && gate) g = gate[col];
+  if (!next && dgate && w_post) w = w_post[col];
+  __syncthreads();
+  const float total = warp_sum(sums[lane][warp]);
+  if (lane != 0) return;
+  if (next) {
+    dw_next[col] = total;
+  } else {
+    if (dw_post) dw_post[col] = beta * total * g;
+    if (dgate) dgate[col] = beta * total * w;
   }
 }
 
-int row_threads(int64_t K) { return static_cast<int>((K / 8 + 31) / 32 * 32); }
+// How T rows of K columns are laid out: `vectors` of 8 columns a thread, 512 threads an
+// SM (128 registers each).
+struct Shape {
+  int row_threads, threads, teams, grid;
+  Shape(int64_t T, int64_t K, int vectors, int sms) {
+    const int64_t each = 8 * 32 * vectors;  // columns of a warp
+    row_threads = static_cast<int>((K + each - 1) / each * 32);
+    threads = row_threads <= 256 ? 256 : 512;
+    teams = threads / row_threads;
+    const long long need = (T + teams - 1) / teams, room = static_cast<long long>(sms) * (512 / threads);
+    grid = static_cast<int>(need < room ? need : room);
+  }
+};
+
+// Vectors a thread.  The backward pass holds more for each: two only where one would
+// take over 512 threads.
+constexpr int kForward = 2;
+int backward_vectors(int64_t K) { return K > 8 * 512 ? 2 : 1; }
+
+template <typename S, bool FULL>
+cudaError_t forward(const NormJoinArgs& a, const Shape& sh, cudaStream_t stream) {
+  return sh.threads == 256
+             ? launch_pdl(norm_join_kernel<S, kForward, 256, FULL>, dim3(sh.grid), dim3(256), 0, stream, a)
+             : launch_pdl(norm_join_kernel<S, kForward, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
+}
+template <typename S, bool FULL>
+cudaError_t backward(const NormJoinBwdArgs& a, const Shape& sh, cudaStream_t stream) {
+  if (backward_vectors(a.K) == 2)
+    return launch_pdl(norm_join_bwd_kernel<S, 2, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
+  return sh.threads == 256
+             ? launch_pdl(norm_join_bwd_kernel<S, 1, 256, FULL>, dim3(sh.grid), dim3(256), 0, stream, a)
+             : launch_pdl(norm_join_bwd_kernel<S, 1, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
+}
 
 }  // namespace
 
-cudaError_t launch_norm_join(const NormJoinArgs& a, int sms, cudaStream_t stream) {
-  const int threads = row_threads(a.K);
-  const long long most = static_cast<long long>(sms) * (2048 / threads > 32 ? 32 : 2048 / threads);
-  const dim3 grid(static_cast<unsigned>(a.T < most ? a.T : most)), block(threads);
-  if (threads <= kHeldThreads)
-    return a.f32 ? launch_pdl(norm_join_kernel<float, kHeldThreads>, grid, block, 0, stream, a)
-                 : launch_pdl(norm_join_kernel<uint16_t, kHeldThreads>, grid, block, 0, stream, a);
-  return a.f32 ? launch_pdl(norm_join_kernel<float, 1024>, grid, block, 0, stream, a)
-               : launch_pdl(norm_join_kernel<uint16_t, 1024>, grid, block, 0, stream, a);
-}
-
 int norm_join_parts(int64_t T, int64_t K, int sms) {
-  const int threads = row_threads(K);
-  const long long most = static_cast<long long>(sms) * (threads > 512 ? 1 : 512 / threads);
-  return static_cast<int>(T < most ? T : most);
+  const Shape sh(T, K, backward_vectors(K), sms);
+  return sh.grid * sh.teams;
 }
 
-cudaError_t launch_norm_join_bwd(const NormJoinBwdArgs& a, int sms, cudaStream_t stream) {
-  const int threads = row_threads(a.K), parts = norm_join_parts(a.T, a.K, sms);
-  const dim3 grid(parts), block(threads);
+cudaError_t launch_norm_join(const NormJoinArgs& args, int sms, cudaStream_t stream) {
+  NormJoinArgs a = args;
+  const Shape sh(a.T, a.K, kForward, sms);
+  a.row_threads = sh.row_threads;
+  if (a.gate_full) return a.f32 ? forward<float, true>(a, sh, stream) : forward<uint16_t, true>(a, sh, stream);
+  return a.f32 ? forward<float, false>(a, sh, stream) : forward<uint16_t, false>(a, sh, stream);
+}
+
+cudaError_t launch_norm_join_bwd(const NormJoinBwdArgs& args, int sms, cudaStream_t stream) {
+  NormJoinBwdArgs a = args;
+  const Shape sh(a.T, a.K, backward_vectors(a.K), sms);
+  a.row_threads = sh.row_threads;
   cudaError_t e = cudaSuccess;
-  if (parts > 0) {
-    if (threads <= kHeldThreads)
-      e = a.f32 ? launch_pdl(norm_join_bwd_kernel<float, kHeldThreads>, grid, block, 0, stream, a)
-                : launch_pdl(norm_join_bwd_kernel<uint16_t, kHeldThreads>, grid, block, 0, stream, a);
+  if (a.T > 0) {
+    if (a.gate_full)
+      e = a.f32 ? backward<float, true>(a, sh, stream) : backward<uint16_t, true>(a, sh, stream);
     else
-      e = a.f32 ? launch_pdl(norm_join_bwd_kernel<float, 1024>, grid, block, 0, stream, a)
-                : launch_pdl(norm_join_bwd_kernel<uint16_t, 1024>, grid, block, 0, stream, a);
+      e = a.f32 ? backward<float, false>(a, sh, stream) : backward<uint16_t, false>(a, sh, stream);
   }
   if (e != cudaSuccess || !(a.dw_post || a.dgate_col || a.dw_next)) return e;
-  return launch_pdl(norm_join_reduce_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32), 3), dim3(512), 0, stream,
-                    static_cast<const float*>(a.parts), parts, static_cast<int>(a.K), a.dw_post, a.dgate_col, a.dw_next);
+  return launch_pdl(norm_join_reduce_kernel, dim3(static_cast<unsigned>(a.K / 8), 2), dim3(256), 0, stream,
+                    static_cast<const float*>(a.parts), sh.grid * sh.teams, static_cast<int>(a.K), a.beta, a.w_post,
+                    a.gate_col, a.dw_post, a.dgate_col, a.dw_next);
 }
 
 }  // namespace gmm
