@@ -970,26 +970,59 @@ def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
 # around the experts: router, sorted rows, norms, clipping
 # ---------------------------------------------------------------------------
 
+# These calls are short (a few microseconds of device time for a decoding step), so
+# their wrappers look at each operand once and hand the library plain numbers.
+
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_empty = torch.empty_strided
+_current_device = torch._C._cuda_getDevice
+_data_ptr, _is_contiguous, _get_device = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
 
 
 def _type_of(what, t):
     """gmm_type of a tensor that may be bf16 or fp32."""
-    if t.dtype is torch.bfloat16:
+    dtype = t.dtype
+    if dtype is _BF16:
         return 0
-    if t.dtype is torch.float32:
+    if dtype is _F32:
         return 1
-    raise ValueError(f"{what}: expected bfloat16 or float32 elements, got {t.dtype}")
+    raise ValueError(f"{what}: expected bfloat16 or float32 elements, got {dtype}")
 
 
 def _score_of(score):
-    if score not in _SCORES:
+    how = _SCORES.get(score)
+    if how is None:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
-    return _SCORES[score]
+    return how
 
 
-def _new1(a, dtype, device):
-    return torch.empty_strided((a,), (1,), dtype=dtype, device=device)
+def _want(what, t, on, dtype, shape):
+    """_need for one exact shape (a tuple)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != on:
+        _refuse(what, t, on, dtype, shape)
+
+
+def _refuse(what, t, on, dtype, shape):
+    where = "" if on < 0 else f" on cuda:{on}"
+    raise ValueError(f"{what}: expected a contiguous CUDA tensor of {'x'.join(map(str, shape))} {dtype} elements{where}, "
+                     f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _first(what, t, dtype):
+    """Checks a call's first tensor, whose shape and device the others have to fit; returns its device."""
+    on = t.get_device()
+    if on < 0 or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(what, t, on, dtype, t.shape)
+    return on
+
+
+def _handle(on, stream):
+    """The raw stream of a launch on device `on`, which has to be the current one."""
+    dev = _current_device()
+    if dev != on:
+        raise ValueError(f"the tensors are on cuda:{on}, the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(on) if stream is None else _s(stream)
 
 
 def route(logits, top_k, bias=None, score="softmax", renorm=False, scale=1.0, stream=None, out=None):
@@ -1003,19 +1036,25 @@ def route(logits, top_k, bias=None, score="softmax", renorm=False, scale=1.0, st
         with other:
             return route(logits, top_k, bias, score, renorm, scale, stream, out)
     T, E = logits.shape
-    kind, how, on = _type_of("logits", logits), _score_of(score), logits.get_device()
-    _need("logits", logits, on, logits.dtype, T, E)
-    _here(on)
+    kind, how = _type_of("logits", logits), _score_of(score)
+    on = _first("logits", logits, logits.dtype)
     if bias is not None:
-        _need("bias", bias, on, torch.float32, E)
-    if out is not None:
-        ids, weights = out
-        _need("out ids", ids, on, torch.int32, T, top_k)
-        _need("out weights", weights, on, torch.float32, T, top_k)
+        _want("bias", bias, on, _F32, (E,))
+    handle = _handle(on, stream)
+    if out is None:
+        if top_k < 1:
+            raise ValueError(f"top_k must be at least 1, got {top_k}")
+        device = logits.device
+        ids = _empty((T, top_k), (top_k, 1), dtype=_I32, device=device)
+        weights = _empty((T, top_k), (top_k, 1), dtype=_F32, device=device)
     else:
-        ids = _new2(T, top_k, torch.int32, logits.device)
-        weights = _new2(T, top_k, torch.float32, logits.device)
-    _check(gmm_route(logits, kind, bias, T, E, top_k, how, renorm, scale, ids, weights, stream), "gmm_route")
+        ids, weights = out
+        _want("out ids", ids, on, _I32, (T, top_k))
+        _want("out weights", weights, on, _F32, (T, top_k))
+    status = (_lib or load()).gmm_route(logits.data_ptr(), kind, None if bias is None else bias.data_ptr(), T, E, top_k,
+                                        how, bool(renorm), scale, ids.data_ptr(), weights.data_ptr(), handle)
+    if status:
+        raise GmmError(status, "gmm_route")
     return ids, weights
 
 
@@ -1026,18 +1065,21 @@ def route_bwd(dweights, logits, ids, score="softmax", renorm=False, scale=1.0, s
         with other:
             return route_bwd(dweights, logits, ids, score, renorm, scale, stream, out)
     T, E = logits.shape
-    T2, k = ids.shape
-    assert T2 == T
-    kind, how, on = _type_of("logits", logits), _score_of(score), logits.get_device()
-    _need("logits", logits, on, logits.dtype, T, E)
-    _here(on)
-    _need("ids", ids, on, torch.int32, T, k)
-    _need("dweights", dweights, on, torch.float32, T, k)
-    if out is not None:
-        _need("out", out, on, logits.dtype, T, E)
+    k = ids.shape[-1]
+    dtype = logits.dtype
+    kind, how = _type_of("logits", logits), _score_of(score)
+    on = _first("logits", logits, dtype)
+    _want("ids", ids, on, _I32, (T, k))
+    _want("dweights", dweights, on, _F32, (T, k))
+    handle = _handle(on, stream)
+    if out is None:
+        out = _empty((T, E), (E, 1), dtype=dtype, device=logits.device)
     else:
-        out = _new2(T, E, logits.dtype, logits.device)
-    _check(gmm_route_bwd(dweights, logits, kind, ids, T, E, k, how, renorm, scale, out, stream), "gmm_route_bwd")
+        _want("out", out, on, dtype, (T, E))
+    status = (_lib or load()).gmm_route_bwd(dweights.data_ptr(), logits.data_ptr(), kind, ids.data_ptr(), T, E, k, how,
+                                            bool(renorm), scale, out.data_ptr(), handle)
+    if status:
+        raise GmmError(status, "gmm_route_bwd")
     return out
 
 
@@ -1050,26 +1092,26 @@ def sort_rows(ids, G, stream=None, out=None):
     if stream is not None and (other := _other(stream)):
         with other:
             return sort_rows(ids, G, stream, out)
-    N, on = ids.numel(), ids.get_device()
-    _need("ids", ids, on, torch.int32, N)
-    _here(on)
-    if out is not None:
-        rows, sizes = out
-        _need("out rows", rows, on, torch.int32, *ids.shape)
-        _need("out group_sizes", sizes, on, torch.int32, G)
+    on, shape, N = _first("ids", ids, _I32), ids.shape, ids.numel()
+    handle = _handle(on, stream)
+    if out is None:
+        if G < 1:
+            raise ValueError(f"G must be at least 1, got {G}")
+        device = ids.device
+        rows = _empty(shape, ids.stride(), dtype=_I32, device=device)
+        sizes = _empty((G,), (1,), dtype=_I32, device=device)
     else:
-        rows = torch.empty_strided(ids.shape, ids.stride(), dtype=torch.int32, device=ids.device)
-        sizes = _new1(G, torch.int32, ids.device)
-    nbytes = gmm_sort_rows_scratch_bytes(N, G)
-    scratch = _new1(nbytes, torch.uint8, ids.device) if nbytes else None
-    _check(gmm_sort_rows(ids, N, G, rows, sizes, scratch, nbytes, stream), "gmm_sort_rows")
+        rows, sizes = out
+        _want("out rows", rows, on, _I32, shape)
+        _want("out group_sizes", sizes, on, _I32, (G,))
+    lib = _lib or load()
+    nbytes = lib.gmm_sort_rows_scratch_bytes(N, G)
+    scratch = _empty((nbytes,), (1,), dtype=torch.uint8, device=ids.device) if nbytes else None
+    status = lib.gmm_sort_rows(ids.data_ptr(), N, G, rows.data_ptr(), sizes.data_ptr(),
+                               None if scratch is None else scratch.data_ptr(), nbytes, handle)
+    if status:
+        raise GmmError(status, "gmm_sort_rows")
     return rows, sizes
-
-
-def _need_rows(rows, on):
-    T, k = rows.shape
-    _need("rows", rows, on, torch.int32, T, k)
-    return T, k
 
 
 def gather_rows(x, rows, stream=None, out=None):
@@ -1078,17 +1120,18 @@ def gather_rows(x, rows, stream=None, out=None):
     if stream is not None and (other := _other(stream)):
         with other:
             return gather_rows(x, rows, stream, out)
-    on = x.get_device()
-    T, k = _need_rows(rows, on)
-    T2, K = x.shape
-    assert T2 == T
-    _need("x", x, on, torch.bfloat16, T, K)
-    _here(on)
-    if out is not None:
-        _need("out", out, on, torch.bfloat16, T * k, K)
+    T, K = x.shape
+    k = rows.shape[-1]
+    on = _first("x", x, _BF16)
+    _want("rows", rows, on, _I32, (T, k))
+    handle = _handle(on, stream)
+    if out is None:
+        out = _empty((T * k, K), (K, 1), dtype=_BF16, device=x.device)
     else:
-        out = _new2(T * k, K, torch.bfloat16, x.device)
-    _check(gmm_gather_rows(x, rows, T, k, K, out, stream), "gmm_gather_rows")
+        _want("out", out, on, _BF16, (T * k, K))
+    status = (_lib or load()).gmm_gather_rows(x.data_ptr(), rows.data_ptr(), T, k, K, out.data_ptr(), handle)
+    if status:
+        raise GmmError(status, "gmm_gather_rows")
     return out
 
 
@@ -1098,20 +1141,23 @@ def gather_quantize(x, rows, stream=None, out=None):
     if stream is not None and (other := _other(stream)):
         with other:
             return gather_quantize(x, rows, stream, out)
-    on = x.get_device()
-    T, k = _need_rows(rows, on)
-    T2, K = x.shape
-    assert T2 == T
-    _need("x", x, on, torch.bfloat16, T, K)
-    _here(on)
-    if out is not None:
-        xq, xs = out
-        _need("out codes", xq, on, torch.uint8, T * k, K)
-        _need("out scales", xs, on, torch.float32, K // 128, T * k)
+    T, K = x.shape
+    k = rows.shape[-1]
+    on, M = _first("x", x, _BF16), T * k
+    _want("rows", rows, on, _I32, (T, k))
+    handle = _handle(on, stream)
+    if out is None:
+        device = x.device
+        xq = _empty((M, K), (K, 1), dtype=torch.uint8, device=device)
+        xs = _empty((K // 128, M), (M, 1), dtype=_F32, device=device)
     else:
-        xq = _new2(T * k, K, torch.uint8, x.device)
-        xs = _new2(K // 128, T * k, torch.float32, x.device)
-    _check(gmm_gather_quantize(x, rows, T, k, K, xq, xs, stream), "gmm_gather_quantize")
+        xq, xs = out
+        _want("out codes", xq, on, torch.uint8, (M, K))
+        _want("out scales", xs, on, _F32, (K // 128, M))
+    status = (_lib or load()).gmm_gather_quantize(x.data_ptr(), rows.data_ptr(), T, k, K, xq.data_ptr(), xs.data_ptr(),
+                                                  handle)
+    if status:
+        raise GmmError(status, "gmm_gather_quantize")
     return xq, xs
 
 
@@ -1121,18 +1167,22 @@ def combine_rows(y, rows, weights=None, stream=None, out=None):
     if stream is not None and (other := _other(stream)):
         with other:
             return combine_rows(y, rows, weights, stream, out)
-    on = y.get_device()
-    T, k = _need_rows(rows, on)
-    K = y.shape[1]
-    _need("y", y, on, torch.bfloat16, T * k, K)
-    _here(on)
+    T, k = rows.shape
+    K = y.shape[-1]
+    on = _first("rows", rows, _I32)
+    _want("y", y, on, _BF16, (T * k, K))
     if weights is not None:
-        _need("weights", weights, on, torch.float32, T, k)
-    if out is not None:
-        _need("out", out, on, torch.bfloat16, T, K)
+        _want("weights", weights, on, _F32, (T, k))
+    handle = _handle(on, stream)
+    if out is None:
+        out = _empty((T, K), (K, 1), dtype=_BF16, device=y.device)
     else:
-        out = _new2(T, K, torch.bfloat16, y.device)
-    _check(gmm_combine_rows(y, rows, weights, T, k, K, out, stream), "gmm_combine_rows")
+        _want("out", out, on, _BF16, (T, K))
+    status = (_lib or load()).gmm_combine_rows(y.data_ptr(), rows.data_ptr(),
+                                               None if weights is None else weights.data_ptr(), T, k, K, out.data_ptr(),
+                                               handle)
+    if status:
+        raise GmmError(status, "gmm_combine_rows")
     return out
 
 
@@ -1142,42 +1192,49 @@ def combine_rows_bwd(dout, y, rows, weights, stream=None, out=None):
     if stream is not None and (other := _other(stream)):
         with other:
             return combine_rows_bwd(dout, y, rows, weights, stream, out)
-    on = dout.get_device()
-    T, k = _need_rows(rows, on)
-    T2, K = dout.shape
-    assert T2 == T
-    _need("dout", dout, on, torch.bfloat16, T, K)
-    _here(on)
-    _need("y", y, on, torch.bfloat16, T * k, K)
-    _need("weights", weights, on, torch.float32, T, k)
-    if out is not None:
-        dy, dweights = out
-        _need("out dy", dy, on, torch.bfloat16, T * k, K)
-        _need("out dweights", dweights, on, torch.float32, T, k)
+    T, K = dout.shape
+    k = rows.shape[-1]
+    on, M = _first("dout", dout, _BF16), T * k
+    _want("y", y, on, _BF16, (M, K))
+    _want("rows", rows, on, _I32, (T, k))
+    _want("weights", weights, on, _F32, (T, k))
+    handle = _handle(on, stream)
+    if out is None:
+        device = dout.device
+        dy = _empty((M, K), (K, 1), dtype=_BF16, device=device)
+        dweights = _empty((T, k), (k, 1), dtype=_F32, device=device)
     else:
-        dy = _new2(T * k, K, torch.bfloat16, dout.device)
-        dweights = _new2(T, k, torch.float32, dout.device)
-    _check(gmm_combine_rows_bwd(dout, y, rows, weights, T, k, K, dy, dweights, stream), "gmm_combine_rows_bwd")
+        dy, dweights = out
+        _want("out dy", dy, on, _BF16, (M, K))
+        _want("out dweights", dweights, on, _F32, (T, k))
+    status = (_lib or load()).gmm_combine_rows_bwd(dout.data_ptr(), y.data_ptr(), rows.data_ptr(), weights.data_ptr(),
+                                                   T, k, K, dy.data_ptr(), dweights.data_ptr(), handle)
+    if status:
+        raise GmmError(status, "gmm_combine_rows_bwd")
     return dy, dweights
 
 
 def _need_join(on, T, K, b, w_post, gate, w_next):
     """Checks what the norms' two directions share; whether the gate has a row per token."""
     if b is not None:
-        _need("b", b, on, torch.bfloat16, T, K)
+        _want("b", b, on, _BF16, (T, K))
     elif w_post is not None or gate is not None:
         raise ValueError("w_post and gate apply to the block's output: pass b")
     if w_post is not None:
-        _need("w_post", w_post, on, torch.float32, K)
+        _want("w_post", w_post, on, _F32, (K,))
     if w_next is not None:
-        _need("w_next", w_next, on, torch.float32, K)
+        _want("w_next", w_next, on, _F32, (K,))
     if gate is None:
         return False
     if gate.dim() == 2:
-        _need("gate", gate, on, torch.bfloat16, T, K)
+        _want("gate", gate, on, _BF16, (T, K))
         return True
-    _need("gate", gate, on, torch.float32, K)
+    _want("gate", gate, on, _F32, (K,))
     return False
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def norm_join(x, b=None, w_post=None, gate=None, w_next=None, residual_scale=1.0, block_scale=1.0, eps=1e-6,
@@ -1194,24 +1251,30 @@ def norm_join(x, b=None, w_post=None, gate=None, w_next=None, residual_scale=1.0
         with other:
             return norm_join(x, b, w_post, gate, w_next, residual_scale, block_scale, eps, stream, out)
     T, K = x.shape
-    kind, on = _type_of("x", x), x.get_device()
-    _need("x", x, on, x.dtype, T, K)
-    _here(on)
+    dtype = x.dtype
+    kind, on = _type_of("x", x), _first("x", x, dtype)
     full = _need_join(on, T, K, b, w_post, gate, w_next)
     if b is None and w_next is None:
         raise ValueError("without b and w_next there is nothing to compute")
-    if out is not None:
-        o, n = out
-        if b is not None:
-            _need("out", o, on, x.dtype, T, K)
-        if w_next is not None:
-            _need("out n", n, on, torch.bfloat16, T, K)
+    handle = _handle(on, stream)
+    if out is None:
+        device = x.device
+        o = x if b is None else _empty((T, K), (K, 1), dtype=dtype, device=device)
+        n = None if w_next is None else _empty((T, K), (K, 1), dtype=_BF16, device=device)
     else:
-        o = x if b is None else _new2(T, K, x.dtype, x.device)
-        n = None if w_next is None else _new2(T, K, torch.bfloat16, x.device)
-    _check(gmm_norm_join(x, kind, b, w_post, gate, full, w_next, T, K, residual_scale, block_scale, eps,
-                         None if b is None else o, n, stream), "gmm_norm_join")
-    return (x if b is None else o), n
+        o, n = out
+        if b is None:
+            o = x
+        else:
+            _want("out", o, on, dtype, (T, K))
+        if w_next is not None:
+            _want("out n", n, on, _BF16, (T, K))
+    status = (_lib or load()).gmm_norm_join(x.data_ptr(), kind, _at(b), _at(w_post), _at(gate), full, _at(w_next), T, K,
+                                            residual_scale, block_scale, eps, None if b is None else o.data_ptr(),
+                                            _at(n), handle)
+    if status:
+        raise GmmError(status, "gmm_norm_join")
+    return o, n
 
 
 def norm_join_bwd(dout, dn, out, b=None, w_post=None, gate=None, w_next=None, residual_scale=1.0, block_scale=1.0,
@@ -1226,46 +1289,52 @@ def norm_join_bwd(dout, dn, out, b=None, w_post=None, gate=None, w_next=None, re
             return norm_join_bwd(dout, dn, out, b, w_post, gate, w_next, residual_scale, block_scale, eps, stream,
                                  into)
     T, K = out.shape
-    kind, on = _type_of("out", out), out.get_device()
-    _need("out", out, on, out.dtype, T, K)
-    _here(on)
-    if dout is None and dn is None:
-        raise ValueError("one of dout and dn must be given")
+    dtype = out.dtype
+    kind, on = _type_of("out", out), _first("out", out, dtype)
     if dout is not None:
-        _need("dout", dout, on, out.dtype, T, K)
+        _want("dout", dout, on, dtype, (T, K))
+    elif dn is None:
+        raise ValueError("one of dout and dn must be given")
     if dn is not None:
-        _need("dn", dn, on, torch.bfloat16, T, K)
+        _want("dn", dn, on, _BF16, (T, K))
         if w_next is None:
             raise ValueError("dn is the gradient of n: pass w_next")
     full = _need_join(on, T, K, b, w_post, gate, w_next)
-    dx = db = dw_post = dgate = dw_next = None
-    if into is not None:
-        dx, db = into
-        _need("into dx", dx, on, out.dtype, T, K)
-        if b is not None:
-            _need("into db", db, on, torch.bfloat16, T, K)
+    handle = _handle(on, stream)
+    device = out.device
+    if into is None:
+        dx = _empty((T, K), (K, 1), dtype=dtype, device=device)
+        db = None if b is None else _empty((T, K), (K, 1), dtype=_BF16, device=device)
     else:
-        dx = _new2(T, K, out.dtype, out.device)
-        db = None if b is None else _new2(T, K, torch.bfloat16, out.device)
-    if w_post is not None:
-        dw_post = _new1(K, torch.float32, out.device)
+        dx, db = into
+        _want("into dx", dx, on, dtype, (T, K))
+        if b is None:
+            db = None
+        else:
+            _want("into db", db, on, _BF16, (T, K))
+    dw_post = None if w_post is None else _empty((K,), (1,), dtype=_F32, device=device)
+    dw_next = None if w_next is None else _empty((K,), (1,), dtype=_F32, device=device)
+    dgate = None
     if gate is not None:
-        dgate = _new2(T, K, torch.bfloat16, out.device) if full else _new1(K, torch.float32, out.device)
-    if w_next is not None:
-        dw_next = _new1(K, torch.float32, out.device)
-    nbytes = gmm_norm_join_bwd_scratch_bytes(T, K)
-    scratch = _new1(nbytes, torch.uint8, out.device) if nbytes else None
-    _check(gmm_norm_join_bwd(dout, dn, out, kind, b, w_post, gate, full, w_next, T, K, residual_scale, block_scale,
-                             eps, dx, None if b is None else db, dw_post, dgate, dw_next, scratch, nbytes, stream),
-           "gmm_norm_join_bwd")
-    return dx, (None if b is None else db), dw_post, dgate, dw_next
+        dgate = (_empty((T, K), (K, 1), dtype=_BF16, device=device) if full
+                 else _empty((K,), (1,), dtype=_F32, device=device))
+    lib = _lib or load()
+    nbytes = lib.gmm_norm_join_bwd_scratch_bytes(T, K)
+    scratch = _empty((nbytes,), (1,), dtype=torch.uint8, device=device) if nbytes else None
+    status = lib.gmm_norm_join_bwd(_at(dout), _at(dn), out.data_ptr(), kind, _at(b), _at(w_post), _at(gate), full,
+                                   _at(w_next), T, K, residual_scale, block_scale, eps, dx.data_ptr(), _at(db),
+                                   _at(dw_post), _at(dgate), _at(dw_next), _at(scratch), nbytes, handle)
+    if status:
+        raise GmmError(status, "gmm_norm_join_bwd")
+    return dx, db, dw_post, dgate, dw_next
 
 
 def clip_grads(grads, max_norm, out=None, stream=None):
     """Gradients scaled by min(1, max_norm / norm), norm being the root of the sum of
-    all their squares, in place or into the tensors of `out` -> norm, float32 [1].
-    grads: contiguous bf16 or float32 tensors of any shapes.  A norm that is not
-    finite scales nothing; max_norm = math.inf computes the norm only."""
+    all their squares, in place or into the tensors of `out` (of the same types and
+    numbers of elements) -> norm, float32 [1].  grads: contiguous bf16 or float32
+    tensors of any shapes.  A norm that is not finite scales nothing; max_norm =
+    math.inf computes the norm only."""
     if stream is not None and (other := _other(stream)):
         with other:
             return clip_grads(grads, max_norm, out, stream)
@@ -1273,23 +1342,37 @@ def clip_grads(grads, max_norm, out=None, stream=None):
     n = len(grads)
     if out is not None and len(out) != n:
         raise ValueError(f"out: expected {n} tensors, got {len(out)}")
-    device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
-    on = grads[0].get_device() if n else device.index
-    types, counts = array.array("i"), array.array("q")
-    for i, g in enumerate(grads):
-        types.append(_type_of(f"grads[{i}]", g))
-        counts.append(g.numel())
-        if not g.is_contiguous() or g.get_device() != on or on < 0:
-            _need(f"grads[{i}]", g, on, g.dtype, *g.shape)
-        if out is not None and (out[i].dtype is not g.dtype or out[i].shape != g.shape or
-                                not out[i].is_contiguous() or out[i].get_device() != on):
-            _need(f"out[{i}]", out[i], on, g.dtype, *g.shape)
-    _here(on)
-    src = array.array("Q", [g.data_ptr() for g in grads])
-    dst = None if out is None else array.array("Q", [o.data_ptr() for o in out])
-    norm = _new1(1, torch.float32, device)
-    nbytes = gmm_clip_grads_scratch_bytes(n)
-    scratch = _new1(nbytes, torch.uint8, device) if nbytes else None
-    _check(gmm_clip_grads(src.buffer_info()[0], dst.buffer_info()[0] if dst else None, counts.buffer_info()[0],
-                          types.buffer_info()[0], n, max_norm, norm, scratch, nbytes, stream), "gmm_clip_grads")
+    on = grads[0].get_device() if n else _current_device()
+    dtypes, counts = _flat_tensors("grads", grads, on)
+    if out is not None:
+        if _flat_tensors("out", out, on) != (dtypes, counts):
+            raise ValueError("out: expected tensors of the gradients' types and numbers of elements")
+        dst = array.array("Q", list(map(_data_ptr, out)))
+    handle = _handle(on, stream)
+    src = array.array("Q", list(map(_data_ptr, grads)))
+    types = array.array("i", [d is _F32 for d in dtypes])
+    counts = array.array("q", counts)
+    device = grads[0].device if n else torch.device("cuda", on)
+    lib = _lib or load()
+    norm = _empty((1,), (1,), dtype=_F32, device=device)
+    nbytes = lib.gmm_clip_grads_scratch_bytes(n)
+    scratch = _empty((nbytes,), (1,), dtype=torch.uint8, device=device) if nbytes else None
+    status = lib.gmm_clip_grads(src.buffer_info()[0], None if out is None else dst.buffer_info()[0],
+                                counts.buffer_info()[0], types.buffer_info()[0], n, max_norm, norm.data_ptr(),
+                                _at(scratch), nbytes, handle)
+    if status:
+        raise GmmError(status, "gmm_clip_grads")
     return norm
+
+
+def _flat_tensors(what, tensors, on):
+    """Types and numbers of elements of contiguous bf16 or fp32 tensors on device `on`."""
+    dtypes = [t.dtype for t in tensors]
+    if not (all(map(_is_contiguous, tensors)) and set(map(_get_device, tensors)) <= {on} and on >= 0
+            and dtypes.count(_BF16) + dtypes.count(_F32) == len(dtypes)):
+        for i, t in enumerate(tensors):
+            _type_of(f"{what}[{i}]", t)
+            _want(f"{what}[{i}]", t, on, t.dtype, t.shape)
+            if on < 0:
+                _refuse(f"{what}[{i}]", t, on, t.dtype, t.shape)
+    return dtypes, [t.numel() for t in tensors]

@@ -240,8 +240,7 @@ gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, 
 
 size_t gmm_clip_grads_scratch_bytes(int n) {
   int sms = 0;
-  if (n < 0 || host_device_sms(&sms) != GMM_OK) return 0;
-  return static_cast<size_t>(clip_launches(n < 1 ? 1 : n)) * clip_ctas(sms) * sizeof(double);
+  return n < 0 || host_device_sms(&sms) != GMM_OK ? 0 : clip_scratch_bytes(n, sms);
 }
 
 gmm_status gmm_clip_grads(const void* const* grads, void* const* out, const int64_t* counts, const int32_t* types,
@@ -263,7 +262,7 @@ gmm_status gmm_clip_grads(const void* const* grads, void* const* out, const int6
   int sms = 0;
   const gmm_status st = host_device_sms(&sms);
   if (st != GMM_OK) return st;
-  if (!scratch || scratch_bytes < gmm_clip_grads_scratch_bytes(n)) return GMM_ERR_WORKSPACE;
+  if (!scratch || scratch_bytes < clip_scratch_bytes(n, sms)) return GMM_ERR_WORKSPACE;
   try {
     std::vector<ClipTensor> t;
     t.reserve(n);
@@ -271,7 +270,7 @@ gmm_status gmm_clip_grads(const void* const* grads, void* const* out, const int6
       if (counts[i] > 0)
         t.push_back({grads[i], out ? out[i] : const_cast<void*>(grads[i]), counts[i], types[i] == GMM_F32});
     return launched(launch_clip(t.data(), static_cast<int>(t.size()), max_norm, out == nullptr,
-                                static_cast<double*>(scratch), norm, sms, static_cast<cudaStream_t>(stream)),
+                                scratch, norm, sms, static_cast<cudaStream_t>(stream)),
                     "clip_grads launch");
   } catch (const std::bad_alloc&) {
     return host_fail(GMM_ERR_CUDA, "out of host memory");

@@ -1,11 +1,15 @@
 // The global norm of many gradients, and their scaling to a largest norm.
 //
 // The tensors come as a table in the launch's parameters, cut into chunks of one
-// length; a CTA finds a chunk's tensor by bisection.  The first pass leaves a sum
-// of squares a CTA, in double; each CTA of the second adds them all up in their
-// order, so that the norm is one number whatever the schedule, and scales.  The
-// second pass takes the chunks backwards: the ones that the first read last are
-// still in the L2.
+// length; a CTA finds a chunk's tensor by bisection.  The first pass leaves a sum of
+// squares a CTA; each CTA of the second adds them all up in their order, so that the
+// norm is one number whatever the schedule, and scales.  The second pass takes the
+// chunks backwards: the ones that the first read last are still in the L2.
+//
+// Sums are fp32, compensated from chunk to chunk, while every square keeps its bits
+// there; a CTA that meets a sum outside that range adds its values up in double, of
+// which this GPU does two a cycle and SM (sums in double throughout: 19.7 us for 60
+// tensors of 3 M values).
 #include "common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -60,15 +64,16 @@ __device__ __forceinline__ void put(uint16_t* p, long long i, float v) {
   p[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xffffu);
 }
 
-// This thread's share of a chunk's squares.  The sum is fp32 over at most a few
-// hundred values (relative error below 2^-18 / 8, and of either sign); where that
-// left the range in which squares keep their bits, the share is added up again in
-// double: 1e-25 is 2^43 times the smallest normal square's.
+// Sums in which squares keep their bits: 1e-25 is 2^43 times the smallest normal
+// number, and a few thousand sums of 1e30 stay finite.
+__device__ __forceinline__ bool in_range(float s) { return s >= 1e-25f && s <= 1e30f; }
+
+// This thread's share of a chunk's squares; *some: whether it has a value but 0.
 template <typename T>
-__device__ double squares_of(const T* __restrict__ p, int n) {
+__device__ float squares_of(const T* __restrict__ p, int n, bool* some_out) {
   constexpr int W = 16 / sizeof(T);
   float s = 0.0f;
-  bool some = false;
+  uint32_t some = 0;
   const bool wide = (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
   const int nv = wide ? n / W : 0;
   const uint4* v = reinterpret_cast<const uint4*>(p);
@@ -82,7 +87,7 @@ __device__ double squares_of(const T* __restrict__ p, int n) {
     float a[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      some |= (u[j].x | u[j].y | u[j].z | u[j].w) != 0;
+      some |= u[j].x | u[j].y | u[j].z | u[j].w;
       a[j] = 0.0f;
       if constexpr (sizeof(T) == 2) {
         float f[8];
@@ -100,51 +105,79 @@ __device__ double squares_of(const T* __restrict__ p, int n) {
   }
   for (int i = nv * W + threadIdx.x; i < n; i += kThreads) {
     const float f = value_of(p, i);
-    some |= f != 0.0f;
+    some |= __float_as_uint(f);
     s = fmaf(f, f, s);
   }
-  if (!some || (s > 1e-25f && s < 1e37f)) return s;
+  *some_out = some != 0;
+  return s;
+}
+
+template <typename T>
+__device__ double squares_in_double(const T* __restrict__ p, int n) {
   double d = 0.0;
-  for (int i0 = 0; i0 < nv; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    if (i < nv)
-      for (int e = 0; e < W; ++e) {
-        const double f = value_of(p, static_cast<long long>(i) * W + e);
-        d += f * f;
-      }
-  }
-  for (int i = nv * W + threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     const double f = value_of(p, i);
     d += f * f;
   }
   return d;
 }
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
+// Sum over the CTA, in its order; red: a value a warp.
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T* red) {
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  double s = 0.0;
+  T s = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) s += red[w];
   return s;
 }
 
+// The CTAs' sums: fp32, and double (read where the fp32 one is out of range).
+struct Parts {
+  double* exact;
+  float* sum;
+};
+
 template <int N>
-__global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_constant__ ClipTable<N> tab,
-                                                             double* __restrict__ parts) {
-  __shared__ double red[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_constant__ ClipTable<N> tab, Parts parts) {
+  __shared__ float red[kThreads / 32];
+  __shared__ double red_exact[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
-  double s = 0.0;
+  float s = 0.0f, lost = 0.0f;  // compensated
+  bool odd = false;
   for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
     const Piece p = piece_of(tab, c);
-    s += p.f32 ? squares_of(static_cast<const float*>(p.src) + p.at, p.n)
-               : squares_of(static_cast<const uint16_t*>(p.src) + p.at, p.n);
+    bool some;
+    const float add = (p.f32 ? squares_of(static_cast<const float*>(p.src) + p.at, p.n, &some)
+                             : squares_of(static_cast<const uint16_t*>(p.src) + p.at, p.n, &some));
+    odd |= some && !in_range(add);
+    const float y = add - lost, t = s + y;
+    lost = (t - s) - y;
+    s = t;
   }
-  s = block_sum(s, red);
-  if (threadIdx.x == 0) parts[blockIdx.x] = s;
+  if (!__syncthreads_or(odd)) {
+    s = block_sum(s, red);
+    if (threadIdx.x == 0) {
+      parts.sum[blockIdx.x] = s;
+      parts.exact[blockIdx.x] = s;
+    }
+    return;
+  }
+  double d = 0.0;
+  for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
+    const Piece p = piece_of(tab, c);
+    d += p.f32 ? squares_in_double(static_cast<const float*>(p.src) + p.at, p.n)
+               : squares_in_double(static_cast<const uint16_t*>(p.src) + p.at, p.n);
+  }
+  d = block_sum(d, red_exact);
+  if (threadIdx.x == 0) {
+    parts.sum[blockIdx.x] = __int_as_float(0x7fc00000);  // NaN: not in range
+    parts.exact[blockIdx.x] = d;
+  }
 }
 
 // dst = src * by; a factor of 1 copies the bits (a product would give NaNs another payload).
@@ -190,15 +223,28 @@ __device__ void scale_piece(const T* src, T* dst, int n, float by) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ ClipTable<N> tab,
-                                                              const double* __restrict__ parts, int P, float max_norm,
-                                                              int in_place, float* __restrict__ norm) {
-  __shared__ double red[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ ClipTable<N> tab, Parts parts,
+                                                              int P, float max_norm, int in_place,
+                                                              float* __restrict__ norm) {
+  __shared__ float red[kThreads / 32];
+  __shared__ double red_exact[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < P; i += kThreads) s += parts[i];
-  const float whole = static_cast<float>(sqrt(block_sum(s, red)));
+  float s = 0.0f;
+  bool odd = false;
+  for (int i = threadIdx.x; i < P; i += kThreads) {
+    const float v = parts.sum[i];
+    odd |= v != 0.0f && !in_range(v);
+    s += v;
+  }
+  float whole;
+  if (!__syncthreads_or(odd)) {
+    whole = sqrtf(block_sum(s, red));
+  } else {
+    double d = 0.0;
+    for (int i = threadIdx.x; i < P; i += kThreads) d += parts.exact[i];
+    whole = static_cast<float>(sqrt(block_sum(d, red_exact)));
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
   // a norm that is not finite scales nothing
   const float by = whole > max_norm && whole <= 3.402823466e38f ? max_norm / whole : 1.0f;
@@ -235,14 +281,15 @@ void fill(ClipTable<N>& tab, const ClipTensor* t, int n, int chunk) {
 int grid_of(const int* first, int n, int most) { return first[n] < most ? (first[n] > 0 ? first[n] : 1) : most; }
 
 template <int N>
-cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_place, double* parts, int most,
+cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_place, const Parts& parts, int most,
                 float* norm, bool norm_only, cudaStream_t s) {
   int P = 0;
   ClipTable<N> tab;
   for (int i = 0; i == 0 || i < n; i += N) {
     fill<N>(tab, t + i, n - i < N ? n - i : N, chunk);
     const int grid = grid_of(tab.first, tab.n, most);
-    const cudaError_t e = launch_pdl(clip_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab, parts + P);
+    const cudaError_t e = launch_pdl(clip_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
+                                     Parts{parts.exact + P, parts.sum + P});
     if (e != cudaSuccess) return e;
     P += grid;
   }
@@ -250,7 +297,7 @@ cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_pl
     if (n > N) fill<N>(tab, t + i, n - i < N ? n - i : N, chunk);
     const int grid = norm_only ? 1 : grid_of(tab.first, tab.n, most);
     const cudaError_t e = launch_pdl(clip_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
-                                     static_cast<const double*>(parts), P, max_norm, in_place || norm_only, norm);
+                                     parts, P, max_norm, in_place || norm_only, norm);
     if (e != cudaSuccess || norm_only) return e;
   }
   return cudaSuccess;
@@ -258,11 +305,20 @@ cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_pl
 
 }  // namespace
 
+namespace {
 int clip_ctas(int sms) { return 8 * sms; }
 int clip_launches(int n) { return n <= kSmallTable ? 1 : (n + kLargeTable - 1) / kLargeTable; }
+}  // namespace
 
-cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, double* parts, float* norm, int sms,
+size_t clip_scratch_bytes(int n, int sms) {
+  return static_cast<size_t>(clip_launches(n)) * clip_ctas(sms) * (sizeof(double) + sizeof(float));
+}
+
+cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, void* scratch, float* norm, int sms,
                         cudaStream_t stream) {
+  Parts parts;
+  parts.exact = static_cast<double*>(scratch);
+  parts.sum = reinterpret_cast<float*>(parts.exact + static_cast<size_t>(clip_launches(n)) * clip_ctas(sms));
   long long total = 0;
   for (int i = 0; i < n; ++i) total += t[i].count;
   // some eight chunks a CTA, of 4096 values at least and 32768 at most

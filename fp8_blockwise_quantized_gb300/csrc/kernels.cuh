@@ -244,9 +244,8 @@ struct ClipTensor {
   int64_t count;
   int f32;
 };
-int clip_ctas(int sms);     // sums of squares that a launch leaves, at most
-int clip_launches(int n);   // launches that n tensors take
-cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, double* parts, float* norm, int sms,
+size_t clip_scratch_bytes(int n, int sms);
+cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, void* scratch, float* norm, int sms,
                         cudaStream_t stream);
 
 // Tile geometry the host needs to build tensor maps and size grids.

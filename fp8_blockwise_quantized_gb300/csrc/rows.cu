@@ -13,11 +13,17 @@ namespace {
 // ---- places -------------------------------------------------------------------
 // A stable counting sort of N ids into G + 1 bins, the last for the ids outside
 // 0 .. G - 1.  A CTA takes a chunk of consecutive ids, each of its warps a run of
-// the chunk; within a warp, the lanes with one id find each other with a match,
-// and the warp's count of that id so far gives their places in the run.  The
-// places' bases are the ids before in the chunk (summed over the warps), in the
-// chunks before (a table that a first kernel fills) and in the bins before.
+// the chunk, 32 ids a round; the warp's count of an id in the rounds before and the
+// lanes before with the same id give its place in the run.  The lanes of one id find
+// each other in a word of shared memory for each bin, or where there are too many bins
+// for that by a ballot for each bit (65536 ids of 256: 6.2 us; by ballots 8.6; by the
+// match instruction, which takes a round for each different id, 11.8).  The places'
+// bases are the ids before in the chunk (summed over the warps), in the chunks before
+// and in the bins before.  Up to 65536 ids the chunks are a cluster's CTAs, which read
+// each other's counts; beyond, a first kernel leaves them in a table.
 constexpr int kSortThreads = 512;
+constexpr int kSortCluster = 8;
+constexpr int kMaskBins = 1025;  // so many bins, and their words are at most 107 KB with the counts
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDirectChunks = 64;  // so many rows of the table each CTA sums itself
 
@@ -55,39 +61,62 @@ __global__ void __launch_bounds__(64) sort_scan_kernel(int32_t* __restrict__ tab
   *p = run;
 }
 
-template <int R>
+// rounds: of a warp, at most R; a CTA's chunk is kSortThreads * rounds ids.
+template <int R, bool CLUSTER, bool MASKS>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t* __restrict__ ids, int N, int G,
-                                                                  int chunks, const int32_t* __restrict__ table,
+                                                                  int rounds, int chunks, const int32_t* __restrict__ table,
                                                                   int32_t* __restrict__ rows,
                                                                   int32_t* __restrict__ sizes) {
   extern __shared__ int smem[];
   __shared__ int warp_sums[kSortWarps];
   const int B = G + 1, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   int* base = smem;                                           // [B]
-  uint16_t* runs = reinterpret_cast<uint16_t*>(smem + B);     // [kSortWarps][B]; a chunk has at most 8192 ids
+  int* counts = smem + B;                                     // [B]
+  uint16_t* runs = reinterpret_cast<uint16_t*>(smem + 2 * B);  // [kSortWarps][B]; a chunk has at most 8192 ids
   uint16_t* mine = runs + warp * B;
   griddep_launch_dependents();
-  for (int b = t; b < kSortWarps * B; b += kSortThreads) runs[b] = 0;
+  for (int b = t; b < kSortWarps / 2 * B; b += kSortThreads) reinterpret_cast<uint32_t*>(runs)[b] = 0;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(runs + kSortWarps * B);  // [kSortWarps][B]
+  if constexpr (MASKS)
+    for (int b = t; b < kSortWarps * B; b += kSortThreads) masks[b] = 0;
+  const int bits = 32 - __clz(G);  // of a bin
   __syncthreads();
   griddep_wait();
-  const long long first = static_cast<long long>(blockIdx.x) * (kSortThreads * R) + warp * (32 * R) + lane;
+  const long long first = (static_cast<long long>(blockIdx.x) * kSortThreads + warp * 32) * rounds + lane;
   int bin[R], rank[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) bin[r] = first + 32 * r < N ? bin_of(__ldg(ids + first + 32 * r), G) : -1;
+  for (int r = 0; r < R; ++r) bin[r] = r < rounds && first + 32 * r < N ? bin_of(__ldg(ids + first + 32 * r), G) : -1;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const unsigned peers = __match_any_sync(0xffffffffu, bin[r]);
+    if (r >= rounds) break;
+    const bool live = bin[r] >= 0;  // the lanes behind the last id count nothing
+    uint32_t* mask = masks + warp * B + bin[r];
+    unsigned peers;
+    if constexpr (MASKS) {
+      if (live) atomicOr(mask, 1u << lane);
+      __syncwarp();
+      peers = live ? *mask : 0;
+    } else {
+      peers = __ballot_sync(0xffffffffu, live);
+      for (int i = 0; i < bits; ++i) {
+        const bool set = bin[r] >> i & 1;
+        const unsigned with = __ballot_sync(0xffffffffu, set);
+        peers &= set ? with : ~with;
+      }
+    }
     const int before = __popc(peers & ((1u << lane) - 1u));
-    const int so_far = bin[r] >= 0 ? mine[bin[r]] : 0;
+    const int so_far = live ? mine[bin[r]] : 0;
     __syncwarp();
-    if (before == 0 && bin[r] >= 0) mine[bin[r]] = static_cast<uint16_t>(so_far + __popc(peers));
+    if (live && before == 0) {
+      mine[bin[r]] = static_cast<uint16_t>(so_far + __popc(peers));
+      if constexpr (MASKS) *mask = 0;
+    }
     __syncwarp();
     rank[r] = so_far + before;
   }
   __syncthreads();
   // per bin: the warps' counts as sums of those before, the chunks before, all chunks
   const int per = (B + kSortThreads - 1) / kSortThreads, b0 = min(B, t * per), b1 = min(B, b0 + per);
-  int sum = 0;
   for (int b = b0; b < b1; ++b) {
     int run = 0;
 #pragma unroll
@@ -96,8 +125,25 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t*
       runs[w * B + b] = static_cast<uint16_t>(run);
       run += c;
     }
-    int earlier = 0, total = run;
-    if (chunks > kDirectChunks) {
+    counts[b] = run;
+  }
+  if constexpr (CLUSTER) {
+    __syncwarp();
+    cluster_sync_all();
+  }
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    int earlier = 0, total = counts[b];
+    if constexpr (CLUSTER) {
+      total = 0;
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) {
+        int v;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(counts + b), c)));
+        if (c < static_cast<int>(blockIdx.x)) earlier += v;
+        total += v;
+      }
+    } else if (chunks > kDirectChunks) {
       earlier = table[static_cast<long long>(blockIdx.x) * B + b];
       total = table[static_cast<long long>(chunks) * B + b];
     } else if (chunks > 1) {
@@ -115,7 +161,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t*
   }
   const int inc = warp_inclusive_scan(sum);
   if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
+  // (the other CTAs' counts have been read: none of them leaves before)
+  if constexpr (CLUSTER) {
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
   int start = inc - sum;
 #pragma unroll
   for (int w = 0; w < kSortWarps; ++w) start += w < warp ? warp_sums[w] : 0;
@@ -123,7 +175,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t*
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    if (bin[r] < 0) continue;
+    if (r >= rounds || bin[r] < 0) continue;
     const int row = base[bin[r]] + mine[bin[r]] + rank[r];
     rows[first + 32 * r] = bin[r] < G ? row : -1 - row;
   }
@@ -318,9 +370,14 @@ constexpr long long kNarrow = 1LL << 31;  // indices below it are 32 bits
 
 unsigned blocks_of(long long threads) { return static_cast<unsigned>((threads + 255) / 256); }
 
-int sort_chunk(int64_t N) { return N <= 512 ? 512 : N <= 131072 ? 2048 : 8192; }
-// one CTA's chunk may hold all
-int sort_chunks(int64_t N) { return N <= 8192 ? 1 : static_cast<int>((N + sort_chunk(N) - 1) / sort_chunk(N)); }
+constexpr int64_t kOneCta = 2048, kOneCluster = kSortCluster * kSortThreads * 16;
+// Rounds of a warp in a table's sort: few while that gives chunks for a good part of the SMs.
+int sort_rounds(int64_t N) { return N <= 131072 ? 4 : 16; }
+// chunks of a table's sort; 1 where a CTA or a cluster holds all ids
+int sort_chunks(int64_t N) {
+  const int64_t chunk = kSortThreads * sort_rounds(N);
+  return N <= kOneCluster ? 1 : static_cast<int>((N + chunk - 1) / chunk);
+}
 
 }  // namespace
 
@@ -336,26 +393,46 @@ cudaError_t launch_sort_rows(const int32_t* ids, int64_t N, int G, int32_t* rows
   cudaError_t e;
   if (chunks > 1) {
     e = launch_pdl(sort_count_kernel, dim3(chunks), dim3(kSortThreads), B * sizeof(int), stream, ids, n, G,
-                   sort_chunk(N), table);
+                   kSortThreads * sort_rounds(N), table);
     if (e != cudaSuccess) return e;
     if (chunks > kDirectChunks &&
         (e = launch_pdl(sort_scan_kernel, dim3((B + 63) / 64), dim3(64), 0, stream, table, B, chunks)) != cudaSuccess)
       return e;
   }
-  const int smem = B * sizeof(int) + kSortWarps * B * sizeof(uint16_t);
-  static std::atomic<uint64_t> done1, done4, done16;
-  auto place = [&](auto kernel, std::atomic<uint64_t>& done) {
-    if (smem > 40 * 1024) {
-      const cudaError_t err = allow_smem(kernel, kSortWarps * (kMaxGroups + 1) * 2 + (kMaxGroups + 1) * 4, done);
+  const bool cluster = N > kOneCta && N <= kOneCluster;
+  const int ctas = cluster ? kSortCluster : chunks;
+  const int rounds = chunks > 1 ? sort_rounds(N) : static_cast<int>((N + ctas * kSortThreads - 1) / (ctas * kSortThreads));
+  static std::atomic<uint64_t> done[2][5];
+  auto place = [&](auto masks, auto kernel, int i) {
+    constexpr bool kMasks = decltype(masks)::value;
+    const auto bytes = [](int bins) { return bins * (2 * 4 + kSortWarps * (kMasks ? 6 : 2)); };
+    if (bytes(B) > 40 * 1024) {
+      const cudaError_t err = allow_smem(kernel, bytes(kMasks ? kMaskBins : kMaxGroups + 1), done[kMasks][i]);
       if (err != cudaSuccess) return err;
     }
-    return launch_pdl(kernel, dim3(chunks), dim3(kSortThreads), smem, stream, ids, n, G, chunks,
-                      static_cast<const int32_t*>(table), rows, sizes);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = bytes(B);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kSortCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, ids, n, G, rounds, chunks, static_cast<const int32_t*>(table), rows, sizes);
   };
-  const int per_cta = chunks > 1 ? sort_chunk(N) : n;
-  if (per_cta <= 512) return place(sort_place_kernel<1>, done1);
-  if (per_cta <= 2048) return place(sort_place_kernel<4>, done4);
-  return place(sort_place_kernel<16>, done16);
+  auto sized = [&](auto masks) {
+    constexpr bool M = decltype(masks)::value;
+    if (cluster)
+      return rounds <= 4 ? place(masks, sort_place_kernel<4, true, M>, 0) : place(masks, sort_place_kernel<16, true, M>, 1);
+    if (rounds <= 1) return place(masks, sort_place_kernel<1, false, M>, 2);
+    return rounds <= 4 ? place(masks, sort_place_kernel<4, false, M>, 3) : place(masks, sort_place_kernel<16, false, M>, 4);
+  };
+  return B <= kMaskBins ? sized(std::true_type()) : sized(std::false_type());
 }
 
 cudaError_t launch_gather_rows(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* out,
