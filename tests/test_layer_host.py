@@ -66,8 +66,8 @@ def test_sort_refusals(lib, kw, code):
 
 def test_sort_scratch(lib):
     need = lib.gmm_sort_rows_scratch_bytes
-    assert need(0, 4) == 0 and need(8192, 4096) == 0 and need(-1, 4) == 0 and need(10, 0) == 0
-    for n, g in ((8193, 1), (65536, 256), (1 << 20, 4096), (2 ** 31 - 1, 4096)):
+    assert need(0, 4) == 0 and need(65536, 4096) == 0 and need(-1, 4) == 0 and need(10, 0) == 0
+    for n, g in ((65537, 1), (1 << 18, 256), (1 << 20, 4096), (2 ** 31 - 1, 4096)):
         assert 0 < need(n, g) < 5 * 2 ** 32
 
 
