@@ -282,13 +282,13 @@ int grid_of(const int* first, int n, int most) { return first[n] < most ? (first
 
 template <int N>
 cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_place, const Parts& parts, int most,
-                float* norm, bool norm_only, cudaStream_t s) {
+                float* norm, bool norm_only, bool over, cudaStream_t s) {
   int P = 0;
   ClipTable<N> tab;
   for (int i = 0; i == 0 || i < n; i += N) {
     fill<N>(tab, t + i, n - i < N ? n - i : N, chunk);
     const int grid = grid_of(tab.first, tab.n, most);
-    const cudaError_t e = launch_pdl(clip_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
+    const cudaError_t e = launch_short(over, clip_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
                                      Parts{parts.exact + P, parts.sum + P});
     if (e != cudaSuccess) return e;
     P += grid;
@@ -296,7 +296,7 @@ cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_pl
   for (int i = 0; i == 0 || i < n; i += N) {
     if (n > N) fill<N>(tab, t + i, n - i < N ? n - i : N, chunk);
     const int grid = norm_only ? 1 : grid_of(tab.first, tab.n, most);
-    const cudaError_t e = launch_pdl(clip_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
+    const cudaError_t e = launch_short(over, clip_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
                                      parts, P, max_norm, in_place || norm_only, norm);
     if (e != cudaSuccess || norm_only) return e;
   }
@@ -325,10 +325,11 @@ cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_plac
   const int most = clip_ctas(sms);
   long long chunk = (total / (8LL * most) + 4095) / 4096 * 4096;
   chunk = chunk < 4096 ? 4096 : chunk > 32768 ? 32768 : chunk;
+  const bool over = launch_over(6 * total, stream);  // two reads and a write
   const bool norm_only = max_norm > 3.402823466e38f && in_place;
   if (n <= kSmallTable)
-    return run<kSmallTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, stream);
-  return run<kLargeTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, stream);
+    return run<kSmallTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, over, stream);
+  return run<kLargeTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, over, stream);
 }
 
 }  // namespace gmm

@@ -464,17 +464,18 @@ int backward_vectors(int64_t K) { return K > 8 * 512 ? 2 : 1; }
 
 template <typename S, bool FULL>
 cudaError_t forward(const NormJoinArgs& a, const Shape& sh, cudaStream_t stream) {
+  const bool over = launch_over(8 * a.T * a.K, stream);
   return sh.threads == 256
-             ? launch_pdl(norm_join_kernel<S, kForward, 256, FULL>, dim3(sh.grid), dim3(256), 0, stream, a)
-             : launch_pdl(norm_join_kernel<S, kForward, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
+             ? launch_short(over, norm_join_kernel<S, kForward, 256, FULL>, dim3(sh.grid), dim3(256), 0, stream, a)
+             : launch_short(over, norm_join_kernel<S, kForward, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
 }
 template <typename S, bool FULL>
-cudaError_t backward(const NormJoinBwdArgs& a, const Shape& sh, cudaStream_t stream) {
+cudaError_t backward(const NormJoinBwdArgs& a, const Shape& sh, bool over, cudaStream_t stream) {
   if (backward_vectors(a.K) == 2)
-    return launch_pdl(norm_join_bwd_kernel<S, 2, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
+    return launch_short(over, norm_join_bwd_kernel<S, 2, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
   return sh.threads == 256
-             ? launch_pdl(norm_join_bwd_kernel<S, 1, 256, FULL>, dim3(sh.grid), dim3(256), 0, stream, a)
-             : launch_pdl(norm_join_bwd_kernel<S, 1, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
+             ? launch_short(over, norm_join_bwd_kernel<S, 1, 256, FULL>, dim3(sh.grid), dim3(256), 0, stream, a)
+             : launch_short(over, norm_join_bwd_kernel<S, 1, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
 }
 
 }  // namespace
@@ -496,15 +497,16 @@ cudaError_t launch_norm_join_bwd(const NormJoinBwdArgs& args, int sms, cudaStrea
   NormJoinBwdArgs a = args;
   const Shape sh(a.T, a.K, backward_vectors(a.K), sms);
   a.row_threads = sh.row_threads;
+  const bool over = launch_over(12 * a.T * a.K, stream);
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     if (a.gate_full)
-      e = a.f32 ? backward<float, true>(a, sh, stream) : backward<uint16_t, true>(a, sh, stream);
+      e = a.f32 ? backward<float, true>(a, sh, over, stream) : backward<uint16_t, true>(a, sh, over, stream);
     else
-      e = a.f32 ? backward<float, false>(a, sh, stream) : backward<uint16_t, false>(a, sh, stream);
+      e = a.f32 ? backward<float, false>(a, sh, over, stream) : backward<uint16_t, false>(a, sh, over, stream);
   }
   if (e != cudaSuccess || !(a.dw_post || a.dgate_col || a.dw_next)) return e;
-  return launch_pdl(norm_join_reduce_kernel, dim3(static_cast<unsigned>(a.K / 8), 2), dim3(256), 0, stream,
+  return launch_short(over, norm_join_reduce_kernel, dim3(static_cast<unsigned>(a.K / 8), 2), dim3(256), 0, stream,
                     static_cast<const float*>(a.parts), sh.grid * sh.teams, static_cast<int>(a.K), a.beta, a.w_post,
                     a.gate_col, a.dw_post, a.dgate_col, a.dw_next);
 }

@@ -237,25 +237,29 @@ cudaError_t by_words(int E, F&& launch) {
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.T + kWarps - 1) / kWarps)), block(32 * kWarps);
+  // (a fifth of the memory's rate)
+  const bool over = launch_over(5 * a.T * a.E * (a.f32 ? 4 : 2), stream);
   return by_words(a.E, [&](auto v) {
     constexpr int V = decltype(v)::value;
     if (a.f32)
-      return launch_pdl(route_kernel<float, V>, grid, block, 0, stream, static_cast<const float*>(a.logits), a.bias, a.T,
+      return launch_short(over, route_kernel<float, V>, grid, block, 0, stream, static_cast<const float*>(a.logits), a.bias, a.T,
                         a.E, a.k, a.softmax, a.renorm, a.scale, a.ids_out, a.weights);
-    return launch_pdl(route_kernel<uint16_t, V>, grid, block, 0, stream, static_cast<const uint16_t*>(a.logits), a.bias,
+    return launch_short(over, route_kernel<uint16_t, V>, grid, block, 0, stream, static_cast<const uint16_t*>(a.logits), a.bias,
                       a.T, a.E, a.k, a.softmax, a.renorm, a.scale, a.ids_out, a.weights);
   });
 }
 
 cudaError_t launch_route_bwd(const RouteArgs& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.T + kWarps - 1) / kWarps)), block(32 * kWarps);
+  // (a fifth of the memory's rate)
+  const bool over = launch_over(5 * a.T * a.E * (a.f32 ? 4 : 2), stream);
   return by_words(a.E, [&](auto v) {
     constexpr int V = decltype(v)::value;
     if (a.f32)
-      return launch_pdl(route_bwd_kernel<float, V>, grid, block, 0, stream, a.dweights,
+      return launch_short(over, route_bwd_kernel<float, V>, grid, block, 0, stream, a.dweights,
                         static_cast<const float*>(a.logits), a.ids, a.T, a.E, a.k, a.softmax, a.renorm, a.scale,
                         static_cast<float*>(a.dlogits));
-    return launch_pdl(route_bwd_kernel<uint16_t, V>, grid, block, 0, stream, a.dweights,
+    return launch_short(over, route_bwd_kernel<uint16_t, V>, grid, block, 0, stream, a.dweights,
                       static_cast<const uint16_t*>(a.logits), a.ids, a.T, a.E, a.k, a.softmax, a.renorm, a.scale,
                       static_cast<uint16_t*>(a.dlogits));
   });

@@ -407,6 +407,8 @@ cudaError_t launch_sort_rows(const int32_t* ids, int64_t N, int G, int32_t* rows
                              cudaStream_t stream) {
   const int B = G + 1, n = static_cast<int>(N), chunks = sort_chunks(N);
   int32_t* table = static_cast<int32_t*>(scratch);
+  // 16384 ids sort in the time of those 32 MB
+  const bool over = launch_over(2048LL * N, stream);
   cudaError_t e;
   if (chunks > 1) {
     e = launch_pdl(sort_count_kernel, dim3(chunks), dim3(kSortThreads), B * sizeof(int), stream, ids, n, G,
@@ -433,13 +435,20 @@ cudaError_t launch_sort_rows(const int32_t* ids, int64_t N, int G, int32_t* rows
     cfg.dynamicSmemBytes = bytes(B);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kSortCluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    int attrs = 0;
+    if (cluster) {
+      attr[attrs].id = cudaLaunchAttributeClusterDimension;
+      attr[attrs].val.clusterDim.x = kSortCluster;
+      attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
+      ++attrs;
+    }
+    if (over) {
+      attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[attrs].val.programmaticStreamSerializationAllowed = 1;
+      ++attrs;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = cluster ? 2 : 1;
+    cfg.numAttrs = attrs;
     return cudaLaunchKernelEx(&cfg, kernel, ids, n, G, rounds, chunks, static_cast<const int32_t*>(table), rows, sizes);
   };
   auto sized = [&](auto masks) {
@@ -456,11 +465,12 @@ cudaError_t launch_gather_rows(const void* x, const int32_t* rows, int64_t T, in
                                cudaStream_t stream) {
   const long long vectors = T * (K / 8), M = T * k;
   const unsigned KV = static_cast<unsigned>(K / 8);
+  const bool over = launch_over(2 * M * K, stream);
   if (vectors < kNarrow)
-    return launch_pdl(gather_kernel<uint32_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
+    return launch_short(over, gather_kernel<uint32_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
                       static_cast<const uint4*>(x), rows, static_cast<uint32_t>(vectors), k, KV, M,
                       static_cast<uint4*>(out));
-  return launch_pdl(gather_kernel<uint64_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
+  return launch_short(over, gather_kernel<uint64_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
                     static_cast<const uint4*>(x), rows, static_cast<uint64_t>(vectors), k, KV, M,
                     static_cast<uint4*>(out));
 }
@@ -469,11 +479,12 @@ cudaError_t launch_gather_quantize(const void* x, const int32_t* rows, int64_t T
                                    cudaStream_t stream) {
   const long long units = T * (K / 128), M = T * k;
   const unsigned KB = static_cast<unsigned>(K / 128);
+  const bool over = launch_over(M * K, stream);
   if (units < kNarrow / 8)
-    return launch_pdl(gather_quantize_kernel<uint32_t>, dim3(blocks_of(units * 8)), dim3(256), 0, stream,
+    return launch_short(over, gather_quantize_kernel<uint32_t>, dim3(blocks_of(units * 8)), dim3(256), 0, stream,
                       static_cast<const uint4*>(x), rows, static_cast<uint32_t>(units), k, KB, M,
                       static_cast<uint4*>(xq), xs);
-  return launch_pdl(gather_quantize_kernel<uint64_t>, dim3(blocks_of(units * 8)), dim3(256), 0, stream,
+  return launch_short(over, gather_quantize_kernel<uint64_t>, dim3(blocks_of(units * 8)), dim3(256), 0, stream,
                     static_cast<const uint4*>(x), rows, static_cast<uint64_t>(units), k, KB, M,
                     static_cast<uint4*>(xq), xs);
 }
@@ -484,8 +495,9 @@ cudaError_t launch_combine_rows(const void* y, const int32_t* rows, const float*
   const int V = k <= 2 ? 2 : 1;
   const unsigned part = (KV + V - 1) / V;
   const long long units = T * static_cast<long long>(part), M = T * k;
+  const bool over = launch_over(2 * M * K, stream);
   auto launch = [&](auto kernel, auto narrow) {
-    return launch_pdl(kernel, dim3(blocks_of(units)), dim3(256), 0, stream, static_cast<const uint4*>(y), rows, weights,
+    return launch_short(over, kernel, dim3(blocks_of(units)), dim3(256), 0, stream, static_cast<const uint4*>(y), rows, weights,
                       static_cast<decltype(narrow)>(units), k, KV, part, M, static_cast<uint4*>(out));
   };
   if (units < kNarrow) return V == 2 ? launch(combine_kernel<uint32_t, 2>, uint32_t()) : launch(combine_kernel<uint32_t, 1>, uint32_t());
@@ -499,7 +511,8 @@ cudaError_t launch_combine_rows_bwd(const void* dout, const void* y, const int32
   int span = 1;
   while (span < kBwdWarps && T * span < 16LL * sms && span * 256 < K) span *= 2;
   const long long per = kBwdWarps / span;
-  return launch_pdl(combine_bwd_kernel, dim3(static_cast<unsigned>((T + per - 1) / per)), dim3(32 * kBwdWarps), 0,
+  const bool over = launch_over(4 * T * k * K, stream);
+  return launch_short(over, combine_bwd_kernel, dim3(static_cast<unsigned>((T + per - 1) / per)), dim3(32 * kBwdWarps), 0,
                     stream, static_cast<const uint4*>(dout), static_cast<const uint4*>(y), rows, weights,
                     static_cast<long long>(T), k, static_cast<unsigned>(K / 8), span, static_cast<uint4*>(dy), dweights);
 }
