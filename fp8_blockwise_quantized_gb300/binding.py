@@ -975,7 +975,7 @@ def mx4_fwd_swiglu_quant(xq, xs, wq, ws, group_sizes, with_h=True, workspace=Non
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-_empty = torch.empty_strided
+_empty, _like = torch.empty_strided, torch.empty_like  # _like takes a little less time
 _current_device = torch._C._cuda_getDevice
 _data_ptr, _is_contiguous, _get_device = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
 
@@ -1073,7 +1073,7 @@ def route_bwd(dweights, logits, ids, score="softmax", renorm=False, scale=1.0, s
     _want("dweights", dweights, on, _F32, (T, k))
     handle = _handle(on, stream)
     if out is None:
-        out = _empty((T, E), (E, 1), dtype=dtype, device=logits.device)
+        out = _like(logits)
     else:
         _want("out", out, on, dtype, (T, E))
     status = (_lib or load()).gmm_route_bwd(dweights.data_ptr(), logits.data_ptr(), kind, ids.data_ptr(), T, E, k, how,
@@ -1097,9 +1097,8 @@ def sort_rows(ids, G, stream=None, out=None):
     if out is None:
         if G < 1:
             raise ValueError(f"G must be at least 1, got {G}")
-        device = ids.device
-        rows = _empty(shape, ids.stride(), dtype=_I32, device=device)
-        sizes = _empty((G,), (1,), dtype=_I32, device=device)
+        rows = _like(ids)
+        sizes = _empty((G,), (1,), dtype=_I32, device=ids.device)
     else:
         rows, sizes = out
         _want("out rows", rows, on, _I32, shape)
@@ -1200,9 +1199,8 @@ def combine_rows_bwd(dout, y, rows, weights, stream=None, out=None):
     _want("weights", weights, on, _F32, (T, k))
     handle = _handle(on, stream)
     if out is None:
-        device = dout.device
-        dy = _empty((M, K), (K, 1), dtype=_BF16, device=device)
-        dweights = _empty((T, k), (k, 1), dtype=_F32, device=device)
+        dy = _like(y)
+        dweights = _like(weights)
     else:
         dy, dweights = out
         _want("out dy", dy, on, _BF16, (M, K))
@@ -1258,9 +1256,8 @@ def norm_join(x, b=None, w_post=None, gate=None, w_next=None, residual_scale=1.0
         raise ValueError("without b and w_next there is nothing to compute")
     handle = _handle(on, stream)
     if out is None:
-        device = x.device
-        o = x if b is None else _empty((T, K), (K, 1), dtype=dtype, device=device)
-        n = None if w_next is None else _empty((T, K), (K, 1), dtype=_BF16, device=device)
+        o = x if b is None else _like(x)
+        n = None if w_next is None else _like(b) if b is not None else _empty((T, K), (K, 1), dtype=_BF16, device=x.device)
     else:
         o, n = out
         if b is None:
@@ -1301,10 +1298,9 @@ def norm_join_bwd(dout, dn, out, b=None, w_post=None, gate=None, w_next=None, re
             raise ValueError("dn is the gradient of n: pass w_next")
     full = _need_join(on, T, K, b, w_post, gate, w_next)
     handle = _handle(on, stream)
-    device = out.device
     if into is None:
-        dx = _empty((T, K), (K, 1), dtype=dtype, device=device)
-        db = None if b is None else _empty((T, K), (K, 1), dtype=_BF16, device=device)
+        dx = _like(out)
+        db = None if b is None else _like(b)
     else:
         dx, db = into
         _want("into dx", dx, on, dtype, (T, K))
@@ -1312,15 +1308,12 @@ def norm_join_bwd(dout, dn, out, b=None, w_post=None, gate=None, w_next=None, re
             db = None
         else:
             _want("into db", db, on, _BF16, (T, K))
-    dw_post = None if w_post is None else _empty((K,), (1,), dtype=_F32, device=device)
-    dw_next = None if w_next is None else _empty((K,), (1,), dtype=_F32, device=device)
-    dgate = None
-    if gate is not None:
-        dgate = (_empty((T, K), (K, 1), dtype=_BF16, device=device) if full
-                 else _empty((K,), (1,), dtype=_F32, device=device))
+    dw_post = None if w_post is None else _like(w_post)
+    dw_next = None if w_next is None else _like(w_next)
+    dgate = None if gate is None else _like(gate)
     lib = _lib or load()
     nbytes = lib.gmm_norm_join_bwd_scratch_bytes(T, K)
-    scratch = _empty((nbytes,), (1,), dtype=torch.uint8, device=device) if nbytes else None
+    scratch = _empty((nbytes,), (1,), dtype=torch.uint8, device=out.device) if nbytes else None
     status = lib.gmm_norm_join_bwd(_at(dout), _at(dn), out.data_ptr(), kind, _at(b), _at(w_post), _at(gate), full,
                                    _at(w_next), T, K, residual_scale, block_scale, eps, dx.data_ptr(), _at(db),
                                    _at(dw_post), _at(dgate), _at(dw_next), _at(scratch), nbytes, handle)

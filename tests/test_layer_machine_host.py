@@ -127,6 +127,7 @@ def machine(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: now[-1].cuda_stream, raising=False)
     monkeypatch.setattr(g, "_current_device", lambda: HERE)
     monkeypatch.setattr(g, "_empty", empty)
+    monkeypatch.setattr(g, "_like", lambda t: empty(t.shape, None, t.dtype, t.device))
     monkeypatch.setattr(g, "_lib", Library(log))
     for name in ("data_ptr", "is_contiguous", "get_device"):
         monkeypatch.setattr(g, "_" + name, lambda t, _n=name: getattr(t, _n)())
