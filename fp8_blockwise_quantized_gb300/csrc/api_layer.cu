@@ -3,9 +3,9 @@
 // Nothing here allocates device memory or synchronizes.
 #include <cuda_runtime.h>
 
-#include <cmath>
+#include <algorithm>
 #include <cstdint>
-#include <new>
+#include <utility>
 #include <vector>
 
 #include "gmm.h"
@@ -70,6 +70,36 @@ gmm_status check_join(int64_t T, int64_t K, gmm_type type, const void* b, const 
   if (T < 0 || T > INT32_MAX || check_columns(K, 8) != GMM_OK || K > kMaxNormColumns) return GMM_ERR_SHAPE;
   if ((type != GMM_BF16 && type != GMM_F32) || !(eps >= 0.0f)) return GMM_ERR_UNSUPPORTED;
   return T > 0 && !b && (w_post || gate) ? GMM_ERR_NULL : GMM_OK;  // without tokens b has no address
+}
+
+// Whether an output shares memory with another one, or with a gradient that is not its
+// own: the CTAs would scale it twice, or read it scaled.
+bool outputs_overlap(const std::vector<ClipTensor>& t) {
+  using Range = std::pair<uintptr_t, uintptr_t>;
+  const auto range = [](const ClipTensor& c, const void* p) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return Range(at, at + static_cast<uintptr_t>(c.count) * (c.f32 ? 4 : 2));
+  };
+  std::vector<Range> out;
+  out.reserve(t.size());
+  bool elsewhere = false;
+  for (const ClipTensor& c : t) {
+    out.push_back(range(c, c.dst));
+    elsewhere |= c.dst != c.src;
+  }
+  std::sort(out.begin(), out.end());
+  for (size_t i = 1; i < out.size(); ++i)
+    if (out[i].first < out[i - 1].second) return true;
+  if (!elsewhere) return false;
+  for (const ClipTensor& c : t) {
+    const Range in = range(c, c.src), own = range(c, c.dst);
+    // the first output that ends behind the gradient's start (they are disjoint, so sorted by their ends too)
+    auto it = std::upper_bound(out.begin(), out.end(), in.first,
+                               [](uintptr_t at, const Range& r) { return at < r.second; });
+    for (; it != out.end() && it->first < in.second; ++it)
+      if (!(*it == own && own == in)) return true;
+  }
+  return false;
 }
 
 }  // namespace
@@ -259,20 +289,21 @@ gmm_status gmm_clip_grads(const void* const* grads, void* const* out, const int6
     if (at & (types[i] == GMM_F32 ? 3u : 1u)) return GMM_ERR_ALIGN;
   }
   if (!all_aligned(norm, scratch)) return GMM_ERR_ALIGN;
-  int sms = 0;
-  const gmm_status st = host_device_sms(&sms);
-  if (st != GMM_OK) return st;
-  if (!scratch || scratch_bytes < clip_scratch_bytes(n, sms)) return GMM_ERR_WORKSPACE;
   try {
     std::vector<ClipTensor> t;
     t.reserve(n);
     for (int i = 0; i < n; ++i)
       if (counts[i] > 0)
         t.push_back({grads[i], out ? out[i] : const_cast<void*>(grads[i]), counts[i], types[i] == GMM_F32});
+    if (outputs_overlap(t)) return host_fail(GMM_ERR_UNSUPPORTED, "clip_grads: outputs overlap");
+    int sms = 0;
+    const gmm_status st = host_device_sms(&sms);
+    if (st != GMM_OK) return st;
+    if (!scratch || scratch_bytes < clip_scratch_bytes(n, sms)) return GMM_ERR_WORKSPACE;
     return launched(launch_clip(t.data(), static_cast<int>(t.size()), max_norm, out == nullptr,
                                 scratch, norm, sms, static_cast<cudaStream_t>(stream)),
                     "clip_grads launch");
-  } catch (const std::bad_alloc&) {
+  } catch (...) {
     return host_fail(GMM_ERR_CUDA, "out of host memory");
   }
 }

@@ -568,7 +568,9 @@ gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, 
  * max_norm = +infinity with out = NULL computes the norm only.
  *   grads, out  HOST arrays of n device pointers, aligned to their elements (not to
  *            16 bytes; those that are not go a slower way); out NULL: in place.  A
- *            pointer with count 0 may be NULL.  n may be 0 (norm 0).
+ *            pointer with count 0 may be NULL.  n may be 0 (norm 0).  No output may
+ *            share memory with another, or with a gradient but its own, whole
+ *            (GMM_ERR_UNSUPPORTED): a gradient given twice in place is refused.
  *   counts   HOST array: elements of each tensor;  types  HOST array of gmm_type
  *   norm     fp32 [1], device
  *   scratch  gmm_clip_grads_scratch_bytes(n) bytes; its contents do not matter

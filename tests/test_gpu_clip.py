@@ -133,3 +133,19 @@ def test_runs_repeat_bit_for_bit():
     for _ in range(3):
         assert gmm.clip_grads(grads, 0.5, out=out).item() == first
         assert all(torch.equal(a, b) for a, b in zip(out, kept))
+
+
+def test_outputs_that_share_memory_are_refused_and_gradients_may():
+    g = _grads([1000], [F32])[0]
+    with pytest.raises(gmm.GmmError):
+        gmm.clip_grads([g, g], 1.0)
+    with pytest.raises(gmm.GmmError):
+        gmm.clip_grads([g[:600], g[400:]], 1.0)
+    out = [torch.empty_like(g), torch.empty_like(g)]
+    norm = gmm.clip_grads([g, g], 1.0, out=out).item()  # read twice, written apart
+    want = math.sqrt(2) * g.double().norm().item()
+    assert abs(norm - want) <= R.F32 * want and torch.equal(out[0], out[1])
+    mixed = [g.clone(), g.clone()]
+    kept = torch.empty_like(g)
+    gmm.clip_grads(mixed, 1.0, out=[mixed[0], kept])  # one in place, one not
+    assert torch.equal(mixed[0], out[0]) and torch.equal(kept, out[1]) and torch.equal(mixed[1], g)

@@ -123,7 +123,7 @@ def test_join_bwd_refusals(lib, kw, code):
 
 def _clip(lib, kw):
     n = kw.pop("n", 2)
-    ptrs = kw.pop("grads", [FAKE, FAKE + 6])
+    ptrs = kw.pop("grads", [FAKE, FAKE + 64])
     outs = kw.pop("out", None)
     counts, types = kw.pop("counts", [5, 7]), kw.pop("types", [1, 0])
     arr = lambda t, v: None if v is None else (t * max(1, len(v)))(*v)  # noqa: E731
@@ -137,8 +137,13 @@ def _clip(lib, kw):
     (dict(n=-1), 2), (dict(max_norm=-1.0), 4), (dict(max_norm=math.nan), 4), (dict(norm=None), 1), (dict(grads=None), 1),
     (dict(counts=None), 1), (dict(types=None), 1), (dict(types=[1, 2]), 4), (dict(counts=[5, -1]), 2),
     (dict(counts=[1 << 42, 1]), 2), (dict(grads=[None, FAKE]), 1), (dict(out=[FAKE, None]), 1),
-    (dict(grads=[FAKE + 2, FAKE]), 3), (dict(grads=[FAKE, FAKE + 1]), 3), (dict(out=[FAKE, FAKE + 1]), 3),
-    (dict(norm=FAKE + 4), 3), (dict(scratch=FAKE + 8), 3)])
+    (dict(grads=[FAKE + 2, FAKE + 64]), 3), (dict(grads=[FAKE, FAKE + 65]), 3), (dict(out=[FAKE, FAKE + 65]), 3),
+    (dict(norm=FAKE + 4), 3), (dict(scratch=FAKE + 8), 3),
+    # 5 fp32 values (20 bytes) and 7 bf16 values (14 bytes) that share memory
+    (dict(grads=[FAKE, FAKE]), 4), (dict(grads=[FAKE, FAKE + 18]), 4), (dict(grads=[FAKE + 12, FAKE]), 4),
+    (dict(out=[FAKE, FAKE + 4]), 4), (dict(grads=[FAKE, FAKE + 64], out=[FAKE + 4, FAKE + 64]), 4),
+    (dict(grads=[FAKE, FAKE + 64], out=[FAKE + 64, FAKE]), 4),
+    (dict(grads=[FAKE, FAKE + 64], out=[FAKE + 128, FAKE + 4]), 4)])
 def test_clip_refusals(lib, kw, code):
     assert _clip(lib, dict(kw)) == code
 
