@@ -172,7 +172,7 @@ def load():
     lib.gmm_norm_join_bwd.restype = I
     lib.gmm_norm_join_bwd.argtypes = [P, P, P, I, P, P, P, I, P, I64, I64, F, F, F, P, P, P, P, P, P, SZ, P]
     lib.gmm_clip_grads_scratch_bytes.restype = SZ
-    lib.gmm_clip_grads_scratch_bytes.argtypes = [I]
+    lib.gmm_clip_grads_scratch_bytes.argtypes = [I, I64]
     lib.gmm_clip_grads.restype = I
     lib.gmm_clip_grads.argtypes = [P, P, P, P, I, F, P, P, SZ, P]
     _lib = lib
@@ -420,8 +420,8 @@ def gmm_norm_join_bwd(dout, dn, out, stream_type, b, w_post, gate, gate_rows, w_
                                     _s(stream))
 
 
-def gmm_clip_grads_scratch_bytes(n: int) -> int:
-    return int(load().gmm_clip_grads_scratch_bytes(n))
+def gmm_clip_grads_scratch_bytes(n: int, total: int) -> int:
+    return int(load().gmm_clip_grads_scratch_bytes(n, total))
 
 
 def gmm_clip_grads(grads, out, counts, types, n, max_norm, norm, scratch, scratch_bytes, stream=None) -> int:
@@ -1348,7 +1348,7 @@ def clip_grads(grads, max_norm, out=None, stream=None):
     device = grads[0].device if n else torch.device("cuda", on)
     lib = _lib or load()
     norm = _empty((1,), (1,), dtype=_F32, device=device)
-    nbytes = lib.gmm_clip_grads_scratch_bytes(n)
+    nbytes = lib.gmm_clip_grads_scratch_bytes(n, sum(counts))
     scratch = _empty((nbytes,), (1,), dtype=torch.uint8, device=device) if nbytes else None
     status = lib.gmm_clip_grads(src.buffer_info()[0], None if out is None else dst.buffer_info()[0],
                                 counts.buffer_info()[0], types.buffer_info()[0], n, max_norm, norm.data_ptr(),

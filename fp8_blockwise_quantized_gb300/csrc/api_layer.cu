@@ -268,9 +268,9 @@ gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, 
   return launched(launch_norm_join_bwd(a, sms, static_cast<cudaStream_t>(stream)), "norm_join_bwd launch");
 }
 
-size_t gmm_clip_grads_scratch_bytes(int n) {
+size_t gmm_clip_grads_scratch_bytes(int n, int64_t total) {
   int sms = 0;
-  return n < 0 || host_device_sms(&sms) != GMM_OK ? 0 : clip_scratch_bytes(n, sms);
+  return n < 0 || total < 0 || host_device_sms(&sms) != GMM_OK ? 0 : clip_scratch_bytes(n, total, sms);
 }
 
 gmm_status gmm_clip_grads(const void* const* grads, void* const* out, const int64_t* counts, const int32_t* types,
@@ -299,7 +299,8 @@ gmm_status gmm_clip_grads(const void* const* grads, void* const* out, const int6
     int sms = 0;
     const gmm_status st = host_device_sms(&sms);
     if (st != GMM_OK) return st;
-    if (!scratch || scratch_bytes < clip_scratch_bytes(n, sms)) return GMM_ERR_WORKSPACE;
+    const size_t need = clip_scratch_bytes(n, total, sms);
+    if (need && (!scratch || scratch_bytes < need)) return GMM_ERR_WORKSPACE;
     return launched(launch_clip(t.data(), static_cast<int>(t.size()), max_norm, out == nullptr,
                                 scratch, norm, sms, static_cast<cudaStream_t>(stream)),
                     "clip_grads launch");

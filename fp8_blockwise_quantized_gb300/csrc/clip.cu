@@ -9,7 +9,11 @@
 // Sums are fp32, compensated from chunk to chunk, while every square keeps its bits
 // there; a CTA that meets a sum outside that range adds its values up in double, of
 // which this GPU does two a cycle and SM (sums in double throughout: 19.7 us for 60
-// tensors of 3 M values).
+// tensors of 3 M values, for 8.6).
+//
+// A few values are one launch's: a cluster's CTAs, which read each other's sums and
+// keep their chunks' values in the caches.  It saves the host a launch and the caller
+// the scratch.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -19,7 +23,9 @@ namespace gmm {
 
 namespace {
 
-constexpr int kThreads = 256;
+// A chunk is 256 threads' at a time: a CTA's, or in the one launch for a few values a
+// quarter of a CTA's.
+constexpr int kThreads = 256, kOneThreads = 1024, kOneCtas = 8;
 
 template <int N>
 struct ClipTable {
@@ -70,7 +76,7 @@ __device__ __forceinline__ bool in_range(float s) { return s >= 1e-25f && s <= 1
 
 // This thread's share of a chunk's squares; *some: whether it has a value but 0.
 template <typename T>
-__device__ float squares_of(const T* __restrict__ p, int n, bool* some_out) {
+__device__ float squares_of(const T* __restrict__ p, int n, int tid, bool* some_out) {
   constexpr int W = 16 / sizeof(T);
   float s = 0.0f;
   uint32_t some = 0;
@@ -81,7 +87,7 @@ __device__ float squares_of(const T* __restrict__ p, int n, bool* some_out) {
     uint4 u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * kThreads + threadIdx.x;
+      const int i = i0 + j * kThreads + tid;
       u[j] = i < nv ? __ldg(v + i) : make_uint4(0, 0, 0, 0);
     }
     float a[4];
@@ -103,7 +109,7 @@ __device__ float squares_of(const T* __restrict__ p, int n, bool* some_out) {
     }
     s += (a[0] + a[1]) + (a[2] + a[3]);
   }
-  for (int i = nv * W + threadIdx.x; i < n; i += kThreads) {
+  for (int i = nv * W + tid; i < n; i += kThreads) {
     const float f = value_of(p, i);
     some |= __float_as_uint(f);
     s = fmaf(f, f, s);
@@ -113,9 +119,9 @@ __device__ float squares_of(const T* __restrict__ p, int n, bool* some_out) {
 }
 
 template <typename T>
-__device__ double squares_in_double(const T* __restrict__ p, int n) {
+__device__ double squares_in_double(const T* __restrict__ p, int n, int tid) {
   double d = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = tid; i < n; i += kThreads) {
     const double f = value_of(p, i);
     d += f * f;
   }
@@ -130,8 +136,7 @@ __device__ __forceinline__ T block_sum(T v, T* red) {
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   T s = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += red[w];
   return s;
 }
 
@@ -141,19 +146,24 @@ struct Parts {
   float* sum;
 };
 
+// Sum over the CTA of the squares of every `step`th chunk from `first` on (which may
+// differ between its 256s of threads): fp32, or NaN where it is out of range; and double.
+struct Sum {
+  float sum;
+  double exact;
+};
 template <int N>
-__global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_constant__ ClipTable<N> tab, Parts parts) {
-  __shared__ float red[kThreads / 32];
-  __shared__ double red_exact[kThreads / 32];
-  griddep_launch_dependents();
-  griddep_wait();
+__device__ __forceinline__ Sum sum_chunks(const ClipTable<N>& tab, int first, int step) {
+  __shared__ float red[32];
+  __shared__ double red_exact[32];
+  const int tid = threadIdx.x & (kThreads - 1);
   float s = 0.0f, lost = 0.0f;  // compensated
   bool odd = false;
-  for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
+  for (int c = first; c < tab.first[tab.n]; c += step) {
     const Piece p = piece_of(tab, c);
     bool some;
-    const float add = (p.f32 ? squares_of(static_cast<const float*>(p.src) + p.at, p.n, &some)
-                             : squares_of(static_cast<const uint16_t*>(p.src) + p.at, p.n, &some));
+    const float add = p.f32 ? squares_of(static_cast<const float*>(p.src) + p.at, p.n, tid, &some)
+                            : squares_of(static_cast<const uint16_t*>(p.src) + p.at, p.n, tid, &some);
     odd |= some && !in_range(add);
     const float y = add - lost, t = s + y;
     lost = (t - s) - y;
@@ -161,28 +171,31 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_consta
   }
   if (!__syncthreads_or(odd)) {
     s = block_sum(s, red);
-    if (threadIdx.x == 0) {
-      parts.sum[blockIdx.x] = s;
-      parts.exact[blockIdx.x] = s;
-    }
-    return;
+    return {s, s};
   }
   double d = 0.0;
-  for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
+  for (int c = first; c < tab.first[tab.n]; c += step) {
     const Piece p = piece_of(tab, c);
-    d += p.f32 ? squares_in_double(static_cast<const float*>(p.src) + p.at, p.n)
-               : squares_in_double(static_cast<const uint16_t*>(p.src) + p.at, p.n);
+    d += p.f32 ? squares_in_double(static_cast<const float*>(p.src) + p.at, p.n, tid)
+               : squares_in_double(static_cast<const uint16_t*>(p.src) + p.at, p.n, tid);
   }
-  d = block_sum(d, red_exact);
+  return {__int_as_float(0x7fc00000), block_sum(d, red_exact)};
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_constant__ ClipTable<N> tab, Parts parts) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const Sum s = sum_chunks(tab, blockIdx.x, gridDim.x);
   if (threadIdx.x == 0) {
-    parts.sum[blockIdx.x] = __int_as_float(0x7fc00000);  // NaN: not in range
-    parts.exact[blockIdx.x] = d;
+    parts.sum[blockIdx.x] = s.sum;
+    parts.exact[blockIdx.x] = s.exact;
   }
 }
 
 // dst = src * by; a factor of 1 copies the bits (a product would give NaNs another payload).
 template <typename T>
-__device__ void scale_piece(const T* src, T* dst, int n, float by) {
+__device__ void scale_piece(const T* src, T* dst, int n, float by, int tid) {
   const bool copy = by == 1.0f;
   constexpr int W = 16 / sizeof(T);
   const bool wide = ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15u) == 0;
@@ -193,12 +206,12 @@ __device__ void scale_piece(const T* src, T* dst, int n, float by) {
     uint4 u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * kThreads + threadIdx.x;
+      const int i = i0 + j * kThreads + tid;
       if (i < nv) u[j] = v[i];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * kThreads + threadIdx.x;
+      const int i = i0 + j * kThreads + tid;
       if (i >= nv) continue;
       if (copy) {
         __stcs(o + i, u[j]);
@@ -219,7 +232,22 @@ __device__ void scale_piece(const T* src, T* dst, int n, float by) {
       }
     }
   }
-  for (int i = nv * W + threadIdx.x; i < n; i += kThreads) if (copy) dst[i] = src[i]; else put(dst, i, value_of(src, i) * by);
+  for (int i = nv * W + tid; i < n; i += kThreads) if (copy) dst[i] = src[i]; else put(dst, i, value_of(src, i) * by);
+}
+
+// The factor; a norm that is not finite scales nothing.
+__device__ __forceinline__ float factor_of(float norm, float max_norm) {
+  return norm > max_norm && norm <= 3.402823466e38f ? max_norm / norm : 1.0f;
+}
+
+template <int N>
+__device__ __forceinline__ void scale_chunk(const ClipTable<N>& tab, int c, float by) {
+  const Piece p = piece_of(tab, c);
+  const int tid = threadIdx.x & (kThreads - 1);
+  if (p.f32)
+    scale_piece(static_cast<const float*>(p.src) + p.at, static_cast<float*>(p.dst) + p.at, p.n, by, tid);
+  else
+    scale_piece(static_cast<const uint16_t*>(p.src) + p.at, static_cast<uint16_t*>(p.dst) + p.at, p.n, by, tid);
 }
 
 template <int N>
@@ -246,16 +274,51 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
     whole = static_cast<float>(sqrt(block_sum(d, red_exact)));
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
-  // a norm that is not finite scales nothing
-  const float by = whole > max_norm && whole <= 3.402823466e38f ? max_norm / whole : 1.0f;
+  const float by = factor_of(whole, max_norm);
   if (in_place && by == 1.0f) return;
-  for (int c = tab.first[tab.n] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
-    const Piece p = piece_of(tab, c);
-    if (p.f32)
-      scale_piece(static_cast<const float*>(p.src) + p.at, static_cast<float*>(p.dst) + p.at, p.n, by);
-    else
-      scale_piece(static_cast<const uint16_t*>(p.src) + p.at, static_cast<uint16_t*>(p.dst) + p.at, p.n, by);
+  for (int c = tab.first[tab.n] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) scale_chunk(tab, c, by);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kOneThreads) clip_one_kernel(const __grid_constant__ ClipTable<N> tab, float max_norm,
+                                                               int in_place, float* __restrict__ norm) {
+  __shared__ float sum;
+  __shared__ double exact;
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int kStep = kOneCtas * (kOneThreads / kThreads);
+  const int first = (threadIdx.x / kThreads) * kOneCtas + blockIdx.x;
+  const Sum own = sum_chunks(tab, first, kStep);
+  if (threadIdx.x == 0) {
+    sum = own.sum;
+    exact = own.exact;
   }
+  __syncwarp();
+  cluster_sync_all();
+  float s = 0.0f;
+  double d = 0.0;
+  bool odd = false;
+#pragma unroll
+  for (int c = 0; c < kOneCtas; ++c) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&sum), c)));
+    odd |= v != 0.0f && !in_range(v);
+    s += v;
+  }
+  if (odd) {
+    for (int c = 0; c < kOneCtas; ++c) {
+      double v;
+      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(smem_u32(&exact), c)));
+      d += v;
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // the other CTAs' sums have been read: none of them leaves before
+  const float whole = odd ? static_cast<float>(sqrt(d)) : sqrtf(s);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
+  const float by = factor_of(whole, max_norm);
+  if (in_place && by == 1.0f) return;
+  for (int c = first; c < tab.first[tab.n]; c += kStep) scale_chunk(tab, c, by);
 }
 
 constexpr int kSmallTable = 64, kLargeTable = 1000;  // 1.9 and 28.2 KB of parameters
@@ -310,17 +373,36 @@ int clip_ctas(int sms) { return 8 * sms; }
 int clip_launches(int n) { return n <= kSmallTable ? 1 : (n + kLargeTable - 1) / kLargeTable; }
 }  // namespace
 
-size_t clip_scratch_bytes(int n, int sms) {
+// What one cluster takes: 262144 values are 8 us of its device time.
+constexpr int64_t kOneValues = 1 << 18;
+
+size_t clip_scratch_bytes(int n, int64_t total, int sms) {
+  if (n <= kSmallTable && total <= kOneValues) return 0;
   return static_cast<size_t>(clip_launches(n)) * clip_ctas(sms) * (sizeof(double) + sizeof(float));
 }
 
 cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, void* scratch, float* norm, int sms,
                         cudaStream_t stream) {
+  long long total = 0;
+  for (int i = 0; i < n; ++i) total += t[i].count;
+  if (n <= kSmallTable && total <= kOneValues) {
+    ClipTable<kSmallTable> tab;
+    fill(tab, t, n, 4096);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kOneCtas);
+    cfg.blockDim = dim3(kOneThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kOneCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, clip_one_kernel<kSmallTable>, tab, max_norm, static_cast<int>(in_place), norm);
+  }
   Parts parts;
   parts.exact = static_cast<double*>(scratch);
   parts.sum = reinterpret_cast<float*>(parts.exact + static_cast<size_t>(clip_launches(n)) * clip_ctas(sms));
-  long long total = 0;
-  for (int i = 0; i < n; ++i) total += t[i].count;
   // some eight chunks a CTA, of 4096 values at least and 32768 at most
   const int most = clip_ctas(sms);
   long long chunk = (total / (8LL * most) + 4095) / 4096 * 4096;

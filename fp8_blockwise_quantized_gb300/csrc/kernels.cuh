@@ -269,7 +269,7 @@ struct ClipTensor {
   int64_t count;
   int f32;
 };
-size_t clip_scratch_bytes(int n, int sms);
+size_t clip_scratch_bytes(int n, int64_t total, int sms);
 cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, void* scratch, float* norm, int sms,
                         cudaStream_t stream);
 

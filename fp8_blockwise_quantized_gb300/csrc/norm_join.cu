@@ -14,7 +14,7 @@
 // of two values for five exchanges, loads without predicates.  At 8192 x 2048 (floor
 // at the measured copy rate in brackets): forward 20.9 us (20.1) with a bf16 stream,
 // 33.5 (30.2) with an fp32 stream and a gate per column; backward 39.4 (30.2) and 52.6
-// (45.2), 8 of them the sums over the rows.  The next row's values are on their way to
+// (45.2), 5 of them the sums over the rows.  The next row's values are on their way to
 // registers while a row is worked on: through shared memory (asynchronous copies, two
 // to six rows ahead) they pass the SM's load path twice, and the same calls took 22.0,
 // 40.2, 42.1 and 71.4 us; rows asked for in the L2 further ahead, 22.6 to 25.6 and
@@ -267,10 +267,22 @@ __device__ __forceinline__ void row_to_l2(const void* p, int bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+constexpr int kOneCtas = 8;
+
+// The parameters' gradients of column c from its two sums.
+__device__ __forceinline__ void put_columns(const NormJoinBwdArgs& a, int c, float post, float next) {
+  if (a.dw_post) a.dw_post[c] = a.beta * post * (a.gate_col ? a.gate_col[c] : 1.0f);
+  if (a.dgate_col) a.dgate_col[c] = a.beta * post * (a.w_post ? a.w_post[c] : 1.0f);
+  if (a.dw_next) a.dw_next[c] = next;
+}
+
 // V = 2 (over 4096 columns): the registers hold the sums, but neither the factors,
 // which come from the cache for each row, nor the row ahead.
-template <typename S, int V, int NT, bool FULL>
+// ONE: few rows are one cluster's, whose CTAs add up each other's sums; no parts and no
+// second kernel.
+template <typename S, int V, int NT, bool FULL, bool ONE>
 __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwdArgs a) {
+  static_assert(V == 1 || !ONE, "a thread's columns are 8 words of shared memory a sum");
   constexpr bool kHeld = V == 1;
   __shared__ SumBuffer red;
   griddep_launch_dependents();
@@ -398,6 +410,29 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
       }
     }
   }
+  if constexpr (ONE) {
+    __shared__ __align__(16) float cols[2][8 * NT];
+    put8(&cols[0][8 * threadIdx.x], sb[0]);
+    put8(&cols[1][8 * threadIdx.x], sn[0]);
+    __syncwarp();
+    cluster_sync_all();
+    for (int c = static_cast<int>(blockIdx.x) * NT + threadIdx.x; c < a.K; c += kOneCtas * NT) {
+      float post = 0.0f, next = 0.0f;
+      for (int cta = 0; cta < kOneCtas; ++cta)
+        for (int team = 0; team < me.rows; ++team) {
+          const uint32_t at = mapa_shared(smem_u32(&cols[0][8 * a.row_threads * team + c]), cta);
+          float p, n;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(at));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(n) : "r"(at + static_cast<uint32_t>(sizeof(cols[0]))));
+          post += p;
+          next += n;
+        }
+      put_columns(a, c, post, next);
+    }
+    __syncwarp();
+    cluster_sync_all();  // none of the CTAs leaves before its sums have been read
+    return;
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (!on[v]) continue;
@@ -461,6 +496,11 @@ struct Shape {
 // take over 512 threads.
 constexpr int kForward = 2;
 int backward_vectors(int64_t K) { return K > 8 * 512 ? 2 : 1; }
+// Rows that the backward pass gives one cluster: up to eight a CTA (and row of a CTA).
+bool one_cluster(int64_t T, int64_t K) {
+  const int row_threads = static_cast<int>((K / 8 + 31) / 32 * 32);
+  return T > 0 && row_threads <= 512 && T <= 8 * kOneCtas * (row_threads <= 256 ? 256 / row_threads : 1);
+}
 
 template <typename S, bool FULL>
 cudaError_t forward(const NormJoinArgs& a, const Shape& sh, cudaStream_t stream) {
@@ -471,16 +511,31 @@ cudaError_t forward(const NormJoinArgs& a, const Shape& sh, cudaStream_t stream)
 }
 template <typename S, bool FULL>
 cudaError_t backward(const NormJoinBwdArgs& a, const Shape& sh, bool over, cudaStream_t stream) {
+  if (one_cluster(a.T, a.K)) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kOneCtas);
+    cfg.blockDim = dim3(sh.threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kOneCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return sh.threads == 256 ? cudaLaunchKernelEx(&cfg, norm_join_bwd_kernel<S, 1, 256, FULL, true>, a)
+                             : cudaLaunchKernelEx(&cfg, norm_join_bwd_kernel<S, 1, 512, FULL, true>, a);
+  }
   if (backward_vectors(a.K) == 2)
-    return launch_short(over, norm_join_bwd_kernel<S, 2, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
+    return launch_short(over, norm_join_bwd_kernel<S, 2, 512, FULL, false>, dim3(sh.grid), dim3(512), 0, stream, a);
   return sh.threads == 256
-             ? launch_short(over, norm_join_bwd_kernel<S, 1, 256, FULL>, dim3(sh.grid), dim3(256), 0, stream, a)
-             : launch_short(over, norm_join_bwd_kernel<S, 1, 512, FULL>, dim3(sh.grid), dim3(512), 0, stream, a);
+             ? launch_short(over, norm_join_bwd_kernel<S, 1, 256, FULL, false>, dim3(sh.grid), dim3(256), 0, stream, a)
+             : launch_short(over, norm_join_bwd_kernel<S, 1, 512, FULL, false>, dim3(sh.grid), dim3(512), 0, stream, a);
 }
 
 }  // namespace
 
 int norm_join_parts(int64_t T, int64_t K, int sms) {
+  if (one_cluster(T, K)) return 0;
   const Shape sh(T, K, backward_vectors(K), sms);
   return sh.grid * sh.teams;
 }
@@ -505,7 +560,7 @@ cudaError_t launch_norm_join_bwd(const NormJoinBwdArgs& args, int sms, cudaStrea
     else
       e = a.f32 ? backward<float, false>(a, sh, over, stream) : backward<uint16_t, false>(a, sh, over, stream);
   }
-  if (e != cudaSuccess || !(a.dw_post || a.dgate_col || a.dw_next)) return e;
+  if (e != cudaSuccess || one_cluster(a.T, a.K) || !(a.dw_post || a.dgate_col || a.dw_next)) return e;
   return launch_short(over, norm_join_reduce_kernel, dim3(static_cast<unsigned>(a.K / 8), 2), dim3(256), 0, stream,
                     static_cast<const float*>(a.parts), sh.grid * sh.teams, static_cast<int>(a.K), a.beta, a.w_post,
                     a.gate_col, a.dw_post, a.dgate_col, a.dw_next);

@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const uint4* __restrict__ x
 
 // The same with the 1x128 e4m3 quantisation of gmm_quantize_lhs in between: each
 // token is quantised once, whatever its number of places.  Eight lanes take a
-// block of 128 values.
+// block of 128 values.  8192 tokens of 8 choices, 2048 columns: 29.5 us (floor 25.8);
+// what it has beyond the floor are the scales, 4 bytes a sector here and there.
 template <typename I>
 __global__ void __launch_bounds__(256) gather_quantize_kernel(const uint4* __restrict__ x,
                                                               const int32_t* __restrict__ rows, I units, int k,
@@ -227,9 +228,16 @@ __global__ void __launch_bounds__(256) gather_quantize_kernel(const uint4* __res
   const unsigned kb = static_cast<unsigned>(u - t * KB);
   uint4 a = make_uint4(0, 0, 0, 0), b = a;
   const int32_t* at = rows + static_cast<long long>(t) * k;
-  bool any = false;  // a token that no expert has is not read
+  // a token that no expert has is not read; the first eight places are kept
+  int first[8];
+  bool any = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    first[j] = live && j < k ? __ldg(at + j) : INT32_MIN;
+    any |= first[j] >= 0;
+  }
   if (live)
-    for (int j = 0; j < k; ++j) any |= __ldg(at + j) >= 0;
+    for (int j = 8; j < k; ++j) any |= __ldg(at + j) >= 0;
   if (any) {
     a = __ldcs(x + 2 * static_cast<long long>(v));
     b = __ldcs(x + 2 * static_cast<long long>(v) + 1);
@@ -242,14 +250,24 @@ __global__ void __launch_bounds__(256) gather_quantize_kernel(const uint4* __res
   e4m3_block_scale(m, s, inv);
   const uint2 qa = bf16x8_to_e4m3(a, inv), qb = bf16x8_to_e4m3(b, inv);
   const uint4 q = make_uint4(qa.x, qa.y, qb.x, qb.y);
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int row = __ldg(at + j);
+  auto send = [&](int row, int j) {
     const long long p = place_of(row, M);
-    if (p < 0) continue;
+    if (p < 0) return;
     xq[(p * KB + kb) * 8 + l8] = row >= 0 ? q : make_uint4(0, 0, 0, 0);
-    if (l8 == (j & 7)) xs[kb * M + p] = row >= 0 ? s : 0.0f;
+    if (j >= 8 && l8 == (j & 7)) xs[kb * M + p] = row >= 0 ? s : 0.0f;
+  };
+  int own = first[0];  // each of the eight lanes writes one choice's scale
+#pragma unroll
+  for (int j = 1; j < 8; ++j)
+    if (l8 == j) own = first[j];
+  const long long po = place_of(own, M);
+  if (po >= 0) xs[kb * M + po] = own >= 0 ? s : 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j >= k) break;
+    send(first[j], j);
   }
+  for (int j = 8; j < k; ++j) send(__ldg(at + j), j);
 }
 
 // ---- sorted rows -> tokens --------------------------------------------------------

@@ -573,10 +573,11 @@ gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, 
  *            (GMM_ERR_UNSUPPORTED): a gradient given twice in place is refused.
  *   counts   HOST array: elements of each tensor;  types  HOST array of gmm_type
  *   norm     fp32 [1], device
- *   scratch  gmm_clip_grads_scratch_bytes(n) bytes; its contents do not matter
+ *   scratch  gmm_clip_grads_scratch_bytes(n, total) bytes, total being the sum of
+ *            counts, or NULL where that is 0; its contents do not matter
  * The host arrays are read before the call returns.
  */
-size_t gmm_clip_grads_scratch_bytes(int n);
+size_t gmm_clip_grads_scratch_bytes(int n, int64_t total);
 gmm_status gmm_clip_grads(const void* const* grads, void* const* out, const int64_t* counts, const int32_t* types,
                           int n, float max_norm, float* norm, void* scratch, size_t scratch_bytes, void* stream);
 

@@ -37,7 +37,7 @@ def _check(grads, max_norm, in_place):
 
 
 LISTS = [[1], [7], [8, 1, 0, 4096, 4097], [0], [3, 100000, 5], [33000] * 70, list(range(1, 200)), [1] * 1500,
-         [40000000, 3], [257] * 2003]
+         [40000000, 3], [257] * 2003, [262144], [262143, 1], [262144, 1], [8191] * 32]
 
 
 @pytest.mark.parametrize("counts", LISTS, ids=lambda c: f"{len(c)}x{max(c)}")

@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
 EPS = 1e-5
-SIZES = [(1, 8), (2, 264), (16, 2048), (5, 4096), (3, 4104), (4, 8192), (7, 72), (1031, 1000), (2100, 256), (400, 5120)]
+SIZES = [(1, 8), (64, 2048), (65, 2048), (512, 256), (513, 256), (64, 4096), (31, 2304), (2, 264), (16, 2048), (5, 4096), (3, 4104), (4, 8192), (7, 72), (1031, 1000), (2100, 256), (400, 5120)]
 
 
 def _case(T, K, stream, post, gate, seed=0):
