@@ -256,12 +256,6 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_kernel(NormJoinArgs a)
   }
 }
 
-// With c = dn * w_next, D = dout + ro c - out ro^3 / K sum(c out); dx = alpha D.
-// With p = beta * w_post * gate, b's gradient is that of its norm from t = D p:
-// db = rb t - b rb^3 / K sum(t b).  With s = sum over the rows of D b rb (times a
-// gate per element), dw_post = beta gate s and a column gate's gradient beta w_post s:
-// one sum for both, a part of it a CTA row (and of dw_next's), joined by
-// norm_join_reduce_kernel.
 // A row of an input on its way to the L2, asked for by one thread.
 __device__ __forceinline__ void row_to_l2(const void* p, int bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -276,6 +270,13 @@ __device__ __forceinline__ void put_columns(const NormJoinBwdArgs& a, int c, flo
   if (a.dw_next) a.dw_next[c] = next;
 }
 
+// With c = dn * w_next, D = dout + ro c - out ro^3 / K sum(c out); dx = alpha D.
+// With p = beta * w_post * gate, b's gradient is that of its norm from t = D p:
+// db = rb t - b rb^3 / K sum(t b).  With s = sum over the rows of D b rb (times a
+// gate per element), dw_post = beta gate s and a column gate's gradient beta w_post s:
+// one sum for both, a part of it a CTA row (and of dw_next's), joined by
+// norm_join_reduce_kernel.
+//
 // V = 2 (over 4096 columns): the registers hold the sums, but neither the factors,
 // which come from the cache for each row, nor the row ahead.
 // ONE: few rows are one cluster's, whose CTAs add up each other's sums; no parts and no

@@ -1,5 +1,5 @@
-// Row vectors of the layer's memory-bound kernels: 8 values a thread at a time,
-// held in fp32, and the warp sums they share.
+// What the layer's memory-bound kernels share: 8 bf16 values of a 16-byte word in
+// fp32, and warp sums.
 #pragma once
 
 #include <cstdint>
@@ -19,46 +19,6 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                     pack_bf16x2(f[6], f[7]));
-}
-
-// Eight consecutive values as they lie in memory: one or two 16-byte words.
-struct Raw8Bf16 {
-  uint4 v;
-  __device__ __forceinline__ void load(const uint16_t* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(v, f); }
-};
-struct Raw8F32 {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  }
-};
-template <typename T>
-struct RawOf;
-template <>
-struct RawOf<uint16_t> {
-  using type = Raw8Bf16;
-};
-template <>
-struct RawOf<float> {
-  using type = Raw8F32;
-};
-
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) { *reinterpret_cast<uint4*>(p) = pack8(f); }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-// Eight fp32 parameters that many rows share (through the read-only cache).
-__device__ __forceinline__ void load_params8(const float* p, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -536,7 +536,8 @@ gmm_status gmm_combine_rows_bwd(const void* dout, const void* y, const int32_t* 
  *   x, out  bf16 or fp32 (stream_type) [T, K];  b, n  bf16 [T, K]
  *   w_post, w_next  fp32 [K]
  *   gate    gate_rows = 0: fp32 [K], one value per column; gate_rows = 1: bf16 [T, K]
- * out may be x; n may be b.  eps >= 0.
+ * out may be x; n may be b.  eps >= 0.  The squares are summed in fp32: a row's sum has
+ * to stay below 3.4e38, and with eps = 0 a row of zeros gives NaN.
  */
 gmm_status gmm_norm_join(const void* x, gmm_type stream_type, const void* b, const float* w_post, const void* gate,
                          int gate_rows, const float* w_next, int64_t T, int64_t K, float residual_scale,
@@ -550,7 +551,8 @@ gmm_status gmm_norm_join(const void* x, gmm_type stream_type, const void* b, con
  *   out  the forward's out (b NULL: its x), read when dn is given
  * dx may be NULL, and any of dw_post, dgate (gate_rows = 0), dw_next; what is not
  * NULL is written (dw_next as zeros without dn).  dx may be dout, db may be dn or b.
- *   scratch  gmm_norm_join_bwd_scratch_bytes(T, K) bytes; its contents do not matter
+ *   scratch  gmm_norm_join_bwd_scratch_bytes(T, K) bytes, or NULL where that is 0; its
+ *            contents do not matter
  */
 size_t gmm_norm_join_bwd_scratch_bytes(int64_t T, int64_t K);
 gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, gmm_type stream_type, const void* b,

@@ -149,3 +149,15 @@ def test_outputs_that_share_memory_are_refused_and_gradients_may():
     kept = torch.empty_like(g)
     gmm.clip_grads(mixed, 1.0, out=[mixed[0], kept])  # one in place, one not
     assert torch.equal(mixed[0], out[0]) and torch.equal(kept, out[1]) and torch.equal(mixed[1], g)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_negative_zeros_and_tiny_values_beside_others(dtype):
+    """-0 is nothing; what vanishes beside the rest may, and what stands alone may not."""
+    z = torch.zeros(300000, dtype=dtype, device="cuda").neg()
+    tiny = torch.full((300000,), 1e-22, dtype=dtype, device="cuda")
+    one = torch.ones(1, dtype=dtype, device="cuda")
+    assert gmm.clip_grads([z], math.inf).item() == 0.0
+    assert gmm.clip_grads([z, one, tiny], math.inf).item() == 1.0
+    want = _norm([tiny])
+    assert abs(gmm.clip_grads([z, tiny], math.inf).item() - want) <= R.F32 * want
