@@ -274,7 +274,7 @@ __device__ __forceinline__ void put_columns(const NormJoinBwdArgs& a, int c, flo
 // With p = beta * w_post * gate, b's gradient is that of its norm from t = D p:
 // db = rb t - b rb^3 / K sum(t b).  With s = sum over the rows of D b rb (times a
 // gate per element), dw_post = beta gate s and a column gate's gradient beta w_post s:
-// one sum for both, a part of it a CTA row (and of dw_next's), joined by
+// one sum for both, a part of it a CTA (and of dw_next's), joined by
 // norm_join_reduce_kernel.
 //
 // V = 2 (over 4096 columns): the registers hold the sums, but neither the factors,
@@ -434,10 +434,29 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
     cluster_sync_all();  // none of the CTAs leaves before its sums have been read
     return;
   }
+  if constexpr (NT == 256) {
+    if (me.rows > 1) {  // the CTA's rows, joined in their order
+      __shared__ __align__(16) float cols[2][8 * NT];
+      put8(&cols[0][8 * threadIdx.x], sb[0]);
+      put8(&cols[1][8 * threadIdx.x], sn[0]);
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.K; c += NT) {
+        float post = 0.0f, next = 0.0f;
+        for (int team = 0; team < me.rows; ++team) {
+          post += cols[0][8 * a.row_threads * team + c];
+          next += cols[1][8 * a.row_threads * team + c];
+        }
+        float* p = a.parts + static_cast<long long>(blockIdx.x) * 2 * a.K + c;
+        p[0] = post;
+        p[a.K] = next;
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (!on[v]) continue;
-    float* p = a.parts + (static_cast<long long>(blockIdx.x) * me.rows + me.team) * 2 * a.K + col[v];
+    float* p = a.parts + static_cast<long long>(blockIdx.x) * 2 * a.K + col[v];
     if (a.dw_post || a.dgate_col) put8(p, sb[v]);
     if (a.dw_next) put8(p + a.K, sn[v]);
   }
@@ -538,7 +557,7 @@ cudaError_t backward(const NormJoinBwdArgs& a, const Shape& sh, bool over, cudaS
 int norm_join_parts(int64_t T, int64_t K, int sms) {
   if (one_cluster(T, K)) return 0;
   const Shape sh(T, K, backward_vectors(K), sms);
-  return sh.grid * sh.teams;
+  return sh.grid;
 }
 
 cudaError_t launch_norm_join(const NormJoinArgs& args, int sms, cudaStream_t stream) {
@@ -563,7 +582,7 @@ cudaError_t launch_norm_join_bwd(const NormJoinBwdArgs& args, int sms, cudaStrea
   }
   if (e != cudaSuccess || one_cluster(a.T, a.K) || !(a.dw_post || a.dgate_col || a.dw_next)) return e;
   return launch_short(over, norm_join_reduce_kernel, dim3(static_cast<unsigned>(a.K / 8), 2), dim3(256), 0, stream,
-                    static_cast<const float*>(a.parts), sh.grid * sh.teams, static_cast<int>(a.K), a.beta, a.w_post,
+                    static_cast<const float*>(a.parts), sh.grid, static_cast<int>(a.K), a.beta, a.w_post,
                     a.gate_col, a.dw_post, a.dgate_col, a.dw_next);
 }
 
