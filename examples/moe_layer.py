@@ -1,4 +1,4 @@
-"""One whole MoE layer, trained: norm, router, sorted rows, gated experts, joined rows,
+"""One whole MoE layer, trained and then served in 4 bits: norm, router, sorted rows, gated experts, joined rows,
 and the norm, gate and residual stream around them, forward and backward, with the
 gradients clipped by their global norm.
 
@@ -70,6 +70,23 @@ class MoELayer:
         dx, _, _, _, grads["w_pre"] = gmm.norm_join_bwd(dx, dn_in.bfloat16(), x, w_next=p["w_pre"], eps=EPS)
         return dx, grads
 
+    def serve(self):
+        """The layer with MXFP4 experts, as a function of x bf16 [T, K] that returns (out, n)."""
+        p, ws = self.params, self.workspace
+        wq, wqs = gmm.mx4_quantize_rhs(p["w"].bfloat16())
+        w2q, w2qs = gmm.mx4_quantize_rhs(p["w2"].bfloat16())
+
+        def forward(x):
+            _, n = gmm.norm_join(x, w_next=p["w_pre"], eps=EPS)
+            ids, weights = gmm.route(n.float() @ p["w_router"].t(), self.k, bias=self.bias, score=self.score, renorm=True)
+            rows, sizes = gmm.sort_rows(ids, self.E)
+            xq, xs = gmm.gather_mx4_quantize(n, rows)
+            _, hq, hs = gmm.mx4_fwd_swiglu_quant(xq, xs, wq, wqs, sizes, with_h=False, workspace=ws)
+            y = gmm.mx4_fwd(hq, hs, w2q, w2qs, None, workspace=ws)
+            return gmm.norm_join(x, gmm.combine_rows(y, rows, weights), p["w_post"], p["gate"], p["w_next"], eps=EPS)
+
+        return forward
+
     def step(self, x, target, lr, max_norm=1.0):
         """One step on mean((n - target)^2) / 2; returns the loss and the gradients' norm before clipping."""
         _, n = self.forward(x)
@@ -101,6 +118,8 @@ def main(argv=None):
         loss, norm = layer.step(x, target, a.lr)
         losses.append(loss)
         print(f"step {i:3d}  loss {loss:.4f}  gradient norm {norm:.4f}")
+    exact, (served, _) = layer.forward(x)[0].float(), layer.serve()(x)
+    print(f"served in MXFP4: {((served.float() - exact).norm() / exact.norm()).item():.3f} off the bf16 layer")
     if layer.workspace.status() != 0:
         raise SystemExit("a kernel reported an error")
     return losses

@@ -19,9 +19,10 @@ from .binding import (EXPORTED, GmmError, LIB_PATH, STATUS_NAMES, Workspace, bf1
                       swiglu_fwd, swiglu_bwd, tgmm_ckpt, mx4_quantize_lhs,
                       mx4_quantize_rhs, mx4_fwd, mx4_fwd_swiglu_quant,
                       gmm_route, gmm_route_bwd, gmm_sort_rows, gmm_sort_rows_scratch_bytes, gmm_gather_rows,
-                      gmm_gather_quantize, gmm_combine_rows, gmm_combine_rows_bwd, gmm_norm_join, gmm_norm_join_bwd,
+                      gmm_gather_quantize, gmm_gather_mx4_quantize, gmm_combine_rows, gmm_combine_rows_bwd, gmm_norm_join, gmm_norm_join_bwd,
                       gmm_norm_join_bwd_scratch_bytes, gmm_clip_grads, gmm_clip_grads_scratch_bytes,
-                      route, route_bwd, sort_rows, gather_rows, gather_quantize, combine_rows, combine_rows_bwd,
+                      route, route_bwd, sort_rows, gather_rows, gather_quantize, gather_mx4_quantize,
+                      combine_rows, combine_rows_bwd,
                       norm_join, norm_join_bwd, clip_grads)
 
 __all__ = ["EXPORTED", "GmmError", "LIB_PATH", "STATUS_NAMES", "Workspace", "bf16_fwd", "dgrad", "fp8_fwd",
@@ -38,7 +39,8 @@ __all__ = ["EXPORTED", "GmmError", "LIB_PATH", "STATUS_NAMES", "Workspace", "bf1
            "swiglu_fwd", "swiglu_bwd", "tgmm_ckpt", "mx4_quantize_lhs",
            "mx4_quantize_rhs", "mx4_fwd", "mx4_fwd_swiglu_quant",
            "gmm_route", "gmm_route_bwd", "gmm_sort_rows", "gmm_sort_rows_scratch_bytes", "gmm_gather_rows",
-           "gmm_gather_quantize", "gmm_combine_rows", "gmm_combine_rows_bwd", "gmm_norm_join", "gmm_norm_join_bwd",
+           "gmm_gather_quantize", "gmm_gather_mx4_quantize", "gmm_combine_rows", "gmm_combine_rows_bwd", "gmm_norm_join", "gmm_norm_join_bwd",
            "gmm_norm_join_bwd_scratch_bytes", "gmm_clip_grads", "gmm_clip_grads_scratch_bytes",
-           "route", "route_bwd", "sort_rows", "gather_rows", "gather_quantize", "combine_rows", "combine_rows_bwd",
+           "route", "route_bwd", "sort_rows", "gather_rows", "gather_quantize", "gather_mx4_quantize",
+           "combine_rows", "combine_rows_bwd",
            "norm_join", "norm_join_bwd", "clip_grads"]

@@ -38,7 +38,7 @@ EXPORTED = ["gmm_status_string", "gmm_last_cuda_error", "gmm_workspace_bytes", "
             "gmm_fp8_w4_fwd_swiglu_quant", "tgmm_bf16_tiled", "gmm_bf16_swiglu_fwd", "gmm_bf16_swiglu_bwd",
             "tgmm_fp8_ckpt", "tgmm_fp8_ckpt_scratch_bytes", "gmm_mx4_quantize_lhs", "gmm_mx4_quantize_rhs", "gmm_mx4_fwd",
             "gmm_mx4_fwd_swiglu_quant", "gmm_route", "gmm_route_bwd", "gmm_sort_rows_scratch_bytes", "gmm_sort_rows",
-            "gmm_gather_rows", "gmm_gather_quantize", "gmm_combine_rows", "gmm_combine_rows_bwd", "gmm_norm_join",
+            "gmm_gather_rows", "gmm_gather_quantize", "gmm_gather_mx4_quantize", "gmm_combine_rows", "gmm_combine_rows_bwd", "gmm_norm_join",
             "gmm_norm_join_bwd_scratch_bytes", "gmm_norm_join_bwd", "gmm_clip_grads_scratch_bytes", "gmm_clip_grads"]
 
 
@@ -161,6 +161,8 @@ def load():
     lib.gmm_gather_rows.argtypes = [P, P, I64, I, I64, P, P]
     lib.gmm_gather_quantize.restype = I
     lib.gmm_gather_quantize.argtypes = [P, P, I64, I, I64, P, P, P]
+    lib.gmm_gather_mx4_quantize.restype = I
+    lib.gmm_gather_mx4_quantize.argtypes = [P, P, I64, I, I64, P, P, P]
     lib.gmm_combine_rows.restype = I
     lib.gmm_combine_rows.argtypes = [P, P, P, I64, I, I64, P, P]
     lib.gmm_combine_rows_bwd.restype = I
@@ -391,6 +393,10 @@ def gmm_gather_rows(x, rows, T, k, K, out, stream=None) -> int:
 
 def gmm_gather_quantize(x, rows, T, k, K, xq, xs, stream=None) -> int:
     return load().gmm_gather_quantize(_p(x), _p(rows), T, k, K, _p(xq), _p(xs), _s(stream))
+
+
+def gmm_gather_mx4_quantize(x, rows, T, k, K, xq, xs, stream=None) -> int:
+    return load().gmm_gather_mx4_quantize(_p(x), _p(rows), T, k, K, _p(xq), _p(xs), _s(stream))
 
 
 def gmm_combine_rows(y, rows, weights, T, k, K, out, stream=None) -> int:
@@ -1157,6 +1163,32 @@ def gather_quantize(x, rows, stream=None, out=None):
                                                   handle)
     if status:
         raise GmmError(status, "gmm_gather_quantize")
+    return xq, xs
+
+
+def gather_mx4_quantize(x, rows, stream=None, out=None):
+    """mx4_quantize_lhs(gather_rows(x, rows)) in one pass: (xq uint8 [T k, K/2] packed
+    E2M1 codes, xs uint8 [K/128, T k, 4] E8M0 scales).  out: an (xq, xs) pair to write into."""
+    if stream is not None and (other := _other(stream)):
+        with other:
+            return gather_mx4_quantize(x, rows, stream, out)
+    T, K = x.shape
+    k = rows.shape[-1]
+    on, M, KB = _first("x", x, _BF16), T * k, K // 128
+    _want("rows", rows, on, _I32, (T, k))
+    handle = _handle(on, stream)
+    if out is None:
+        device = x.device
+        xq = _empty((M, K // 2), (K // 2, 1), dtype=torch.uint8, device=device)
+        xs = _empty((KB, M, 4), (4 * M, 4, 1), dtype=torch.uint8, device=device)
+    else:
+        xq, xs = out
+        _want("out codes", xq, on, torch.uint8, (M, K // 2))
+        _want("out scales", xs, on, torch.uint8, (KB, M, 4))
+    status = (_lib or load()).gmm_gather_mx4_quantize(x.data_ptr(), rows.data_ptr(), T, k, K, xq.data_ptr(),
+                                                      xs.data_ptr(), handle)
+    if status:
+        raise GmmError(status, "gmm_gather_mx4_quantize")
     return xq, xs
 
 

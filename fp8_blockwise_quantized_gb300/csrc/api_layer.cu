@@ -172,6 +172,15 @@ gmm_status gmm_gather_quantize(const void* x, const int32_t* rows, int64_t T, in
                   "gather_quantize_kernel launch");
 }
 
+gmm_status gmm_gather_mx4_quantize(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, void* xs,
+                                   void* stream) {
+  int sms = 0;
+  const gmm_status st = check_rows(T, k, K, 128, x && rows && xq && xs, all_aligned(x, rows, xq, xs), &sms);
+  if (st != GMM_OK || T == 0) return st;
+  return launched(launch_gather_mx4(x, rows, T, k, K, xq, xs, static_cast<cudaStream_t>(stream)),
+                  "gather_mx4_kernel launch");
+}
+
 gmm_status gmm_combine_rows(const void* y, const int32_t* rows, const float* weights, int64_t T, int k, int64_t K,
                             void* out, void* stream) {
   int sms = 0;

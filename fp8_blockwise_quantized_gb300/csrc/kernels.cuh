@@ -218,6 +218,8 @@ cudaError_t launch_gather_rows(const void* x, const int32_t* rows, int64_t T, in
                                cudaStream_t stream);
 cudaError_t launch_gather_quantize(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, float* xs,
                                    cudaStream_t stream);
+cudaError_t launch_gather_mx4(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, void* xs,
+                              cudaStream_t stream);
 cudaError_t launch_combine_rows(const void* y, const int32_t* rows, const float* weights, int64_t T, int k, int64_t K,
                                 void* out, cudaStream_t stream);
 cudaError_t launch_combine_rows_bwd(const void* dout, const void* y, const int32_t* rows, const float* weights,

@@ -508,6 +508,14 @@ gmm_status gmm_gather_quantize(const void* x, const int32_t* rows, int64_t T, in
                                void* stream);
 
 /*
+ * gmm_mx4_quantize_lhs of gmm_gather_rows' result, bit for bit, each token quantised
+ * once: the operands of gmm_mx4_fwd and gmm_mx4_fwd_swiglu_quant.
+ *   xq  codes [T k, K/2] bytes;  xs  scale bytes [K/128, T k, 4];  K a multiple of 128
+ */
+gmm_status gmm_gather_mx4_quantize(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, void* xs,
+                                   void* stream);
+
+/*
  * The sorted rows joined by token:
  *   out[t] = bf16( sum_j weights[t,j] * y[rows[t,j]] ),  fp32, j rising;
  * weights NULL: 1 each (the gradient of gmm_gather_rows).  A choice of no group adds

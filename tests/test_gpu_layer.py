@@ -74,6 +74,26 @@ def test_layer_forward_and_gradients(E, k, T, score):
         assert _off(g, w_grads[name]) < BACKWARD, name
 
 
+@pytest.mark.parametrize("E,k,T", [(8, 2, 300), (16, 4, 1), (5, 1, 257)])
+def test_layer_served_in_4_bits(E, k, T):
+    """Bit for bit the layer that gathers in bf16 and quantises the sorted rows."""
+    from examples.moe_layer import EPS, MoELayer
+    K, N = 384, 256
+    layer = MoELayer(E, K, N, k, T, seed=E)
+    p, ws = layer.params, layer.workspace
+    x = torch.randn((T, K), generator=torch.Generator(device="cuda").manual_seed(T), device="cuda").to(BF)
+    got = layer.serve()(x)
+    _, n = gmm.norm_join(x, w_next=p["w_pre"], eps=EPS)
+    ids, weights = gmm.route(n.float() @ p["w_router"].t(), k, bias=layer.bias, score=layer.score, renorm=True)
+    rows, sizes = gmm.sort_rows(ids, E)
+    xq, xs = gmm.mx4_quantize_lhs(gmm.gather_rows(n, rows))
+    _, hq, hs = gmm.mx4_fwd_swiglu_quant(xq, xs, *gmm.mx4_quantize_rhs(p["w"].to(BF)), sizes, workspace=ws)
+    y = gmm.mx4_fwd(hq, hs, *gmm.mx4_quantize_rhs(p["w2"].to(BF)), sizes, workspace=ws)
+    want = gmm.norm_join(x, gmm.combine_rows(y, rows, weights), p["w_post"], p["gate"], p["w_next"], eps=EPS)
+    assert ws.status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_example_runs():
     from examples.moe_layer import main
     losses = main(["--steps", "3", "--tokens", "200"])
@@ -109,6 +129,7 @@ CALLS = {
     "sort_rows long": lambda d, **k: gmm.sort_rows(d["long_ids"], d["E"], **k),
     "gather_rows": lambda d, **k: gmm.gather_rows(d["x"], d["rows"], **k),
     "gather_quantize": lambda d, **k: gmm.gather_quantize(d["x"], d["rows"], **k),
+    "gather_mx4_quantize": lambda d, **k: gmm.gather_mx4_quantize(d["x"], d["rows"], **k),
     "combine_rows": lambda d, **k: gmm.combine_rows(d["y"], d["rows"], d["weights"], **k),
     "combine_rows_bwd": lambda d, **k: gmm.combine_rows_bwd(d["x"], d["y"], d["rows"], d["weights"], **k),
     "norm_join": lambda d, **k: gmm.norm_join(d["xf"], d["b"], d["col"], d["col"], d["col"], **k),

@@ -52,6 +52,10 @@ def test_gather_quantize_with_64_bit_thread_indices():
     wq, ws = gmm.quantize_lhs(x[at])
     p = rows[at, 0].long()
     assert torch.equal(xq[p], wq) and torch.equal(xs[:, p], ws)
+    del xq, xs
+    xq, xs = gmm.gather_mx4_quantize(x, rows)
+    wq, ws = gmm.mx4_quantize_lhs(x[at])
+    assert torch.equal(xq[p], wq) and torch.equal(xs[:, p], ws)
 
 
 def test_combine_gradient_past_32_bits():

@@ -121,6 +121,22 @@ def test_gather_quantize_is_the_quantisation_of_the_gathered_rows(T, k, E, K, ki
 
 
 @pytest.mark.parametrize("T,k,E,K,kind", MOVES)
+def test_gather_mx4_quantize_is_the_quantisation_of_the_gathered_rows(T, k, E, K, kind):
+    rows, S, x, _, _ = _case(T, k, E, K, kind)
+    x[T - 1] = 0
+    x[0, :32] *= 1e-30
+    x[0, 40], x[0, 80] = float("inf"), -0.0
+    xq, xs = Guarded((T * k, K // 2), torch.uint8), Guarded((K // 128, T * k, 4), torch.uint8)
+    gmm.gather_mx4_quantize(x, rows, out=(xq.t, xs.t))
+    xq.check("codes")
+    xs.check("scales")
+    wq, ws = gmm.mx4_quantize_lhs(_moved(x, rows))
+    assert torch.equal(xq.t, wq) and torch.equal(xs.t, ws)
+    got = gmm.gather_mx4_quantize(x, rows)
+    assert torch.equal(got[0], wq) and torch.equal(got[1], ws)
+
+
+@pytest.mark.parametrize("T,k,E,K,kind", MOVES)
 @pytest.mark.parametrize("weighted", [False, True])
 def test_combine_rows(T, k, E, K, kind, weighted):
     rows, S, _, y, w = _case(T, k, E, K, kind)
@@ -187,6 +203,7 @@ def test_no_tokens():
     x, w = torch.empty((0, 256), dtype=BF, device="cuda"), torch.empty((0, 8), device="cuda")
     assert gmm.gather_rows(x, rows).shape == (0, 256)
     assert gmm.gather_quantize(x, rows)[0].shape == (0, 256)
+    assert gmm.gather_mx4_quantize(x, rows)[1].shape == (2, 0, 4)
     assert gmm.combine_rows(x, rows, w).shape == (0, 256)
     assert gmm.combine_rows_bwd(x, x, rows, w)[1].shape == (0, 8)
 

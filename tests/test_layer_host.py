@@ -74,6 +74,7 @@ def test_sort_scratch(lib):
 ROWS = {
     "gmm_gather_rows": ("x rows | out", 8),
     "gmm_gather_quantize": ("x rows | xq xs", 128),
+    "gmm_gather_mx4_quantize": ("x rows | xq xs", 128),
     "gmm_combine_rows": ("y rows weights | out", 8),
     "gmm_combine_rows_bwd": ("dout y rows weights | dy dweights", 8),
 }
@@ -155,6 +156,7 @@ def test_python_entry_points_refuse_what_kernels_cannot_take(lib):
     rows, w = z(4, 2, dt=I32), z(4, 2, dt=F32)
     for call in (lambda: g.route(z(4, 8), 2), lambda: g.route_bwd(w, z(4, 8), rows), lambda: g.sort_rows(rows, 8),
                  lambda: g.gather_rows(z(4, 128), rows), lambda: g.gather_quantize(z(4, 128), rows),
+                 lambda: g.gather_mx4_quantize(z(4, 128), rows),
                  lambda: g.combine_rows(z(8, 128), rows, w), lambda: g.combine_rows_bwd(z(4, 128), z(8, 128), rows, w),
                  lambda: g.norm_join(z(4, 128), w_next=z(128, dt=F32)),
                  lambda: g.norm_join_bwd(z(4, 128), None, z(4, 128)), lambda: g.clip_grads([z(4)], 1.0)):

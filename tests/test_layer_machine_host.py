@@ -61,6 +61,8 @@ CASES = {
     "sort_rows": lambda: ([ids(), E], {}, ("out", (ids(), Tensor(I32, E)))),
     "gather_rows": lambda: ([x(), ids()], {}, ("out", Tensor(BF, T * k, K))),
     "gather_quantize": lambda: ([x(), ids()], {}, ("out", (Tensor(U8, T * k, K), Tensor(F32, K // 128, T * k)))),
+    "gather_mx4_quantize": lambda: ([x(), ids()], {},
+                                    ("out", (Tensor(U8, T * k, K // 2), Tensor(U8, K // 128, T * k, 4)))),
     "combine_rows": lambda: ([Tensor(BF, T * k, K), ids(), w()], {}, ("out", x())),
     "combine_rows_bwd": lambda: ([x(), Tensor(BF, T * k, K), ids(), w()], {}, ("out", (Tensor(BF, T * k, K), w()))),
     "norm_join": lambda: ([x(F32), x(), col(), col(), col()], {}, ("out", (x(F32), x()))),
