@@ -256,11 +256,6 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_kernel(NormJoinArgs a)
   }
 }
 
-// A row of an input on its way to the L2, asked for by one thread.
-__device__ __forceinline__ void row_to_l2(const void* p, int bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 constexpr int kOneCtas = 8;
 
 // The parameters' gradients of column c from its two sums.
@@ -277,14 +272,20 @@ __device__ __forceinline__ void put_columns(const NormJoinBwdArgs& a, int c, flo
 // one sum for both, a part of it a CTA (and of dw_next's), joined by
 // norm_join_reduce_kernel.
 //
-// V = 2 (over 4096 columns): the registers hold the sums, but neither the factors,
-// which come from the cache for each row, nor the row ahead.
+// V = 2 (over 4096 columns): the registers hold the sums and the factors, but not the
+// row ahead, which goes through shared memory, and its values are read there again when
+// they are needed again.  2048 x 8192: 41.8 us with a bf16 stream (floor 30.2), 55.9
+// with fp32 (45.2); with the row read when its turn came, asked for in the L2 before,
+// and factors from the cache, 55.0 and 79.4.  What is left is a row's two sums, one after
+// the other, with no other row in the SM.
 // ONE: few rows are one cluster's, whose CTAs add up each other's sums; no parts and no
 // second kernel.
 template <typename S, int V, int NT, bool FULL, bool ONE>
 __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwdArgs a) {
   static_assert(V == 1 || !ONE, "a thread's columns are 8 words of shared memory a sum");
   constexpr bool kHeld = V == 1;
+  constexpr int kS = sizeof(S) / 2, kChunks = V * (2 * kS + 2 + FULL);  // 16 bytes of a row
+  extern __shared__ uint4 ahead[];                                      // [2][kChunks][NT] where V = 2
   __shared__ SumBuffer red;
   griddep_launch_dependents();
   clear(red);
@@ -294,20 +295,16 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
   const float inv_k = 1.0f / static_cast<float>(a.K);
   bool on[V];
   int col[V];
-  Cols held_p, held_n, sb[V], sn[V];
+  Cols post[V], next[V], sb[V], sn[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     col[v] = me.col + 8 * a.row_threads * v;
     on[v] = me.team < me.rows && col[v] < a.K;
     if (!on[v]) col[v] = 0;
     sb[v] = sn[v] = Cols::of(0.0f);
+    post[v] = factors8(a.w_post, a.gate_col, a.beta, col[v]);
+    next[v] = factors8(a.w_next, nullptr, 1.0f, col[v]);
   }
-  if constexpr (kHeld) {
-    held_p = factors8(a.w_post, a.gate_col, a.beta, col[0]);
-    held_n = factors8(a.w_next, nullptr, 1.0f, col[0]);
-  }
-  auto post = [&](int v) { return kHeld ? held_p : factors8(a.w_post, a.gate_col, a.beta, col[v]); };
-  auto next = [&](int v) { return kHeld ? held_n : factors8(a.w_next, nullptr, 1.0f, col[v]); };
   Raw<S> rd[V], ro[V];
   Raw<uint16_t> rn[V], rb[V], rg[V];
   auto fetch = [&](long long t) {
@@ -324,26 +321,67 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
       if (FULL) rg[v].load(a.gate_full + at);
     }
   };
+  // Through shared memory each warp copies its own columns as they lie in memory: of
+  // fp32 a lane takes every 32nd 16 bytes and reads two neighbours (with its own 32 bytes
+  // in two copies every sector was read twice: 75.2 us).
+  const int lane = threadIdx.x & 31;
+  int turn = 0;
+  auto stage = [&](long long t) {
+    if (t < a.T) {
+      const long long row = t * a.K;
+      uint4* to = ahead + turn * kChunks * NT + threadIdx.x;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (kS == 2) {
+          const int first = me.col + 8 * (a.row_threads * v - lane) + 4 * lane;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int at = first + 128 * i;
+            uint4* here = to + 2 * v * NT + (threadIdx.x - lane) + 32 * i;
+            if (me.team >= me.rows || at >= a.K) continue;
+            if (a.dout) cp_async_16(here, static_cast<const S*>(a.dout) + row + at);
+            if (a.dn) cp_async_16(here + 2 * V * NT, static_cast<const S*>(a.out) + row + at);
+          }
+        }
+        if (!on[v]) continue;
+        if constexpr (kS == 1) {
+          if (a.dout) cp_async_16(to + v * NT, static_cast<const S*>(a.dout) + row + col[v]);
+          if (a.dn) cp_async_16(to + (V + v) * NT, static_cast<const S*>(a.out) + row + col[v]);
+        }
+        if (a.dn) cp_async_16(to + (2 * kS * V + v) * NT, a.dn + row + col[v]);
+        if (a.b) cp_async_16(to + (2 * kS * V + V + v) * NT, a.b + row + col[v]);
+        if (FULL) cp_async_16(to + (2 * kS * V + 2 * V + v) * NT, a.gate_full + row + col[v]);
+      }
+    }
+    cp_async_commit();
+    turn ^= 1;
+  };
+  const uint4* at_hand = nullptr;
+  auto wide = [&](int i) {
+    if constexpr (kS == 1) return cols_of(at_hand[i * NT]);
+    // lanes 4 to 7 of 8 read their second 16 bytes first: no two in one bank
+    const bool swap = lane & 4;
+    const float4* q = reinterpret_cast<const float4*>(at_hand + 2 * i * NT + threadIdx.x);
+    const float4 x = q[swap], y = q[!swap];
+    return cols_of(swap ? y : x, swap ? x : y);
+  };
+  auto half = [&](int i) { return cols_of(at_hand[(2 * kS * V + i) * NT]); };
 #pragma unroll
   for (int v = 0; v < V; ++v) rd[v].zero();
   long long t = static_cast<long long>(blockIdx.x) * me.rows + me.team;
-  if (kHeld) fetch(t);
+  if (kHeld)
+    fetch(t);
+  else
+    stage(t);
   Sums<2> sums{red};
   for (long long t0 = t - me.team; t0 < a.T; t0 += step, t += step) {
     const long long row = t * a.K;
-    if (!kHeld) {
-      fetch(t);
-      if (threadIdx.x == 0 && t + step < a.T) {
-        const long long at = row + step * a.K;
-        const int wide = a.K * static_cast<int>(sizeof(S)), narrow = 2 * a.K;
-        if (a.dout) row_to_l2(static_cast<const S*>(a.dout) + at, wide);
-        if (a.dn) {
-          row_to_l2(a.dn + at, narrow);
-          row_to_l2(static_cast<const S*>(a.out) + at, wide);
-        }
-        if (a.b) row_to_l2(a.b + at, narrow);
-        if (FULL) row_to_l2(a.gate_full + at, narrow);
-      }
+    if constexpr (!kHeld) {
+      __syncthreads();  // the row that the next one replaces has been read
+      at_hand = ahead + (turn ^ 1) * kChunks * NT + threadIdx.x;
+      stage(t + step);
+      cp_async_wait_but_one();
+      __syncwarp();
     }
     Cols c_[V], o_[V], f_[V], d[V], g_[V];
     if (kHeld) {
@@ -354,10 +392,11 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
       }
       fetch(t + step);
     }
-    auto c = [&](int v) { return kHeld ? c_[v] : rn[v].get(); };
-    auto o = [&](int v) { return kHeld ? o_[v] : ro[v].get(); };
-    auto f = [&](int v) { return kHeld ? f_[v] : rb[v].get(); };
-    auto g = [&](int v) { return kHeld ? g_[v] : rg[v].get(); };
+    auto c = [&](int v) { return kHeld ? c_[v] : half(v); };
+    auto o = [&](int v) { return kHeld ? o_[v] : wide(V + v); };
+    auto f = [&](int v) { return kHeld ? f_[v] : half(V + v); };
+    auto g = [&](int v) { return kHeld ? g_[v] : half(2 * V + v); };
+    auto d0 = [&](int v) { return kHeld ? d[v] : a.dout ? wide(v) : Cols::of(0.0f); };
     float s[2];
     if (a.dn) {
       s[0] = s[1] = 0.0f;
@@ -365,18 +404,18 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
       for (int v = 0; v < V; ++v)
         if (on[v]) {
           s[0] += dot8(o(v), o(v));
-          s[1] += dot8(next(v), c(v) * o(v));
+          s[1] += dot8(next[v], c(v) * o(v));
         }
       sums(s, me);
       const float r = inv_rms(s[0], inv_k, a.eps), q = s[1] * r * r * r * inv_k;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (on[v] && t < a.T) sn[v] = fma8(c(v) * o(v), r, sn[v]);
-        d[v] = fma8(c(v) * next(v), r, fma8(o(v), -q, kHeld ? d[v] : rd[v].get()));
+        d[v] = fma8(c(v) * next[v], r, fma8(o(v), -q, d0(v)));
       }
     } else if (!kHeld) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) d[v] = rd[v].get();
+      for (int v = 0; v < V; ++v) d[v] = d0(v);
     }
     if (a.dx) {
 #pragma unroll
@@ -391,7 +430,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
         for (int v = 0; v < V; ++v)
           if (on[v]) {
             s[0] += dot8(f(v), f(v));
-            s[1] += dot8(FULL ? post(v) * g(v) : post(v), d[v] * f(v));
+            s[1] += dot8(FULL ? post[v] * g(v) : post[v], d[v] * f(v));
           }
         sums(s, me);
         r = inv_rms(s[0], inv_k, a.eps);
@@ -400,9 +439,9 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (!on[v] || t >= a.T) continue;
-        Cols e = d[v] * post(v), df = d[v] * f(v);
+        Cols e = d[v] * post[v], df = d[v] * f(v);
         if (FULL) {
-          put8(a.dgate_full + row + col[v], df * r * post(v));
+          put8(a.dgate_full + row + col[v], df * r * post[v]);
           df = df * g(v);
           e = e * g(v);
         }
@@ -545,8 +584,14 @@ cudaError_t backward(const NormJoinBwdArgs& a, const Shape& sh, bool over, cudaS
     return sh.threads == 256 ? cudaLaunchKernelEx(&cfg, norm_join_bwd_kernel<S, 1, 256, FULL, true>, a)
                              : cudaLaunchKernelEx(&cfg, norm_join_bwd_kernel<S, 1, 512, FULL, true>, a);
   }
-  if (backward_vectors(a.K) == 2)
-    return launch_short(over, norm_join_bwd_kernel<S, 2, 512, FULL, false>, dim3(sh.grid), dim3(512), 0, stream, a);
+  if (backward_vectors(a.K) == 2) {
+    constexpr int kSmem = 2 * 2 * static_cast<int>(sizeof(S) + 2 + FULL) * 16 * 512;  // two rows
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = norm_join_bwd_kernel<S, 2, 512, FULL, false>;
+    const cudaError_t e = allow_smem(kernel, kSmem, done);
+    if (e != cudaSuccess) return e;
+    return launch_short(over, kernel, dim3(sh.grid), dim3(512), kSmem, stream, a);
+  }
   return sh.threads == 256
              ? launch_short(over, norm_join_bwd_kernel<S, 1, 256, FULL, false>, dim3(sh.grid), dim3(256), 0, stream, a)
              : launch_short(over, norm_join_bwd_kernel<S, 1, 512, FULL, false>, dim3(sh.grid), dim3(512), 0, stream, a);

@@ -120,6 +120,29 @@ def test_without_a_next_norm():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,K", [(460, 4104), (310, 8184), (155, 8192)])
+@pytest.mark.parametrize("stream", [BF, F32])
+@pytest.mark.parametrize("gate", [None, "column", "full"])
+def test_backward_of_wide_rows_a_cta_has_several_of(T, K, stream, gate):
+    c, dout, dn = _case(T, K, stream, True, gate, 3)
+    rest = {k: c[k] for k in ("b", "w_post", "gate", "w_next")}
+    out, _ = gmm.norm_join(**c, eps=EPS)
+    for d, e in ((dout, dn), (None, dn), (dout, None)):
+        got = gmm.norm_join_bwd(d, e, out, **rest, eps=EPS)
+        ref, mag = R.norm_join_bwd(None if d is None else d.double(), (torch.zeros_like(dn) if e is None else e).double(),
+                                   out.double(), *_ref(c, "b", "w_post", "gate", "w_next"), 1.0, 1.0, EPS)
+        for i, name in enumerate(("dx", "db", "dw_post", "dgate", "dw_next")):
+            if ref[i] is None:
+                continue
+            half = R.BF16 if got[i].dtype == BF else 0.0
+            off = (2 * R.F32 + (T * R.U if ref[i].dim() == 1 else 0.0)) * mag[i]
+            R.assert_within(got[i], ref[i], half * ref[i].abs() + off, name)
+    d, b = dout.clone(), c["b"].clone()  # in place
+    want = gmm.norm_join_bwd(dout, dn, out, **rest, eps=EPS)
+    for u, v in zip(gmm.norm_join_bwd(d, dn, out, b, c["w_post"], c["gate"], c["w_next"], eps=EPS, into=(d, b)), want):
+        assert (u is None and v is None) or torch.equal(u, v)
+
+
 @pytest.mark.parametrize("stream", [BF, F32])
 def test_in_place(stream):
     c, dout, dn = _case(700, 1024, stream, True, "column", 2)
