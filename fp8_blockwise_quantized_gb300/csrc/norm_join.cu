@@ -446,7 +446,8 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
           e = e * g(v);
         }
         sb[v] = fma8(df, r, sb[v]);
-        put8(a.db + row + col[v], fma8(e, r, f(v) * -q));
+        // (without its norm b is no part of its gradient, and 0 times an infinity would be)
+        put8(a.db + row + col[v], a.w_post ? fma8(e, r, f(v) * -q) : e);
       }
     }
   }
