@@ -265,9 +265,10 @@ __device__ __forceinline__ void put_columns(const NormJoinBwdArgs& a, int c, flo
   if (a.dw_next) a.dw_next[c] = next;
 }
 
-// With c = dn * w_next, D = dout + ro c - out ro^3 / K sum(c out); dx = alpha D.
+// With c = dn * w_next, D = dout + ro (c - out ro^2 / K sum(c out)); dx = alpha D.
 // With p = beta * w_post * gate, b's gradient is that of its norm from t = D p:
-// db = rb t - b rb^3 / K sum(t b).  With s = sum over the rows of D b rb (times a
+// db = rb (t - b rb^2 / K sum(t b)).  (A cube of ro or rb leaves fp32's range where the
+// gradient does not: rows below 1e-13 with eps = 0.)  With s = sum over the rows of D b rb (times a
 // gate per element), dw_post = beta gate s and a column gate's gradient beta w_post s:
 // one sum for both, a part of it a CTA (and of dw_next's), joined by
 // norm_join_reduce_kernel.
@@ -407,11 +408,11 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
           s[1] += dot8(next[v], c(v) * o(v));
         }
       sums(s, me);
-      const float r = inv_rms(s[0], inv_k, a.eps), q = s[1] * r * r * r * inv_k;
+      const float r = inv_rms(s[0], inv_k, a.eps), q = s[1] * r * inv_k * r;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (on[v] && t < a.T) sn[v] = fma8(c(v) * o(v), r, sn[v]);
-        d[v] = fma8(c(v) * next[v], r, fma8(o(v), -q, d0(v)));
+        d[v] = fma8(fma8(o(v), -q, c(v) * next[v]), r, d0(v));
       }
     } else if (!kHeld) {
 #pragma unroll
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
           }
         sums(s, me);
         r = inv_rms(s[0], inv_k, a.eps);
-        q = s[1] * r * r * r * inv_k;
+        q = s[1] * r * inv_k * r;
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
         }
         sb[v] = fma8(df, r, sb[v]);
         // (without its norm b is no part of its gradient, and 0 times an infinity would be)
-        put8(a.db + row + col[v], a.w_post ? fma8(e, r, f(v) * -q) : e);
+        put8(a.db + row + col[v], a.w_post ? fma8(f(v), -q, e) * r : e);
       }
     }
   }

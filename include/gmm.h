@@ -545,7 +545,8 @@ gmm_status gmm_combine_rows_bwd(const void* dout, const void* y, const int32_t* 
  *   w_post, w_next  fp32 [K]
  *   gate    gate_rows = 0: fp32 [K], one value per column; gate_rows = 1: bf16 [T, K]
  * out may be x; n may be b.  eps >= 0.  The squares are summed in fp32: a row's sum has
- * to stay below 3.4e38, and with eps = 0 a row of zeros gives NaN.
+ * to stay below 3.4e38, and its mean plus eps above 1.2e-38 (with eps = 0 a row of zeros
+ * gives NaN).
  */
 gmm_status gmm_norm_join(const void* x, gmm_type stream_type, const void* b, const float* w_post, const void* gate,
                          int gate_rows, const float* w_next, int64_t T, int64_t K, float residual_scale,
