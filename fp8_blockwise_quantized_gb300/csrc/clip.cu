@@ -10,7 +10,8 @@
 // Sums are fp32, compensated from chunk to chunk, while every square keeps its bits
 // there; a CTA that meets a sum outside that range adds its values up in double, of
 // which this GPU does two a cycle and SM (sums in double throughout: 19.7 us for 60
-// tensors of 3 M values, for 8.6).
+// tensors of 3 M values, for 8.6).  So are the products where the factor, max_norm / norm,
+// is not a normal number.
 //
 // A few values are one launch's: a cluster's CTAs, which read each other's sums and
 // keep their chunks' values in the caches.  It saves the host a launch and the caller
@@ -235,19 +236,38 @@ __device__ void scale_piece(const T* src, T* dst, int n, float by, int tid) {
   for (int i = nv * W + tid; i < n; i += kThreads) if (copy) dst[i] = src[i]; else put(dst, i, value_of(src, i) * by);
 }
 
-// The factor; a norm that is not finite scales nothing.
-__device__ __forceinline__ float factor_of(float norm, float max_norm) {
-  return norm > max_norm && norm <= 3.402823466e38f ? max_norm / norm : 1.0f;
+// The same where the factor is below fp32's normal numbers: it loses bits there, or all
+// of them, which the products need not.
+template <typename T>
+__device__ void scale_piece_in_double(const T* src, T* dst, int n, double by, int tid) {
+  for (int i = tid; i < n; i += kThreads) put(dst, i, static_cast<float>(value_of(src, i) * by));
 }
 
+// The factor; a norm that is not finite scales nothing.
+struct Factor {
+  float by;
+  double exact;  // where by is not normal (else 0)
+  __device__ __forceinline__ Factor(float norm, float max_norm) : by(1.0f), exact(0.0) {
+    if (!(norm > max_norm && norm <= 3.402823466e38f)) return;
+    by = max_norm / norm;
+    if (by < 1.175494351e-38f) exact = static_cast<double>(max_norm) / norm;
+  }
+};
+
 template <int N>
-__device__ __forceinline__ void scale_chunk(const ClipTable<N>& tab, int c, float by) {
+__device__ __forceinline__ void scale_chunk(const ClipTable<N>& tab, int c, const Factor& f) {
   const Piece p = piece_of(tab, c);
   const int tid = threadIdx.x & (kThreads - 1);
+  auto scale = [&](auto src, auto dst) {
+    if (f.exact > 0.0)
+      scale_piece_in_double(src + p.at, dst + p.at, p.n, f.exact, tid);
+    else
+      scale_piece(src + p.at, dst + p.at, p.n, f.by, tid);
+  };
   if (p.f32)
-    scale_piece(static_cast<const float*>(p.src) + p.at, static_cast<float*>(p.dst) + p.at, p.n, by, tid);
+    scale(static_cast<const float*>(p.src), static_cast<float*>(p.dst));
   else
-    scale_piece(static_cast<const uint16_t*>(p.src) + p.at, static_cast<uint16_t*>(p.dst) + p.at, p.n, by, tid);
+    scale(static_cast<const uint16_t*>(p.src), static_cast<uint16_t*>(p.dst));
 }
 
 template <int N>
@@ -274,9 +294,9 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
     whole = static_cast<float>(sqrt(block_sum(d, red_exact)));
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
-  const float by = factor_of(whole, max_norm);
-  if (in_place && by == 1.0f) return;
-  for (int c = tab.first[tab.n] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) scale_chunk(tab, c, by);
+  const Factor factor(whole, max_norm);
+  if (in_place && factor.by == 1.0f) return;
+  for (int c = tab.first[tab.n] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) scale_chunk(tab, c, factor);
 }
 
 template <int N>
@@ -316,9 +336,9 @@ __global__ void __launch_bounds__(kOneThreads) clip_one_kernel(const __grid_cons
   cluster_sync_all();  // the other CTAs' sums have been read: none of them leaves before
   const float whole = odd ? static_cast<float>(sqrt(d)) : sqrtf(s);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
-  const float by = factor_of(whole, max_norm);
-  if (in_place && by == 1.0f) return;
-  for (int c = first; c < tab.first[tab.n]; c += kStep) scale_chunk(tab, c, by);
+  const Factor factor(whole, max_norm);
+  if (in_place && factor.by == 1.0f) return;
+  for (int c = first; c < tab.first[tab.n]; c += kStep) scale_chunk(tab, c, factor);
 }
 
 constexpr int kSmallTable = 64, kLargeTable = 1000;  // 1.9 and 28.2 KB of parameters
