@@ -1296,7 +1296,9 @@ def norm_join(x, b=None, w_post=None, gate=None, w_next=None, residual_scale=1.0
             o = x
         else:
             _want("out", o, on, dtype, (T, K))
-        if w_next is not None:
+        if w_next is None:
+            n = None  # nothing is written to it
+        else:
             _want("out n", n, on, _BF16, (T, K))
     status = (_lib or load()).gmm_norm_join(x.data_ptr(), kind, _at(b), _at(w_post), _at(gate), full, _at(w_next), T, K,
                                             residual_scale, block_scale, eps, None if b is None else o.data_ptr(),
