@@ -7,11 +7,13 @@
 // chunks backwards, from those that may still be in the L2 (60 M values 83.7 us, forwards
 // 85.6; no difference at 805 M, 725 us, where two reads and a write take 724).
 //
-// Sums are fp32, compensated from chunk to chunk, while every square keeps its bits
-// there; a CTA that meets a sum outside that range adds its values up in double, of
-// which this GPU does two a cycle and SM (sums in double throughout: 19.7 us for 60
-// tensors of 3 M values, for 8.6).  So are the products where the factor, max_norm / norm,
-// is not a normal number.
+// Sums are pairs of fp32 values, a sum and what its roundings left (a thread's share of
+// one chunk, up to 128 squares, is one value), and the norm and the factor come from both,
+// so that each is rounded once.  That holds while every square keeps its bits in fp32; a
+// CTA that meets a sum outside that range adds its values up in double, of which this GPU
+// does two a cycle and SM (sums in double throughout: 19.7 us for 60 tensors of 3 M values,
+// for 8.5).  So are the products where the factor, max_norm / norm, is not a normal number
+// (60 M values: 383 us for 57).
 //
 // A few values are one launch's: a cluster's CTAs, which read each other's sums and
 // keep their chunks' values in the caches.  It saves the host a launch and the caller
@@ -131,34 +133,50 @@ __device__ double squares_in_double(const T* __restrict__ p, int n, int tid) {
   return d;
 }
 
-// Sum over the CTA, in its order; red: a value a warp.
-template <typename T>
+// hi + lo, lo being what the roundings of hi left: the next sum waits for hi alone.
+struct alignas(8) Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Pair exchanged(const Pair& v, int d) {
+  return {__shfl_xor_sync(0xffffffffu, v.hi, d), __shfl_xor_sync(0xffffffffu, v.lo, d)};
+}
+__device__ __forceinline__ double exchanged(double v, int d) { return __shfl_xor_sync(0xffffffffu, v, d); }
+
+// Sum over a CTA of NT threads, in its order; red: a value a warp.
+template <int NT, typename T>
 __device__ __forceinline__ T block_sum(T v, T* red) {
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  for (int d = 16; d >= 1; d >>= 1) v = v + exchanged(v, d);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  T s = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += red[w];
-  return s;
+  v = red[threadIdx.x & (NT / 32 - 1)];
+#pragma unroll
+  for (int d = NT / 64; d >= 1; d >>= 1) v = v + exchanged(v, d);
+  return v;
 }
 
-// The CTAs' sums: fp32, and double (read where the fp32 one is out of range).
+// The CTAs' sums: pairs, and double (where the pair is out of range).
 struct Parts {
   double* exact;
-  float* sum;
+  Pair* sum;
 };
+__device__ __forceinline__ bool is_odd(const Pair& sum) { return sum.hi != 0.0f && !in_range(sum.hi); }
 
 // Sum over the CTA of the squares of every `step`th chunk from `first` on (which may
-// differ between its 256s of threads): fp32, or NaN where it is out of range; and double.
+// differ between its 256s of threads): a pair, or NaN where it is out of range, and then
+// double.
 struct Sum {
-  float sum;
+  Pair sum;
   double exact;
 };
-template <int N>
+template <int NT, int N>
 __device__ __forceinline__ Sum sum_chunks(const ClipTable<N>& tab, int first, int step) {
-  __shared__ float red[32];
-  __shared__ double red_exact[32];
+  __shared__ Pair red[NT / 32];
+  __shared__ double red_exact[NT / 32];
   const int tid = threadIdx.x & (kThreads - 1);
   float s = 0.0f, lost = 0.0f;  // compensated
   bool any = false;
@@ -172,25 +190,25 @@ __device__ __forceinline__ Sum sum_chunks(const ClipTable<N>& tab, int first, in
     lost = (t - s) - y;
     s = t;
   }
-  s = block_sum(s, red);
-  if (!__syncthreads_or(any) || in_range(s)) return {s, s};
+  const Pair sum = block_sum<NT>(Pair{s, -lost}, red);
+  if (!__syncthreads_or(any) || in_range(sum.hi)) return {sum, 0.0};
   double d = 0.0;
   for (int c = first; c < tab.first[tab.n]; c += step) {
     const Piece p = piece_of(tab, c);
     d += p.f32 ? squares_in_double(static_cast<const float*>(p.src) + p.at, p.n, tid)
                : squares_in_double(static_cast<const uint16_t*>(p.src) + p.at, p.n, tid);
   }
-  return {__int_as_float(0x7fc00000), block_sum(d, red_exact)};
+  return {{__int_as_float(0x7fc00000), 0.0f}, block_sum<NT>(d, red_exact)};
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_constant__ ClipTable<N> tab, Parts parts) {
   griddep_launch_dependents();
   griddep_wait();
-  const Sum s = sum_chunks(tab, blockIdx.x, gridDim.x);
+  const Sum s = sum_chunks<kThreads>(tab, blockIdx.x, gridDim.x);
   if (threadIdx.x == 0) {
     parts.sum[blockIdx.x] = s.sum;
-    parts.exact[blockIdx.x] = s.exact;
+    if (is_odd(s.sum)) parts.exact[blockIdx.x] = s.exact;
   }
 }
 
@@ -243,14 +261,37 @@ __device__ void scale_piece_in_double(const T* src, T* dst, int n, double by, in
   for (int i = tid; i < n; i += kThreads) put(dst, i, static_cast<float>(value_of(src, i) * by));
 }
 
-// The factor; a norm that is not finite scales nothing.
+// The norm and the factor; a norm that is not finite scales nothing.
 struct Factor {
-  float by;
-  double exact;  // where by is not normal (else 0)
-  __device__ __forceinline__ Factor(float norm, float max_norm) : by(1.0f), exact(0.0) {
-    if (!(norm > max_norm && norm <= 3.402823466e38f)) return;
-    by = max_norm / norm;
-    if (by < 1.175494351e-38f) exact = static_cast<double>(max_norm) / norm;
+  float norm, by = 1.0f;
+  bool far = false;    // by is not normal:
+  double exact = 0.0;  // the factor then
+
+  // Of a sum of squares that is in range, or 0.  By Newton's step for the root from what
+  // its square leaves of the sum, and for the quotient from what the product leaves.
+  __device__ __forceinline__ Factor(const Pair& sum, float max_norm) {
+    const float r = sqrtf(sum.hi), inv = 1.0f / r;
+    const float rest = r > 0.0f ? (fmaf(-r, r, sum.hi) + sum.lo) * (0.5f * inv) : 0.0f;
+    norm = r + rest;
+    if (!(norm > max_norm)) return;
+    by = max_norm * inv;
+    if (by < 2.0f * 1.175494351e-38f)
+      in_double(static_cast<double>(r) + rest, max_norm);
+    else
+      by += (fmaf(-by, r, max_norm) - by * rest) * inv;
+  }
+  __device__ __forceinline__ Factor(double sum, float max_norm) {
+    const double r = sqrt(sum);
+    norm = static_cast<float>(r);
+    if (norm > max_norm && norm <= 3.402823466e38f) in_double(r, max_norm);
+  }
+
+ private:
+  __device__ __forceinline__ void in_double(double r, float max_norm) {
+    const double f = max_norm / r;
+    by = static_cast<float>(f);
+    far = by < 1.175494351e-38f && max_norm > 0.0f;
+    exact = f;
   }
 };
 
@@ -259,7 +300,7 @@ __device__ __forceinline__ void scale_chunk(const ClipTable<N>& tab, int c, cons
   const Piece p = piece_of(tab, c);
   const int tid = threadIdx.x & (kThreads - 1);
   auto scale = [&](auto src, auto dst) {
-    if (f.exact > 0.0)
+    if (f.far)
       scale_piece_in_double(src + p.at, dst + p.at, p.n, f.exact, tid);
     else
       scale_piece(src + p.at, dst + p.at, p.n, f.by, tid);
@@ -274,27 +315,33 @@ template <int N>
 __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ ClipTable<N> tab, Parts parts,
                                                               int P, float max_norm, int in_place,
                                                               float* __restrict__ norm) {
-  __shared__ float red[kThreads / 32];
+  __shared__ Pair red[kThreads / 32];
   __shared__ double red_exact[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
-  float s = 0.0f;
+  Pair s = {0.0f, 0.0f};
   bool odd = false;
-  for (int i = threadIdx.x; i < P; i += kThreads) {
-    const float v = parts.sum[i];
-    odd |= v != 0.0f && !in_range(v);
-    s += v;
+  for (int i0 = threadIdx.x; i0 < P; i0 += 5 * kThreads) {
+    Pair v[5];  // all on their way at once: up to 1280 sums in one round
+#pragma unroll
+    for (int j = 0; j < 5; ++j) v[j] = i0 + j * kThreads < P ? parts.sum[i0 + j * kThreads] : Pair{0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+      odd |= is_odd(v[j]);
+      s = s + v[j];
+    }
   }
-  float whole;
-  if (!__syncthreads_or(odd)) {
-    whole = sqrtf(block_sum(s, red));
-  } else {
-    double d = 0.0;
-    for (int i = threadIdx.x; i < P; i += kThreads) d += parts.exact[i];
-    whole = static_cast<float>(sqrt(block_sum(d, red_exact)));
+  const bool any_odd = __syncthreads_or(odd);
+  double d = 0.0;
+  if (any_odd) {
+    for (int i = threadIdx.x; i < P; i += kThreads) {
+      const Pair v = parts.sum[i];
+      d += is_odd(v) ? parts.exact[i] : static_cast<double>(v.hi) + v.lo;
+    }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
-  const Factor factor(whole, max_norm);
+  const Factor factor = any_odd ? Factor(block_sum<kThreads>(d, red_exact), max_norm)
+                                : Factor(block_sum<kThreads>(s, red), max_norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = factor.norm;
   if (in_place && factor.by == 1.0f) return;
   for (int c = tab.first[tab.n] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) scale_chunk(tab, c, factor);
 }
@@ -302,41 +349,46 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
 template <int N>
 __global__ void __launch_bounds__(kOneThreads) clip_one_kernel(const __grid_constant__ ClipTable<N> tab, float max_norm,
                                                                int in_place, float* __restrict__ norm) {
-  __shared__ float sum;
+  __shared__ Pair sum;
   __shared__ double exact;
   griddep_launch_dependents();
   griddep_wait();
   constexpr int kStep = kOneCtas * (kOneThreads / kThreads);
   const int first = (threadIdx.x / kThreads) * kOneCtas + blockIdx.x;
-  const Sum own = sum_chunks(tab, first, kStep);
+  const Sum own = sum_chunks<kOneThreads>(tab, first, kStep);
   if (threadIdx.x == 0) {
     sum = own.sum;
     exact = own.exact;
   }
   __syncwarp();
   cluster_sync_all();
-  float s = 0.0f;
+  auto sum_of = [&](int c) {
+    const uint32_t at = mapa_shared(smem_u32(&sum), c);
+    Pair v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.hi), "=f"(v.lo) : "r"(at));
+    return v;
+  };
+  Pair s = {0.0f, 0.0f};
   double d = 0.0;
   bool odd = false;
 #pragma unroll
   for (int c = 0; c < kOneCtas; ++c) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&sum), c)));
-    odd |= v != 0.0f && !in_range(v);
-    s += v;
+    const Pair v = sum_of(c);
+    odd |= is_odd(v);
+    s = s + v;
   }
   if (odd) {
     for (int c = 0; c < kOneCtas; ++c) {
-      double v;
-      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(smem_u32(&exact), c)));
-      d += v;
+      const Pair v = sum_of(c);
+      double e;
+      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(e) : "r"(mapa_shared(smem_u32(&exact), c)));
+      d += is_odd(v) ? e : static_cast<double>(v.hi) + v.lo;
     }
   }
   __syncwarp();
   cluster_sync_all();  // the other CTAs' sums have been read: none of them leaves before
-  const float whole = odd ? static_cast<float>(sqrt(d)) : sqrtf(s);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
-  const Factor factor(whole, max_norm);
+  const Factor factor = odd ? Factor(d, max_norm) : Factor(s, max_norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = factor.norm;
   if (in_place && factor.by == 1.0f) return;
   for (int c = first; c < tab.first[tab.n]; c += kStep) scale_chunk(tab, c, factor);
 }
@@ -398,7 +450,7 @@ constexpr int64_t kOneValues = 1 << 18;
 
 size_t clip_scratch_bytes(int n, int64_t total, int sms) {
   if (n <= kSmallTable && total <= kOneValues) return 0;
-  return static_cast<size_t>(clip_launches(n)) * clip_ctas(sms) * (sizeof(double) + sizeof(float));
+  return static_cast<size_t>(clip_launches(n)) * clip_ctas(sms) * (sizeof(double) + sizeof(Pair));
 }
 
 cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_place, void* scratch, float* norm, int sms,
@@ -422,7 +474,7 @@ cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_plac
   }
   Parts parts;
   parts.exact = static_cast<double*>(scratch);
-  parts.sum = reinterpret_cast<float*>(parts.exact + static_cast<size_t>(clip_launches(n)) * clip_ctas(sms));
+  parts.sum = reinterpret_cast<Pair*>(parts.exact + static_cast<size_t>(clip_launches(n)) * clip_ctas(sms));
   // some eight chunks a CTA, of 4096 values at least and 32768 at most
   const int most = clip_ctas(sms);
   long long chunk = (total / (8LL * most) + 4095) / 4096 * 4096;
