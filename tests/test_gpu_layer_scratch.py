@@ -27,7 +27,8 @@ def _scratch(nbytes):
 @pytest.mark.parametrize("N,G", [(65537, 1), (65537, 4096), (131072, 257), (131073, 1024), (524288, 1025), (524289, 3),
                                  (524289, 4096), (700001, 300)])
 def test_sort(N, G):
-    ids = torch.randint(-1, G + 1, (N,), device="cuda", dtype=I32, generator=torch.Generator(device="cuda").manual_seed(N))
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    ids = torch.randint(-1, G + 1, (N,), device="cuda", dtype=I32, generator=gen)
     nbytes = gmm.gmm_sort_rows_scratch_bytes(N, G)
     scratch, rows, sizes = _scratch(nbytes), Guarded((N,), I32), Guarded((G,), I32)
     assert gmm.gmm_sort_rows(ids, N, G, rows.t, sizes.t, scratch.t, nbytes) == 0

@@ -28,7 +28,7 @@ def test_the_blocks_gradient_without_its_norm_does_not_read_the_block(T, K, stre
     """Without w_post, out is linear in b: db = block_scale * gate * D whatever b holds.  (A
     gate's gradient does contain b.)"""
     gen = torch.Generator(device="cuda").manual_seed(T)
-    x, dout, b, dn = _rnd(gen, T, K, dt=stream), _rnd(gen, T, K, dt=stream), _rnd(gen, T, K, dt=BF), _rnd(gen, T, K, dt=BF)
+    x, dout, b, dn = (_rnd(gen, T, K, dt=t) for t in (stream, stream, BF, BF))
     g = {None: None, "column": _rnd(gen, K), "full": _rnd(gen, T, K, dt=BF)}[gate]
     how = dict(gate=g, w_next=_rnd(gen, K) if next_norm else None, residual_scale=0.8, block_scale=1.3)
     dn = dn if next_norm else None
@@ -40,9 +40,8 @@ def test_the_blocks_gradient_without_its_norm_does_not_read_the_block(T, K, stre
     assert torch.equal(got[1], want[1])
     if next_norm:
         assert torch.equal(got[4], want[4])
-    ref, mag = R.norm_join_bwd(dout.double(), None if dn is None else dn.double(), x.double(), b.double(), None,
-                               None if g is None else g.double(), how["w_next"].double() if next_norm else None, 0.8, 1.3,
-                               1e-6)
+    ref, mag = R.norm_join_bwd(*(None if v is None else v.double() for v in (dout, dn, x, b, None, g, how["w_next"])),
+                               0.8, 1.3, 1e-6)
     R.assert_within(got[1], ref[1], R.BF16 * ref[1].abs() + 2 * R.F32 * mag[1], "db")
 
 
@@ -67,7 +66,9 @@ def test_gradients_of_tiny_and_huge_rows_without_eps(T, K, stream, post, gate):
     w = dict(w_post=_rnd(gen, K) if post else None, w_next=_rnd(gen, K),
              gate={None: None, "column": _rnd(gen, K), "full": _rnd(gen, T, K, dt=BF)}[gate])
     # in part along the rows, so that their products' means do not vanish
-    along = b.sign() * (1.0 if w["w_post"] is None else w["w_post"].sign()) * (1.0 if w["gate"] is None else w["gate"].sign())
+    along = b.sign()
+    for v in (w["w_post"], w["gate"]):
+        along = along if v is None else along * v.sign()
     dout, dn = (_rnd(gen, T, K) + along).to(stream), (_rnd(gen, T, K) + out.sign() * w["w_next"].sign()).to(BF)
     got = gmm.norm_join_bwd(dout, dn, out, b, **w, residual_scale=0.8, block_scale=1.3, eps=0.0)
     ref, mag = R.norm_join_bwd(dout.double(), dn.double(), out.double(), b.double(),
