@@ -78,7 +78,8 @@ class MoELayer:
 
         def forward(x):
             _, n = gmm.norm_join(x, w_next=p["w_pre"], eps=EPS)
-            ids, weights = gmm.route(n.float() @ p["w_router"].t(), self.k, bias=self.bias, score=self.score, renorm=True)
+            logits = n.float() @ p["w_router"].t()
+            ids, weights = gmm.route(logits, self.k, bias=self.bias, score=self.score, renorm=True)
             rows, sizes = gmm.sort_rows(ids, self.E)
             xq, xs = gmm.gather_mx4_quantize(n, rows)
             _, hq, hs = gmm.mx4_fwd_swiglu_quant(xq, xs, wq, wqs, sizes, with_h=False, workspace=ws)

@@ -36,10 +36,11 @@ EXPORTED = ["gmm_status_string", "gmm_last_cuda_error", "gmm_workspace_bytes", "
             "gmm_bf16_dgrad", "gmm_fp8_fwd_swiglu_quant", "gmm_selftest_wait_timeout", "gmm_fp8_fwd_tiled",
             "gmm_fp8_fwd_swiglu_quant_tiled", "gmm_quantize_rhs_w4", "gmm_fp8_w4_fwd",
             "gmm_fp8_w4_fwd_swiglu_quant", "tgmm_bf16_tiled", "gmm_bf16_swiglu_fwd", "gmm_bf16_swiglu_bwd",
-            "tgmm_fp8_ckpt", "tgmm_fp8_ckpt_scratch_bytes", "gmm_mx4_quantize_lhs", "gmm_mx4_quantize_rhs", "gmm_mx4_fwd",
-            "gmm_mx4_fwd_swiglu_quant", "gmm_route", "gmm_route_bwd", "gmm_sort_rows_scratch_bytes", "gmm_sort_rows",
-            "gmm_gather_rows", "gmm_gather_quantize", "gmm_gather_mx4_quantize", "gmm_combine_rows", "gmm_combine_rows_bwd", "gmm_norm_join",
-            "gmm_norm_join_bwd_scratch_bytes", "gmm_norm_join_bwd", "gmm_clip_grads_scratch_bytes", "gmm_clip_grads"]
+            "tgmm_fp8_ckpt", "tgmm_fp8_ckpt_scratch_bytes", "gmm_mx4_quantize_lhs", "gmm_mx4_quantize_rhs",
+            "gmm_mx4_fwd", "gmm_mx4_fwd_swiglu_quant", "gmm_route", "gmm_route_bwd", "gmm_sort_rows_scratch_bytes",
+            "gmm_sort_rows", "gmm_gather_rows", "gmm_gather_quantize", "gmm_gather_mx4_quantize", "gmm_combine_rows",
+            "gmm_combine_rows_bwd", "gmm_norm_join", "gmm_norm_join_bwd_scratch_bytes", "gmm_norm_join_bwd",
+            "gmm_clip_grads_scratch_bytes", "gmm_clip_grads"]
 
 
 class TileConfig(ctypes.Structure):
@@ -1011,8 +1012,8 @@ def _want(what, t, on, dtype, shape):
 
 def _refuse(what, t, on, dtype, shape):
     where = "" if on < 0 else f" on cuda:{on}"
-    raise ValueError(f"{what}: expected a contiguous CUDA tensor of {'x'.join(map(str, shape))} {dtype} elements{where}, "
-                     f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    raise ValueError(f"{what}: expected a contiguous CUDA tensor of {'x'.join(map(str, shape))} {dtype} elements"
+                     f"{where}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _first(what, t, dtype):
@@ -1289,7 +1290,9 @@ def norm_join(x, b=None, w_post=None, gate=None, w_next=None, residual_scale=1.0
     handle = _handle(on, stream)
     if out is None:
         o = x if b is None else _like(x)
-        n = None if w_next is None else _like(b) if b is not None else _empty((T, K), (K, 1), dtype=_BF16, device=x.device)
+        n = None
+        if w_next is not None:
+            n = _like(b) if b is not None else _empty((T, K), (K, 1), dtype=_BF16, device=x.device)
     else:
         o, n = out
         if b is None:

@@ -251,7 +251,12 @@ __device__ void scale_piece(const T* src, T* dst, int n, float by, int tid) {
       }
     }
   }
-  for (int i = nv * W + tid; i < n; i += kThreads) if (copy) dst[i] = src[i]; else put(dst, i, value_of(src, i) * by);
+  for (int i = nv * W + tid; i < n; i += kThreads) {
+    if (copy)
+      dst[i] = src[i];
+    else
+      put(dst, i, value_of(src, i) * by);
+  }
 }
 
 // The same where the factor is below fp32's normal numbers: it loses bits there, or all
@@ -424,7 +429,7 @@ cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_pl
     fill<N>(tab, t + i, n - i < N ? n - i : N, chunk);
     const int grid = grid_of(tab.first, tab.n, most);
     const cudaError_t e = launch_short(over, clip_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
-                                     Parts{parts.exact + P, parts.sum + P});
+                                       Parts{parts.exact + P, parts.sum + P});
     if (e != cudaSuccess) return e;
     P += grid;
   }
@@ -432,7 +437,7 @@ cudaError_t run(const ClipTensor* t, int n, int chunk, float max_norm, int in_pl
     if (n > N) fill<N>(tab, t + i, n - i < N ? n - i : N, chunk);
     const int grid = norm_only ? 1 : grid_of(tab.first, tab.n, most);
     const cudaError_t e = launch_short(over, clip_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, s, tab,
-                                     parts, P, max_norm, in_place || norm_only, norm);
+                                       parts, P, max_norm, in_place || norm_only, norm);
     if (e != cudaSuccess || norm_only) return e;
   }
   return cudaSuccess;
@@ -482,8 +487,10 @@ cudaError_t launch_clip(const ClipTensor* t, int n, float max_norm, bool in_plac
   const bool over = launch_over(6 * total, stream);  // two reads and a write
   const bool norm_only = max_norm > 3.402823466e38f && in_place;
   if (n <= kSmallTable)
-    return run<kSmallTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, over, stream);
-  return run<kLargeTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, over, stream);
+    return run<kSmallTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, over,
+                            stream);
+  return run<kLargeTable>(t, n, static_cast<int>(chunk), max_norm, in_place, parts, most, norm, norm_only, over,
+                          stream);
 }
 
 }  // namespace gmm

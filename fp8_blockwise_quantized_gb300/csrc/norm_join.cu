@@ -134,7 +134,8 @@ struct Sums {
 };
 // Zeros for a kernel's buffers.
 __device__ __forceinline__ void clear(SumBuffer& red) {
-  for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / sizeof(float)); i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / sizeof(float)); i += blockDim.x)
+    (&red[0][0][0])[i] = 0.0f;
   __syncthreads();
 }
 
@@ -170,13 +171,19 @@ __device__ __forceinline__ void put8(float* p, const Cols& c) {
 // factor * p * q of 8 columns (a null pointer counts as 1).
 __device__ __forceinline__ Cols factors8(const float* p, const float* q, float factor, int col) {
   Cols c = Cols::of(factor);
-  if (p) c = c * cols_of(__ldg(reinterpret_cast<const float4*>(p + col)), __ldg(reinterpret_cast<const float4*>(p + col) + 1));
-  if (q) c = c * cols_of(__ldg(reinterpret_cast<const float4*>(q + col)), __ldg(reinterpret_cast<const float4*>(q + col) + 1));
+  auto at = [&](const float* f) {
+    const float4* v = reinterpret_cast<const float4*>(f + col);
+    return cols_of(__ldg(v), __ldg(v + 1));
+  };
+  if (p) c = c * at(p);
+  if (q) c = c * at(q);
   return c;
 }
 
 // rsqrt is within 2 units of the last place.
-__device__ __forceinline__ float inv_rms(float squares, float inv_k, float eps) { return rsqrtf(fmaf(squares, inv_k, eps)); }
+__device__ __forceinline__ float inv_rms(float squares, float inv_k, float eps) {
+  return rsqrtf(fmaf(squares, inv_k, eps));
+}
 
 // V vectors of 8 columns a thread, at most NT threads a CTA.  A thread without columns
 // reads those of others and adds nothing; the row ahead of the last is the last again.
@@ -505,9 +512,9 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_join_bwd_kernel(NormJoinBwd
 
 // Sums the parts in their order and gives the parameters' gradients: 8 columns a CTA,
 // 32 threads a column with every 32nd part each, a warp a column for what they have.
-__global__ void __launch_bounds__(256) norm_join_reduce_kernel(const float* __restrict__ parts, int P, int K, float beta,
-                                                               const float* w_post, const float* gate, float* dw_post,
-                                                               float* dgate, float* dw_next) {
+__global__ void __launch_bounds__(256) norm_join_reduce_kernel(const float* __restrict__ parts, int P, int K,
+                                                               float beta, const float* w_post, const float* gate,
+                                                               float* dw_post, float* dgate, float* dw_next) {
   __shared__ float sums[32][9];
   griddep_launch_dependents();
   griddep_wait();
@@ -629,8 +636,8 @@ cudaError_t launch_norm_join_bwd(const NormJoinBwdArgs& args, int sms, cudaStrea
   }
   if (e != cudaSuccess || one_cluster(a.T, a.K) || !(a.dw_post || a.dgate_col || a.dw_next)) return e;
   return launch_short(over, norm_join_reduce_kernel, dim3(static_cast<unsigned>(a.K / 8), 2), dim3(256), 0, stream,
-                    static_cast<const float*>(a.parts), sh.grid, static_cast<int>(a.K), a.beta, a.w_post,
-                    a.gate_col, a.dw_post, a.dgate_col, a.dw_next);
+                      static_cast<const float*>(a.parts), sh.grid, static_cast<int>(a.K), a.beta, a.w_post,
+                      a.gate_col, a.dw_post, a.dgate_col, a.dw_next);
 }
 
 }  // namespace gmm

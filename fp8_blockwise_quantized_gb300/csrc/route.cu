@@ -242,10 +242,10 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
   return by_words(a.E, [&](auto v) {
     constexpr int V = decltype(v)::value;
     if (a.f32)
-      return launch_short(over, route_kernel<float, V>, grid, block, 0, stream, static_cast<const float*>(a.logits), a.bias, a.T,
-                        a.E, a.k, a.softmax, a.renorm, a.scale, a.ids_out, a.weights);
-    return launch_short(over, route_kernel<uint16_t, V>, grid, block, 0, stream, static_cast<const uint16_t*>(a.logits), a.bias,
-                      a.T, a.E, a.k, a.softmax, a.renorm, a.scale, a.ids_out, a.weights);
+      return launch_short(over, route_kernel<float, V>, grid, block, 0, stream, static_cast<const float*>(a.logits),
+                          a.bias, a.T, a.E, a.k, a.softmax, a.renorm, a.scale, a.ids_out, a.weights);
+    return launch_short(over, route_kernel<uint16_t, V>, grid, block, 0, stream, static_cast<const uint16_t*>(a.logits),
+                        a.bias, a.T, a.E, a.k, a.softmax, a.renorm, a.scale, a.ids_out, a.weights);
   });
 }
 
@@ -257,11 +257,11 @@ cudaError_t launch_route_bwd(const RouteArgs& a, cudaStream_t stream) {
     constexpr int V = decltype(v)::value;
     if (a.f32)
       return launch_short(over, route_bwd_kernel<float, V>, grid, block, 0, stream, a.dweights,
-                        static_cast<const float*>(a.logits), a.ids, a.T, a.E, a.k, a.softmax, a.renorm, a.scale,
-                        static_cast<float*>(a.dlogits));
+                          static_cast<const float*>(a.logits), a.ids, a.T, a.E, a.k, a.softmax, a.renorm, a.scale,
+                          static_cast<float*>(a.dlogits));
     return launch_short(over, route_bwd_kernel<uint16_t, V>, grid, block, 0, stream, a.dweights,
-                      static_cast<const uint16_t*>(a.logits), a.ids, a.T, a.E, a.k, a.softmax, a.renorm, a.scale,
-                      static_cast<uint16_t*>(a.dlogits));
+                        static_cast<const uint16_t*>(a.logits), a.ids, a.T, a.E, a.k, a.softmax, a.renorm, a.scale,
+                        static_cast<uint16_t*>(a.dlogits));
   });
 }
 

@@ -28,7 +28,9 @@ constexpr int kMaskBins = 1025;  // so many bins, and their words are at most 10
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDirectChunks = 64;  // so many rows of the table each CTA sums itself
 
-__device__ __forceinline__ int bin_of(int id, int G) { return static_cast<unsigned>(id) < static_cast<unsigned>(G) ? id : G; }
+__device__ __forceinline__ int bin_of(int id, int G) {
+  return static_cast<unsigned>(id) < static_cast<unsigned>(G) ? id : G;
+}
 
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int32_t* __restrict__ ids, int N, int G,
                                                                   int chunk, int32_t* __restrict__ table) {
@@ -65,7 +67,8 @@ __global__ void __launch_bounds__(64) sort_scan_kernel(int32_t* __restrict__ tab
 // rounds: of a warp, at most R; a CTA's chunk is kSortThreads * rounds ids.
 template <int R, bool CLUSTER, bool MASKS>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t* __restrict__ ids, int N, int G,
-                                                                  int rounds, int chunks, const int32_t* __restrict__ table,
+                                                                  int rounds, int chunks,
+                                                                  const int32_t* __restrict__ table,
                                                                   int32_t* __restrict__ rows,
                                                                   int32_t* __restrict__ sizes) {
   extern __shared__ int smem[];
@@ -485,7 +488,8 @@ cudaError_t launch_sort_rows(const int32_t* ids, int64_t N, int G, int32_t* rows
   }
   const bool cluster = N > kOneCta && N <= kOneCluster;
   const int ctas = cluster ? kSortCluster : chunks;
-  const int rounds = chunks > 1 ? sort_rounds(N) : static_cast<int>((N + ctas * kSortThreads - 1) / (ctas * kSortThreads));
+  const int rounds =
+      chunks > 1 ? sort_rounds(N) : static_cast<int>((N + ctas * kSortThreads - 1) / (ctas * kSortThreads));
   static std::atomic<uint64_t> done[2][5];
   auto place = [&](auto masks, auto kernel, int i) {
     constexpr bool kMasks = decltype(masks)::value;
@@ -519,9 +523,11 @@ cudaError_t launch_sort_rows(const int32_t* ids, int64_t N, int G, int32_t* rows
   auto sized = [&](auto masks) {
     constexpr bool M = decltype(masks)::value;
     if (cluster)
-      return rounds <= 4 ? place(masks, sort_place_kernel<4, true, M>, 0) : place(masks, sort_place_kernel<16, true, M>, 1);
+      return rounds <= 4 ? place(masks, sort_place_kernel<4, true, M>, 0)
+                         : place(masks, sort_place_kernel<16, true, M>, 1);
     if (rounds <= 1) return place(masks, sort_place_kernel<1, false, M>, 2);
-    return rounds <= 4 ? place(masks, sort_place_kernel<4, false, M>, 3) : place(masks, sort_place_kernel<16, false, M>, 4);
+    return rounds <= 4 ? place(masks, sort_place_kernel<4, false, M>, 3)
+                       : place(masks, sort_place_kernel<16, false, M>, 4);
   };
   return B <= kMaskBins ? sized(std::true_type()) : sized(std::false_type());
 }
@@ -533,11 +539,11 @@ cudaError_t launch_gather_rows(const void* x, const int32_t* rows, int64_t T, in
   const bool over = launch_over(2 * M * K, stream);
   if (vectors < kNarrow)
     return launch_short(over, gather_kernel<uint32_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
-                      static_cast<const uint4*>(x), rows, static_cast<uint32_t>(vectors), k, KV, M,
-                      static_cast<uint4*>(out));
+                        static_cast<const uint4*>(x), rows, static_cast<uint32_t>(vectors), k, KV, M,
+                        static_cast<uint4*>(out));
   return launch_short(over, gather_kernel<uint64_t>, dim3(blocks_of(vectors)), dim3(256), 0, stream,
-                    static_cast<const uint4*>(x), rows, static_cast<uint64_t>(vectors), k, KV, M,
-                    static_cast<uint4*>(out));
+                      static_cast<const uint4*>(x), rows, static_cast<uint64_t>(vectors), k, KV, M,
+                      static_cast<uint4*>(out));
 }
 
 cudaError_t launch_gather_quantize(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, float* xs,
@@ -547,11 +553,11 @@ cudaError_t launch_gather_quantize(const void* x, const int32_t* rows, int64_t T
   const bool over = launch_over(M * K, stream);
   if (units < kNarrow / 8)
     return launch_short(over, gather_quantize_kernel<uint32_t>, dim3(blocks_of(units * 8)), dim3(256), 0, stream,
-                      static_cast<const uint4*>(x), rows, static_cast<uint32_t>(units), k, KB, M,
-                      static_cast<uint4*>(xq), xs);
+                        static_cast<const uint4*>(x), rows, static_cast<uint32_t>(units), k, KB, M,
+                        static_cast<uint4*>(xq), xs);
   return launch_short(over, gather_quantize_kernel<uint64_t>, dim3(blocks_of(units * 8)), dim3(256), 0, stream,
-                    static_cast<const uint4*>(x), rows, static_cast<uint64_t>(units), k, KB, M,
-                    static_cast<uint4*>(xq), xs);
+                      static_cast<const uint4*>(x), rows, static_cast<uint64_t>(units), k, KB, M,
+                      static_cast<uint4*>(xq), xs);
 }
 
 cudaError_t launch_gather_mx4(const void* x, const int32_t* rows, int64_t T, int k, int64_t K, void* xq, void* xs,
@@ -576,10 +582,11 @@ cudaError_t launch_combine_rows(const void* y, const int32_t* rows, const float*
   const long long units = T * static_cast<long long>(part), M = T * k;
   const bool over = launch_over(2 * M * K, stream);
   auto launch = [&](auto kernel, auto narrow) {
-    return launch_short(over, kernel, dim3(blocks_of(units)), dim3(256), 0, stream, static_cast<const uint4*>(y), rows, weights,
-                      static_cast<decltype(narrow)>(units), k, KV, part, M, static_cast<uint4*>(out));
+    return launch_short(over, kernel, dim3(blocks_of(units)), dim3(256), 0, stream, static_cast<const uint4*>(y), rows,
+                        weights, static_cast<decltype(narrow)>(units), k, KV, part, M, static_cast<uint4*>(out));
   };
-  if (units < kNarrow) return V == 2 ? launch(combine_kernel<uint32_t, 2>, uint32_t()) : launch(combine_kernel<uint32_t, 1>, uint32_t());
+  if (units < kNarrow)
+    return V == 2 ? launch(combine_kernel<uint32_t, 2>, uint32_t()) : launch(combine_kernel<uint32_t, 1>, uint32_t());
   return V == 2 ? launch(combine_kernel<uint64_t, 2>, uint64_t()) : launch(combine_kernel<uint64_t, 1>, uint64_t());
 }
 
@@ -591,9 +598,10 @@ cudaError_t launch_combine_rows_bwd(const void* dout, const void* y, const int32
   while (span < kBwdWarps && T * span < 16LL * sms && span * 256 < K) span *= 2;
   const long long per = kBwdWarps / span;
   const bool over = launch_over(4 * T * k * K, stream);
-  return launch_short(over, combine_bwd_kernel, dim3(static_cast<unsigned>((T + per - 1) / per)), dim3(32 * kBwdWarps), 0,
-                    stream, static_cast<const uint4*>(dout), static_cast<const uint4*>(y), rows, weights,
-                    static_cast<long long>(T), k, static_cast<unsigned>(K / 8), span, static_cast<uint4*>(dy), dweights);
+  return launch_short(over, combine_bwd_kernel, dim3(static_cast<unsigned>((T + per - 1) / per)), dim3(32 * kBwdWarps),
+                      0, stream, static_cast<const uint4*>(dout), static_cast<const uint4*>(y), rows, weights,
+                      static_cast<long long>(T), k, static_cast<unsigned>(K / 8), span, static_cast<uint4*>(dy),
+                      dweights);
 }
 
 }  // namespace gmm
