@@ -34,7 +34,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // more than it costs.  It hides 2 to 4 us between two kernels of one stream, and its
 // launch takes 1.5 to 2 us more of the host's time, which is what bounds a call of a
 // few microseconds (router of 16 tokens through the Python entry point: 11.5 us with
-// it, 10.0 without).
+// it, 10.7 without).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_short(bool over, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                          Args&&... args) {

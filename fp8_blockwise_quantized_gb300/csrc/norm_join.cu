@@ -275,14 +275,14 @@ __device__ __forceinline__ void put_columns(const NormJoinBwdArgs& a, int c, flo
 // With c = dn * w_next, D = dout + ro (c - out ro^2 / K sum(c out)); dx = alpha D.
 // With p = beta * w_post * gate, b's gradient is that of its norm from t = D p:
 // db = rb (t - b rb^2 / K sum(t b)).  (A cube of ro or rb leaves fp32's range where the
-// gradient does not: rows below 1e-13 with eps = 0.)  With s = sum over the rows of D b rb (times a
-// gate per element), dw_post = beta gate s and a column gate's gradient beta w_post s:
-// one sum for both, a part of it a CTA (and of dw_next's), joined by
+// gradient does not: rows below 1e-13 with eps = 0.)  With s = sum over the rows of
+// D b rb (times a gate per element), dw_post = beta gate s and a column gate's gradient
+// beta w_post s: one sum for both, a part of it a CTA (and of dw_next's), joined by
 // norm_join_reduce_kernel.
 //
 // V = 2 (over 4096 columns): the registers hold the sums and the factors, but not the
 // row ahead, which goes through shared memory, and its values are read there again when
-// they are needed again.  2048 x 8192: 41.8 us with a bf16 stream (floor 30.2), 55.9
+// they are needed again.  2048 x 8192: 41.8 us with a bf16 stream (floor 30.2), 56.3
 // with fp32 (45.2); with the row read when its turn came, asked for in the L2 before,
 // and factors from the cache, 55.0 and 79.4.  What is left is a row's two sums, one after
 // the other, with no other row in the SM.

@@ -3,7 +3,8 @@
 //
 // A warp takes a token and holds its E logits in registers, expert i * 32 + lane
 // in lane's word i, so that every load and store of a word is contiguous.  Bound by
-// its instructions, and for few tokens by the chain of the choice.  Forward, 8192
+// its instructions (60 % of the issue slots, backward 66 %) and the wait for a token's
+// logits together, and for few tokens by the chain of the choice.  Forward, 8192
 // tokens, 256 experts, 8 choices: 7.6 us (k rounds of a warp-wide maximum, each lane
 // looking through its words: 11.6; each keeping its two best: 9.7); backward 6.7.
 //

@@ -574,8 +574,10 @@ gmm_status gmm_norm_join_bwd(const void* dout, const void* dn, const void* out, 
  * Gradients scaled to a largest global norm:
  *   norm = sqrt( sum over all tensors and elements of g^2 ),
  *   out  = g * (max_norm / norm) where norm > max_norm, else g.
- * A norm that is not finite scales nothing (the caller sees it in `norm`).  The
- * squares are summed so that no finite gradients overflow or vanish in them.
+ * A norm that is not finite, or past fp32's range and so +infinity, scales nothing (the
+ * caller sees it in `norm`).  The squares are summed so that no finite gradients
+ * overflow or vanish in them; the norm and the factor are rounded once, and a factor
+ * below fp32's normal numbers keeps its bits.
  * max_norm = +infinity with out = NULL computes the norm only.
  *   grads, out  HOST arrays of n device pointers, aligned to their elements (not to
  *            16 bytes; those that are not go a slower way); out NULL: in place.  A
